@@ -11,6 +11,13 @@ kernel for sm_103a behind a C ABI (``include/bsa.h``, ``libbsa.so``):
 * ``nsa_select_forward_fsa`` -- the same result in the page's block-outer
   split-K form: each selected block's K/V read once, per-pair softmax
   partials, a log-sum-exp combine.
+* ``nsa_select_backward`` and ``nsa_select_attention`` -- the gradients of
+  ``nsa_select_forward``, and the forward as a ``torch.autograd.Function``
+  whose backward runs them.
+* ``nsa_cache_append`` and ``nsa_select_decode`` -- the selection attention in
+  serving: new tokens' keys (rotated by position) and values into a paged
+  cache of e4m3 codes with a scale for each page and head, and one query token
+  per sequence over that cache, its selected blocks or all of them.
 * ``tra_forward_host`` -- ``tra_forward`` on host tensors, streamed through
   the GPU in chunks of heads with overlapped copies.
 * ``tra_backward`` and ``tra_attention`` -- the gradients of ``tra_forward``,
@@ -28,6 +35,15 @@ from .bsa import (  # noqa: F401
     device_error,
     library_path,
     load_library,
+    nsa_cache_append,
+    nsa_cache_append_raw,
+    nsa_select_attention,
+    nsa_select_backward,
+    nsa_select_backward_raw,
+    nsa_select_backward_workspace_size,
+    nsa_select_decode,
+    nsa_select_decode_raw,
+    nsa_select_decode_workspace_size,
     nsa_select_forward,
     nsa_select_forward_fsa,
     nsa_select_forward_fsa_raw,
@@ -74,5 +90,14 @@ __all__ = [
     "nsa_select_forward_fsa",
     "nsa_select_forward_fsa_raw",
     "nsa_select_fsa_workspace_size",
+    "nsa_select_attention",
+    "nsa_select_backward",
+    "nsa_select_backward_raw",
+    "nsa_select_backward_workspace_size",
+    "nsa_cache_append",
+    "nsa_cache_append_raw",
+    "nsa_select_decode",
+    "nsa_select_decode_raw",
+    "nsa_select_decode_workspace_size",
     "status_string",
 ]

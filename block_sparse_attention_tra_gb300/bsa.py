@@ -100,6 +100,17 @@ def open_library(path):
     lib.nsa_select_forward_fsa.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp,
                                            ctypes.c_size_t, vp]
     lib.nsa_select_forward_fsa.restype = i32
+    sz = ctypes.c_size_t
+    lib.nsa_select_backward_workspace_size.argtypes = [i32] * 7
+    lib.nsa_select_backward_workspace_size.restype = sz
+    lib.nsa_select_backward.argtypes = [vp] * 10 + [i32] * 7 + [vp, sz, vp]
+    lib.nsa_select_backward.restype = i32
+    lib.nsa_cache_append.argtypes = [vp] * 12 + [i32] * 11 + [vp]
+    lib.nsa_cache_append.restype = i32
+    lib.nsa_select_decode_workspace_size.argtypes = [i32] * 7
+    lib.nsa_select_decode_workspace_size.restype = sz
+    lib.nsa_select_decode.argtypes = [vp] * 10 + [i32] * 8 + [vp, sz, vp]
+    lib.nsa_select_decode.restype = i32
     lib.bsa_status_string.argtypes = [i32]
     lib.bsa_status_string.restype = ctypes.c_char_p
     lib.bsa_version.argtypes = []
@@ -207,6 +218,74 @@ def nsa_select_forward_fsa_raw(q, k, v, block_idx, out, lse, B, Hq, Hkv, T, D, b
     """Direct C call with integer device pointers; returns the bsa_status."""
     return load_library().nsa_select_forward_fsa(q, k, v, block_idx, out, lse, B, Hq, Hkv, T, D, block_size, S,
                                                  workspace, int(workspace_bytes), stream)
+
+
+def nsa_select_backward_workspace_size(B, Hq, Hkv, T, D, block_size, S) -> int:
+    """Bytes of workspace ``nsa_select_backward`` needs (0 = sizes not accepted)."""
+    return int(load_library().nsa_select_backward_workspace_size(B, Hq, Hkv, T, D, block_size, S))
+
+
+def nsa_select_backward_raw(q, k, v, block_idx, out, lse, dout, dq, dk, dv, B, Hq, Hkv, T, D, block_size, S,
+                            workspace, workspace_bytes, stream=0) -> int:
+    """Direct C call with integer device pointers; returns the bsa_status."""
+    return load_library().nsa_select_backward(q, k, v, block_idx, out, lse, dout, dq, dk, dv, B, Hq, Hkv, T, D,
+                                              block_size, S, workspace, int(workspace_bytes), stream)
+
+
+def nsa_cache_append_raw(k, v, q, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens,
+                         inv_freq, B, Hq, Hkv, n, D, page_size, max_pages, num_pages, rotary_dim, interleaved, dtype,
+                         stream=0) -> int:
+    """Direct C call with integer device pointers (q, q_out, new_lens and
+    inv_freq may be None); returns the bsa_status."""
+    return load_library().nsa_cache_append(k, v, q, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens,
+                                           new_lens, inv_freq, B, Hq, Hkv, n, D, page_size, max_pages, num_pages,
+                                           rotary_dim, int(bool(interleaved)), int(dtype), stream)
+
+
+def nsa_select_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S) -> int:
+    """Bytes of workspace ``nsa_select_decode`` needs (0 = sizes not accepted)."""
+    return int(load_library().nsa_select_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S))
+
+
+def nsa_select_decode_raw(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx, out, lse, B, Hq,
+                          Hkv, D, page_size, max_pages, num_pages, S, workspace, workspace_bytes, stream=0) -> int:
+    """Direct C call with integer device pointers (block_idx and lse may be
+    None); returns the bsa_status."""
+    return load_library().nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx,
+                                            out, lse, B, Hq, Hkv, D, page_size, max_pages, num_pages, S, workspace,
+                                            int(workspace_bytes), stream)
+
+
+@contextlib.contextmanager
+def _on_stream(torch, device, stream):
+    """Within the block ``device`` is current and allocations, copies and the
+    library call all go to ``stream`` (default: the device's current stream),
+    whose handle is yielded."""
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream is not None and stream.device != device:
+        raise BsaError(f"the stream is on {stream.device}, the tensors are on {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield torch.cuda.current_stream(device).cuda_stream
+
+
+def _one_device(what, first, *others):
+    """``first`` on a CUDA device and every other tensor (None: absent) on the same one."""
+    if first.device.type != "cuda":
+        raise BsaError(f"{what} takes CUDA tensors (no CPU path)")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise BsaError(f"{what}: tensors on {first.device} and {t.device}")
+
+
+def _in_place(what, name, t, shape, *dtypes):
+    """Tensors the library writes into (or reads in place) keep their memory: exact shape, type and layout."""
+    if tuple(t.shape) != tuple(shape):
+        raise BsaError(f"{what}: {name} must be {list(shape)}, got {list(t.shape)}", 2)
+    if t.dtype not in dtypes:
+        raise BsaError(f"{what}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}", 3)
+    if not t.is_contiguous():
+        raise BsaError(f"{what}: {name} must be contiguous", 2)
 
 
 def _stream_handle(stream):
@@ -515,6 +594,211 @@ def nsa_select_forward_fsa(q, k, v, block_idx, block_size: int = 64, out=None, l
                                     lse.data_ptr() if lse is not None else None, B, Hq, Hkv, T, D, block_size, S,
                                     workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
     _check(st, "nsa_select_forward_fsa")
+    return (out, lse) if return_lse else out
+
+
+def nsa_select_backward(q, k, v, block_idx, out, lse, dout, block_size: int = 64, workspace=None, stream=None):
+    """Gradients ``(dq, dk, dv)`` of ``nsa_select_forward`` for the upstream
+    gradient ``dout`` of its ``out``.
+
+    q, out, dout ``[B, Hq, T, D]`` and k, v ``[B, Hkv, T, D]`` bf16,
+    ``block_idx [B, Hkv, T, S]``, ``lse [B, Hq, T]`` fp32; ``out`` and ``lse``
+    as the forward returned them.  The probabilities are recomputed from
+    ``lse``; results repeat bit for bit.  ``workspace`` is a uint8 CUDA tensor
+    of at least ``nsa_select_backward_workspace_size(...)`` bytes (allocated
+    when None).  Runs on ``stream`` (default: torch's current stream) without
+    synchronising.
+    """
+    import torch
+
+    _one_device("nsa_select_backward", q, k, v, block_idx, out, lse, dout, workspace)
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or block_idx.dim() != 4:
+        raise BsaError("q [B,Hq,T,D], k/v [B,Hkv,T,D], block_idx [B,Hkv,T,S] expected", 2)
+    B, Hq, T, D = q.shape
+    Hkv, S = k.shape[1], block_idx.shape[-1]
+    if (q.shape != out.shape or q.shape != dout.shape or tuple(lse.shape) != (B, Hq, T)
+            or tuple(k.shape) != (B, Hkv, T, D) or tuple(block_idx.shape) != (B, Hkv, T, S)):
+        raise BsaError("q, out, dout [B,Hq,T,D], lse [B,Hq,T], k/v [B,Hkv,T,D], block_idx [B,Hkv,T,S] expected", 2)
+    if any(t.dtype != torch.bfloat16 for t in (q, k, v, out, dout)) or lse.dtype != torch.float32:
+        raise BsaError("nsa_select_backward takes bfloat16 q, k, v, out, dout and float32 lse", 3)
+    with _on_stream(torch, q.device, stream) as handle:
+        q, k, v, out, lse, dout = (t.contiguous() for t in (q, k, v, out, lse, dout))
+        idx = block_idx.to(torch.int32).contiguous()
+        need = nsa_select_backward_workspace_size(B, Hq, Hkv, T, D, block_size, S)
+        if workspace is None:
+            workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        st = nsa_select_backward_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(), out.data_ptr(),
+                                     lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B,
+                                     Hq, Hkv, T, D, block_size, S, workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), handle)
+    _check(st, "nsa_select_backward")
+    return dq, dk, dv
+
+
+_NSA_FUNCTION = None
+
+
+def _nsa_function():
+    """The autograd function of the selection attention: forward through
+    ``nsa_select_forward``, backward through ``nsa_select_backward``."""
+    global _NSA_FUNCTION
+    if _NSA_FUNCTION is None:
+        import torch
+        from torch.autograd.function import once_differentiable
+
+        class NsaFunction(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, v, block_idx, block_size):
+                out, lse = nsa_select_forward(q, k, v, block_idx, block_size, return_lse=True)
+                ctx.save_for_backward(q, k, v, block_idx, out, lse)
+                ctx.block_size = int(block_size)
+                return out
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dout):
+                q, k, v, block_idx, out, lse = ctx.saved_tensors
+                dq, dk, dv = nsa_select_backward(q, k, v, block_idx, out, lse, dout.to(q.dtype), ctx.block_size)
+                return dq, dk, dv, None, None
+
+        _NSA_FUNCTION = NsaFunction
+    return _NSA_FUNCTION
+
+
+def nsa_select_attention(q, k, v, block_idx, block_size: int = 64):
+    """NSA selection-branch attention with autograd: ``nsa_select_forward``
+    whose gradients with respect to q, k and v come from
+    ``nsa_select_backward`` (arguments as for ``nsa_select_forward``)."""
+    return _nsa_function().apply(q, k, v, block_idx, block_size)
+
+
+def _check_cache(torch, what, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, B, Hkv, D):
+    """Shapes and types of the paged cache; returns (num_pages, page_size, max_pages)."""
+    if k_cache.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != B or tuple(cache_lens.shape) != (B,):
+        raise BsaError(f"{what}: k_cache [pages,Hkv,page_size,D], page_table [B,max_pages], cache_lens [B] expected", 2)
+    pages, page_size = k_cache.shape[0], k_cache.shape[2]
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    _in_place(what, "k_cache", k_cache, (pages, Hkv, page_size, D), *codes)
+    _in_place(what, "v_cache", v_cache, (pages, Hkv, page_size, D), *codes)
+    _in_place(what, "k_scale", k_scale, (pages, Hkv), torch.float32)
+    _in_place(what, "v_scale", v_scale, (pages, Hkv), torch.float32)
+    return pages, page_size, page_table.shape[1]
+
+
+def nsa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens=None, inv_freq=None,
+                     interleaved: bool = False, q=None, q_out=None, stream=None):
+    """Writes the keys and values of new tokens into a paged e4m3 cache, in
+    place, keys rotated by position on the way.
+
+    k, v ``[B, Hkv, n, D]`` bf16 or fp32; ``k_cache``/``v_cache [pages, Hkv,
+    page_size, D]`` float8_e4m3fn (or uint8 codes), ``k_scale``/``v_scale
+    [pages, Hkv]`` fp32, ``page_table [B, max_pages]``; ``cache_lens [B]``
+    counts the tokens held before (it is not advanced here), ``new_lens [B]``
+    the new ones of each sequence (default n).  ``inv_freq [rotary_dim / 2]``
+    gives the rotation's angle per position of each pair, halves apart or
+    neighbours if ``interleaved`` (None: no rotation).  With ``q [B, Hq, n,
+    D]`` the rotated queries are returned, in ``q_out`` if given (q itself is
+    allowed; rows past ``new_lens`` are left as they were, or zero in a new
+    tensor).  Runs on ``stream`` (default: torch's current stream) without
+    synchronising.
+    """
+    import torch
+
+    what = "nsa_cache_append"
+    _one_device(what, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens, inv_freq, q, q_out)
+    if k.dim() != 4 or k.shape != v.shape or (q is not None and q.dim() != 4):
+        raise BsaError("k, v [B,Hkv,n,D] and q [B,Hq,n,D] expected", 2)
+    B, Hkv, n, D = k.shape
+    Hq = Hkv if q is None else q.shape[1]
+    pages, page_size, max_pages = _check_cache(torch, what, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens,
+                                               B, Hkv, D)
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise BsaError("k, v, q must share one dtype", 3)
+    if q is not None and tuple(q.shape) != (B, Hq, n, D):
+        raise BsaError("q must be [B,Hq,n,D] with k's B, n and D", 2)
+    if q is None and q_out is not None:
+        raise BsaError("q_out given without q")
+    if q_out is not None:
+        _in_place(what, "q_out", q_out, q.shape, q.dtype)
+    if new_lens is not None and tuple(new_lens.shape) != (B,):
+        raise BsaError("new_lens must be [B]", 2)
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise BsaError("inv_freq must be [rotary_dim / 2]", 2)
+    rotary = 0 if inv_freq is None else 2 * inv_freq.numel()
+    with _on_stream(torch, k.device, stream) as handle:
+        k, v = k.contiguous(), v.contiguous()
+        table, lens = page_table.to(torch.int32).contiguous(), cache_lens.to(torch.int32).contiguous()
+        news = None if new_lens is None else new_lens.to(torch.int32).contiguous()
+        freq = None if inv_freq is None else inv_freq.to(torch.float32).contiguous()
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if news is None else torch.zeros(
+                    q.shape, dtype=q.dtype, device=q.device)
+            q = q.contiguous()
+        st = nsa_cache_append_raw(k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
+                                  None if q is None else q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                  k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                                  None if news is None else news.data_ptr(), None if freq is None else freq.data_ptr(),
+                                  B, Hq, Hkv, n, D, page_size, max_pages, pages, rotary, interleaved, _dtype_code(k),
+                                  handle)
+    _check(st, what)
+    return q_out
+
+
+def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx=None, out=None,
+                      lse=None, return_lse: bool = False, workspace=None, stream=None):
+    """``nsa_select_forward`` for the last token of each sequence, over the
+    paged e4m3 cache that ``nsa_cache_append`` fills.
+
+    q ``[B, Hq, 1, D]`` bf16 (rotated), the cache as for ``nsa_cache_append``,
+    ``cache_lens [B]`` with the query's own token counted; ``block_idx [B,
+    Hkv, 1, S]`` lists logical pages (a set, -1 = padding), None reads every
+    page.  Returns ``out [B, Hq, 1, D]`` (and ``lse [B, Hq, 1]`` fp32 when
+    ``return_lse``); an empty sequence or selection gives 0 and -1e9.
+    ``workspace`` is a uint8 CUDA tensor of at least
+    ``nsa_select_decode_workspace_size(...)`` bytes (allocated when None).
+    Runs on ``stream`` (default: torch's current stream) without
+    synchronising.
+    """
+    import torch
+
+    what = "nsa_select_decode"
+    _one_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx, out, lse, workspace)
+    if q.dim() != 4 or q.shape[2] != 1 or k_cache.dim() != 4:
+        raise BsaError("q [B,Hq,1,D] and k_cache [pages,Hkv,page_size,D] expected", 2)
+    if q.dtype != torch.bfloat16:
+        raise BsaError("nsa_select_decode takes bfloat16 q", 3)
+    B, Hq, _, D = q.shape
+    Hkv = k_cache.shape[1]
+    pages, page_size, max_pages = _check_cache(torch, what, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens,
+                                               B, Hkv, D)
+    S = 0
+    if block_idx is not None:
+        S = block_idx.shape[-1]
+        if tuple(block_idx.shape) != (B, Hkv, 1, S):
+            raise BsaError("block_idx must be [B,Hkv,1,S]", 2)
+    if out is not None:
+        _in_place(what, "out", out, q.shape, torch.bfloat16)
+    if lse is not None:
+        _in_place(what, "lse", lse, (B, Hq, 1), torch.float32)
+    with _on_stream(torch, q.device, stream) as handle:
+        q = q.contiguous()
+        table, lens = page_table.to(torch.int32).contiguous(), cache_lens.to(torch.int32).contiguous()
+        idx = None if block_idx is None else block_idx.to(torch.int32).contiguous()
+        if workspace is None:
+            need = nsa_select_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S)
+            workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and return_lse:
+            lse = torch.empty((B, Hq, 1), device=q.device, dtype=torch.float32)
+        st = nsa_select_decode_raw(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                   v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                                   None if idx is None else idx.data_ptr(), out.data_ptr(),
+                                   None if lse is None else lse.data_ptr(), B, Hq, Hkv, D, page_size, max_pages, pages,
+                                   S, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+    _check(st, what)
     return (out, lse) if return_lse else out
 
 

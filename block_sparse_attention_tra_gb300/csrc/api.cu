@@ -87,6 +87,24 @@ int check_nsa_args(const void* q, const void* k, const void* v, const int32_t* b
   return BSA_OK;
 }
 
+// Sizes of the paged-cache entry points.
+int check_cache_shape(int B, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || D < 1 || page_size < 1 || max_pages < 1 || num_pages < 1) return BSA_ERR_SHAPE;
+  if (Hq % Hkv != 0) return BSA_ERR_SHAPE;
+  // positions and (sequence, head) pairs are 32-bit numbers
+  if (static_cast<long long>(max_pages) * page_size > 0x7fffffffLL) return BSA_ERR_SHAPE;
+  if (static_cast<long long>(B) * Hq > 0x7fffffffLL || static_cast<long long>(B) * max_pages >= (1LL << 40))
+    return BSA_ERR_SHAPE;
+  if (static_cast<long long>(num_pages) * Hkv >= (1LL << 40) / (static_cast<long long>(page_size) * D))
+    return BSA_ERR_SHAPE;
+  if (D != 16 && D != 32 && D != 64 && D != 128) return BSA_ERR_UNSUPPORTED;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return BSA_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 16) return BSA_ERR_UNSUPPORTED;
+  return BSA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // The kernels are built for sm_103a only; refuse other devices up front
 // instead of failing inside the launch.
 int check_device() {
@@ -373,6 +391,90 @@ int nsa_select_forward_fsa(const void* q, const void* k, const void* v, const in
   return launch_nsa_fsa(q, k, v, block_idx, out, lse, B, Hq, Hkv, T, D, S, workspace, stream);
 }
 
+size_t nsa_select_backward_workspace_size(int B, int Hq, int Hkv, int T, int D, int block_size, int S) {
+  if (check_nsa_shape(B, Hq, Hkv, T, D, block_size, S) != BSA_OK) return 0;
+  // list positions are 32-bit numbers; (batch, kv head) pairs run along a grid's second axis
+  if (static_cast<long long>(B) * Hkv * T * S >= (1LL << 31) || static_cast<long long>(B) * Hkv > 65535) return 0;
+  return nsa_bwd_workspace_bytes(B, Hq, Hkv, T, D, block_size, S);
+}
+
+int nsa_select_backward(const void* q, const void* k, const void* v, const int32_t* block_idx, const void* out,
+                        const float* lse, const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
+                        int T, int D, int block_size, int S, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream) {
+  if (lse == nullptr || dout == nullptr || dq == nullptr || dk == nullptr || dv == nullptr || workspace == nullptr)
+    return BSA_ERR_NULLPTR;
+  const int chk = check_nsa_args(q, k, v, block_idx, out, lse, B, Hq, Hkv, T, D, block_size, S);
+  if (chk != BSA_OK) return chk;
+  if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return BSA_ERR_ALIGN;
+  const size_t need = nsa_select_backward_workspace_size(B, Hq, Hkv, T, D, block_size, S);
+  if (need == 0) return BSA_ERR_SHAPE;
+  if (workspace_bytes < need) return BSA_ERR_SCRATCH_LIMIT;
+  const int dev = check_device();
+  if (dev != OK) return dev;
+  return launch_nsa_bwd(q, k, v, block_idx, out, lse, dout, dq, dk, dv, B, Hq, Hkv, T, D, block_size, S, workspace,
+                        stream);
+}
+
+int nsa_cache_append(const void* k, const void* v, const void* q, void* q_out, void* k_cache, void* v_cache,
+                     float* k_scale, float* v_scale, const int32_t* page_table, const int32_t* cache_lens,
+                     const int32_t* new_lens, const float* inv_freq, int B, int Hq, int Hkv, int n, int D,
+                     int page_size, int max_pages, int num_pages, int rotary_dim, int interleaved, int dtype,
+                     cudaStream_t stream) {
+  if (k == nullptr || v == nullptr || k_cache == nullptr || v_cache == nullptr || k_scale == nullptr ||
+      v_scale == nullptr || page_table == nullptr || cache_lens == nullptr)
+    return BSA_ERR_NULLPTR;
+  if ((q == nullptr) != (q_out == nullptr) || (rotary_dim != 0 && inv_freq == nullptr)) return BSA_ERR_NULLPTR;
+  if (dtype != BSA_F32 && dtype != BSA_BF16) return BSA_ERR_DTYPE;
+  const int sh = check_cache_shape(B, Hq, Hkv, D, page_size, max_pages, num_pages);
+  if (sh != BSA_OK) return sh;
+  if (n < 1 || static_cast<long long>(B) * Hq * n >= (1LL << 40) / D) return BSA_ERR_SHAPE;
+  if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 16 != 0) return BSA_ERR_UNSUPPORTED;
+  const void* ptrs[6] = {k, v, q, q_out, k_cache, v_cache};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return BSA_ERR_ALIGN;
+  const void* words[6] = {k_scale, v_scale, page_table, cache_lens, new_lens, inv_freq};
+  for (const void* ptr : words)
+    if (!aligned4(ptr)) return BSA_ERR_ALIGN;
+  const int dev = check_device();
+  if (dev != OK) return dev;
+  return launch_nsa_cache_append(k, v, q, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens,
+                                 inv_freq, B, Hq, Hkv, n, D, page_size, max_pages, num_pages, rotary_dim,
+                                 interleaved != 0, dtype == BSA_F32, stream);
+}
+
+size_t nsa_select_decode_workspace_size(int B, int Hq, int Hkv, int D, int page_size, int max_pages, int S) {
+  if (S < 0 || S > 32 || check_cache_shape(B, Hq, Hkv, D, page_size, max_pages, 1) != BSA_OK) return 0;
+  return nsa_decode_workspace_bytes(D);
+}
+
+int nsa_select_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                      const float* v_scale, const int32_t* page_table, const int32_t* cache_lens,
+                      const int32_t* block_idx, void* out, float* lse, int B, int Hq, int Hkv, int D, int page_size,
+                      int max_pages, int num_pages, int S, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream) {
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || k_scale == nullptr || v_scale == nullptr ||
+      page_table == nullptr || cache_lens == nullptr || out == nullptr || workspace == nullptr)
+    return BSA_ERR_NULLPTR;
+  const int sh = check_cache_shape(B, Hq, Hkv, D, page_size, max_pages, num_pages);
+  if (sh != BSA_OK) return sh;
+  if (block_idx != nullptr ? (S < 1 || S > 32) : S != 0) return BSA_ERR_SHAPE;
+  const void* ptrs[5] = {q, k_cache, v_cache, out, workspace};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return BSA_ERR_ALIGN;
+  const void* words[6] = {k_scale, v_scale, page_table, cache_lens, block_idx, lse};
+  for (const void* ptr : words)
+    if (!aligned4(ptr)) return BSA_ERR_ALIGN;
+  if (workspace_bytes < nsa_select_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S))
+    return BSA_ERR_SCRATCH_LIMIT;
+  const int dev = check_device();
+  if (dev != OK) return dev;
+  return launch_nsa_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx, out, lse, B, Hq,
+                           Hkv, D, page_size, max_pages, num_pages, S, workspace, stream);
+}
+
 const char* bsa_status_string(int status) {
   switch (status) {
     case BSA_OK: return "success";
@@ -433,9 +535,9 @@ int bsa_read_probe(const void* buf, size_t bytes, int reps, unsigned int* sink, 
 }
 
 int bsa_device_error(void) {
-  const unsigned codes[7] = {tra_bf16_device_error(), tra_f32_device_error(), nsa_device_error(),
+  const unsigned codes[8] = {tra_bf16_device_error(), tra_f32_device_error(), nsa_device_error(),
                              tra_bwd_device_error(), tra_diff_device_error(), nsa_fsa_device_error(),
-                             selftest_device_error()};
+                             nsa_bwd_device_error(), selftest_device_error()};
   unsigned worst = 0;
   for (unsigned c : codes) {
     if (c == 0xffffffffu) return -1;

@@ -127,6 +127,33 @@ int launch_tra_host(const void* q, const void* k, const void* v, void* out, int 
 int launch_nsa_fsa(const void* q, const void* k, const void* v, const int32_t* block_idx, void* out, float* lse,
                    int B, int Hq, int Hkv, int T, int D, int S, void* workspace, cudaStream_t stream);
 
+// Gradients of the NSA selection attention (nsa_bwd.cu).  `workspace` holds
+// nsa_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+size_t nsa_bwd_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int block_size, int S);
+int launch_nsa_bwd(const void* q, const void* k, const void* v, const int32_t* block_idx, const void* out,
+                   const float* lse, const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int T,
+                   int D, int block_size, int S, void* workspace, cudaStream_t stream);
+
+// New tokens' keys and values into the paged e4m3 cache, keys (and q into
+// q_out, both nullable) rotated by position (nsa_cache.cu).  rotary = 0: no
+// rotation; otherwise inv_freq holds rotary / 2 floats.
+int launch_nsa_cache_append(const void* k, const void* v, const void* q, void* q_out, void* k_cache, void* v_cache,
+                            float* k_scale, float* v_scale, const int32_t* table, const int32_t* lens,
+                            const int32_t* new_lens, const float* inv_freq, int B, int Hq, int Hkv, int n, int D,
+                            int page, int max_pages, int num_pages, int rotary, bool interleaved, bool f32,
+                            cudaStream_t stream);
+
+// Attention of one query token per sequence over that cache (nsa_decode.cu);
+// block_idx null: every page.  `workspace` holds nsa_decode_workspace_bytes(D)
+// bytes, 16-byte aligned: the partial results of at most DECODE_MAX_RANGES
+// ranges of the work list.
+constexpr int DECODE_MAX_RANGES = 512;
+size_t nsa_decode_workspace_bytes(int D);
+int launch_nsa_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                      const float* v_scale, const int32_t* table, const int32_t* lens, const int32_t* block_idx,
+                      void* out, float* lse, int B, int Hq, int Hkv, int D, int page, int max_pages, int num_pages,
+                      int S, void* workspace, cudaStream_t stream);
+
 // Self tests (selftest.cu): the bounded wait's expiry branch (result = 0 when
 // the wait gave up, 1 if it unexpectedly completed) and the FMA-pipe log2
 // beside CUDA's log2f.
@@ -144,6 +171,7 @@ unsigned int nsa_device_error();
 unsigned int tra_bwd_device_error();
 unsigned int tra_diff_device_error();
 unsigned int nsa_fsa_device_error();
+unsigned int nsa_bwd_device_error();
 unsigned int selftest_device_error();
 
 // Power class of the TRA epilogue: p == 1, p == 2, or the general exp2/log2

@@ -457,6 +457,167 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
                                    size_t workspace_bytes,
                                    cudaStream_t stream);
 
+/*
+ * nsa_select_backward -- gradients of nsa_select_forward (bf16).
+ *
+ * The page "nsa_selection_kernel.py" defines the operation; this differentiates
+ * it.  With c = D^-0.5, row i's set J of nsa_select_forward, and that call's
+ * out and lse:
+ *
+ *   p_ij  = exp(c q_i . k_j - lse_i)            (recomputed; nothing is stored)
+ *   dS_ij = c p_ij (dout_i . v_j - dout_i . out_i)
+ *   dq_i  = sum_{j in J} dS_ij k_j
+ *   dk_j  = sum dS_ij q_i,  dv_j = sum p_ij dout_i   over the rows i that read j
+ *           and the Hq / Hkv query heads that share the kv head
+ *
+ * A row that selects nothing has dq = 0 and adds nothing to dk and dv; a key
+ * that no row reads has dk = dv = 0.  p and dS are rounded to bf16 before the
+ * products with dout, q and k; every sum is fp32, in an order that does not
+ * vary: results repeat bit for bit.
+ *
+ *   q, out, dout, dq   : [B, Hq, T, D] bf16 (out as the forward wrote it).
+ *   k, v, dk, dv       : [B, Hkv, T, D] bf16.
+ *   block_idx, D, block_size, S, T, Hq, Hkv : as for nsa_select_forward (the
+ *                        same index tensor).
+ *   lse                : [B, Hq, T] fp32, as the forward wrote it.
+ *   dq, dk, dv must not alias the inputs or each other.
+ *   workspace          : caller-owned device memory of at least
+ *                        nsa_select_backward_workspace_size(...) bytes, 256-byte
+ *                        aligned; overwritten, and in use until the work on
+ *                        `stream` completes (one workspace per concurrent call).
+ *
+ * Errors: as for nsa_select_forward, plus BSA_ERR_NULLPTR for any NULL
+ * pointer, BSA_ERR_ALIGN for a misaligned workspace, BSA_ERR_SCRATCH_LIMIT for
+ * one that is too small, and BSA_ERR_SHAPE for B * Hkv * T * S >= 2^31 or
+ * B * Hkv > 65535 (for which the size function returns 0, as for any sizes
+ * that are not accepted).
+ */
+BSA_API size_t nsa_select_backward_workspace_size(int B, int Hq, int Hkv,
+                                                  int T, int D, int block_size,
+                                                  int S);
+BSA_API int nsa_select_backward(const void* q, const void* k, const void* v,
+                                const int32_t* block_idx, const void* out,
+                                const float* lse, const void* dout, void* dq,
+                                void* dk, void* dv, int B, int Hq, int Hkv,
+                                int T, int D, int block_size, int S,
+                                void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/*
+ * The paged cache of nsa_cache_append and nsa_select_decode (the pages have no
+ * counterpart; they end at whole sequences).
+ *
+ *   k_cache, v_cache : [num_pages, Hkv, page_size, D] e4m3 codes (one byte:
+ *                      sign, 4 exponent bits, 3 mantissa bits, no infinities).
+ *   k_scale, v_scale : [num_pages, Hkv] fp32.  A code c of a page stands for
+ *                      scale * c.
+ *   page_table       : [B, max_pages] int32; the pool page of each logical page
+ *                      of each sequence.  Token t of sequence b lies in slot
+ *                      t % page_size of pool page page_table[b, t / page_size].
+ *   page_size        : 16, 32, 64 or 128: the selection's block.
+ *   D                : 16, 32, 64 or 128.   Hq % Hkv == 0, Hq / Hkv <= 16.
+ *   max_pages * page_size <= 2^31 - 1; pool offsets are 64-bit.
+ *
+ * A table entry outside [0, num_pages) is never followed: the append leaves
+ * such a page's tokens out, the decode does not read them.
+ */
+
+/*
+ * nsa_cache_append -- new tokens' keys and values into the paged cache, keys
+ * rotated by position, and optionally queries rotated beside them.
+ *
+ * Sequence b holds cache_lens[b] tokens; its new token t (0 <= t < new_lens[b])
+ * gets position m = cache_lens[b] + t and is written to that slot.  Rotation
+ * by angle m * inv_freq[j] of the pair j < rotary_dim / 2 of a row x:
+ *
+ *   (x_a, x_b) -> (x_a cos - x_b sin, x_a sin + x_b cos),
+ *   (a, b) = (j, j + rotary_dim / 2), or (2j, 2j + 1) when interleaved != 0;
+ *
+ * elements past rotary_dim stay.  Angles are reduced to one turn in 64-bit
+ * fixed point, so far positions lose nothing.  Values are not rotated.
+ *
+ * Scale of a page and head: for a page whose first slot this call writes, the
+ * least 2^e, e >= -96, with max |x| <= 448 * 2^e over the (rotated) values
+ * written; for a page begun before, its scale if max |x| <= 448 * scale, else
+ * that least power of two, and the codes held are multiplied by the ratio of
+ * the scales and rounded to e4m3 again.  Values are rounded to the nearest
+ * code, ties to even; infinities become +-448 and, like NaN (stored as NaN),
+ * do not count towards the maximum.  Slots that get no token, and pages that
+ * get none, are left as they were.
+ *
+ *   k, v       : [B, Hkv, n, D] of `dtype`.
+ *   q, q_out   : [B, Hq, n, D] of `dtype`, or both NULL; q_out may be q.  Rows
+ *                past new_lens[b] are not written.
+ *   cache_lens : [B] int32 (a negative one: nothing is cached for b).
+ *   new_lens   : [B] int32, clamped to n, or NULL (n for every sequence).
+ *   inv_freq   : [rotary_dim / 2] fp32, finite; may be NULL if rotary_dim is 0.
+ *   rotary_dim : a multiple of 16 from 0 (no rotation) to D.
+ *   dtype      : BSA_BF16 or BSA_F32.
+ *   Tokens past max_pages * page_size are left out.  No two sequences may
+ *   write the same pool page in one call.
+ *
+ * cache_lens is not advanced: add the new tokens before the next call and
+ * before the decode, which takes lengths that include the query's own token.
+ *
+ * Errors: BSA_ERR_NULLPTR, BSA_ERR_DTYPE, BSA_ERR_SHAPE, BSA_ERR_UNSUPPORTED
+ * (D, page_size, group size, rotary_dim), BSA_ERR_ALIGN, BSA_ERR_DEVICE,
+ * BSA_ERR_LAUNCH.
+ */
+BSA_API int nsa_cache_append(const void* k, const void* v, const void* q,
+                             void* q_out, void* k_cache, void* v_cache,
+                             float* k_scale, float* v_scale,
+                             const int32_t* page_table,
+                             const int32_t* cache_lens,
+                             const int32_t* new_lens, const float* inv_freq,
+                             int B, int Hq, int Hkv, int n, int D,
+                             int page_size, int max_pages, int num_pages,
+                             int rotary_dim, int interleaved, int dtype,
+                             cudaStream_t stream);
+
+/*
+ * nsa_select_decode -- nsa_select_forward's form for one query token per
+ * sequence over the paged cache: the query of sequence b is its last token,
+ * position cache_lens[b] - 1.  With G = Hq / Hkv and query head h reading kv
+ * head h / G, over
+ *
+ *   J = { t < cache_lens[b] : t / page_size is an entry of block_idx[b, h/G, :] }
+ *       (every t < cache_lens[b] when block_idx is NULL):
+ *
+ *   out = sum_{t in J} softmax_t((q . k_t) D^-0.5) v_t        (0 if J is empty)
+ *   lse = ln sum_{t in J} exp((q . k_t) D^-0.5)            (-1e9 if J is empty)
+ *
+ * with k_t, v_t the values the codes stand for, which enter the products
+ * unrounded (the probabilities are rounded to f16; sums are fp32).
+ *
+ *   q, out     : [B, Hq, 1, D] bf16 (q rotated already).
+ *   block_idx  : [B, Hkv, 1, S] int32 logical pages, read as a set, -1 =
+ *                padding, 1 <= S <= 32; or NULL with S = 0.  Entries outside
+ *                the sequence are skipped.
+ *   lse        : [B, Hq, 1] fp32, or NULL to skip it.
+ *   cache_lens : [B] int32; 0 (or less) is an empty sequence, and lengths past
+ *                max_pages * page_size count as that.
+ *   workspace  : caller-owned device memory of at least
+ *                nsa_select_decode_workspace_size(...) bytes, 16-byte aligned;
+ *                overwritten, in use until the work on `stream` completes (one
+ *                workspace per concurrent call).
+ *
+ * Results repeat bit for bit.  Errors: BSA_ERR_NULLPTR, BSA_ERR_SHAPE,
+ * BSA_ERR_UNSUPPORTED, BSA_ERR_ALIGN, BSA_ERR_SCRATCH_LIMIT, BSA_ERR_DEVICE,
+ * BSA_ERR_LAUNCH.
+ */
+BSA_API size_t nsa_select_decode_workspace_size(int B, int Hq, int Hkv, int D,
+                                                int page_size, int max_pages,
+                                                int S);
+BSA_API int nsa_select_decode(const void* q, const void* k_cache,
+                              const void* v_cache, const float* k_scale,
+                              const float* v_scale, const int32_t* page_table,
+                              const int32_t* cache_lens,
+                              const int32_t* block_idx, void* out, float* lse,
+                              int B, int Hq, int Hkv, int D, int page_size,
+                              int max_pages, int num_pages, int S,
+                              void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
 /* Static, NUL-terminated description of a bsa_status value (never NULL). */
 BSA_API const char* bsa_status_string(int status);
 

@@ -165,3 +165,53 @@ def nsa_pairs(T: int, block_size: int, S: int) -> int:
         c, r = divmod(i, block_size)
         total += (r + 1) + block_size * min(S - 1, c)
     return total
+
+
+def nsa_select_backward(q, k, v, block_idx, out, lse, dout, block_size: int):
+    """Gradients of ``nsa_select_forward``: ``(dq, dk, dv, sums)``.
+
+    With c = D^-0.5 and the row's tokens J: p = exp(c q.k - lse), dS = c p
+    (dout.v - dout.out), dq = sum_J dS k, and dk, dv the sums of dS q and
+    p dout over the rows (and the heads of the group) that read the key.
+
+    ``sums`` holds what an error bound needs, as arrays shaped like the
+    gradients: for each of them, under ``"dq"``, ``"dk"``, ``"dv"``, the sum
+    of the absolute products (what a relative error of every p or dS is
+    multiplied by), and under ``"dq_e"``, ``"dk_e"``, ``"dv_e"`` the same with
+    every product weighted by how far an fp32 evaluation of its p and dP may
+    be off, in units of the sums' rounding step (a dS also by p times the
+    magnitudes that dP and dout.out sum).
+    """
+    q, k, v, idx = _check(q, k, v, block_idx, block_size)
+    out, dout, lse = (np.asarray(x, dtype=np.float64) for x in (out, dout, lse))
+    B, Hq, T, D = q.shape
+    Hkv = k.shape[1]
+    G = Hq // Hkv
+    c = float(D) ** -0.5
+    dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    sums = {n: np.zeros_like(x) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+    sums |= {n + "_e": np.zeros_like(x) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+    for b in range(B):
+        for g in range(Hkv):
+            hs = slice(g * G, (g + 1) * G)
+            for i in range(T):
+                t = selected_tokens(idx[b, g, i], i, block_size)
+                if len(t) == 0:
+                    continue
+                qi, di, oi, ki, vi = q[b, hs, i], dout[b, hs, i], out[b, hs, i], k[b, g, t], v[b, g, t]
+                p = np.exp(c * (qi @ ki.T) - lse[b, hs, i][:, None])
+                ds = c * p * (di @ vi.T - (di * oi).sum(-1, keepdims=True))
+                dq[b, hs, i] = ds @ ki
+                dk[b, g, t] += ds.T @ qi
+                dv[b, g, t] += p.T @ di
+                # steps by which p's exponent, and dP - delta, may be off
+                ep = (D + 4) * c * (np.abs(qi) @ np.abs(ki).T) + 4 * np.abs(lse[b, hs, i])[:, None] + 8
+                ed = (D + 4) * (np.abs(di) @ np.abs(vi).T + (np.abs(di) * np.abs(oi)).sum(-1, keepdims=True))
+                es = np.abs(ds) * (ep + 4) + c * p * ed
+                sums["dq"][b, hs, i] = np.abs(ds) @ np.abs(ki)
+                sums["dk"][b, g, t] += np.abs(ds).T @ np.abs(qi)
+                sums["dv"][b, g, t] += p.T @ np.abs(di)
+                sums["dq_e"][b, hs, i] = es @ np.abs(ki)
+                sums["dk_e"][b, g, t] += es.T @ np.abs(qi)
+                sums["dv_e"][b, g, t] += (p * ep).T @ np.abs(di)
+    return dq, dk, dv, sums
