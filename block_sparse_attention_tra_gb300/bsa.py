@@ -258,34 +258,40 @@ def nsa_select_decode_raw(q, k_cache, v_cache, k_scale, v_scale, page_table, cac
 
 @contextlib.contextmanager
 def _on_stream(torch, device, stream):
-    """Within the block ``device`` is current and allocations, copies and the
-    library call all go to ``stream`` (default: the device's current stream),
-    whose handle is yielded."""
+    """Within the block ``device`` is current and ``stream`` (None: the
+    device's current one) is its current stream, so that allocations, copies
+    and the library call all go there."""
     if stream is not None and not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream is not None and stream.device != device:
         raise BsaError(f"the stream is on {stream.device}, the tensors are on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield torch.cuda.current_stream(device).cuda_stream
+        yield
 
 
 def _one_device(what, first, *others):
-    """``first`` on a CUDA device and every other tensor (None: absent) on the same one."""
-    if first.device.type != "cuda":
+    """``first`` on a CUDA device and every other tensor (None: absent) on the same one; its index."""
+    dev = first.get_device()
+    if dev < 0:
         raise BsaError(f"{what} takes CUDA tensors (no CPU path)")
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != dev:
             raise BsaError(f"{what}: tensors on {first.device} and {t.device}")
+    return dev
 
 
 def _in_place(what, name, t, shape, *dtypes):
     """Tensors the library writes into (or reads in place) keep their memory: exact shape, type and layout."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise BsaError(f"{what}: {name} must be {list(shape)}, got {list(t.shape)}", 2)
     if t.dtype not in dtypes:
         raise BsaError(f"{what}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}", 3)
     if not t.is_contiguous():
         raise BsaError(f"{what}: {name} must be contiguous", 2)
+
+
+def _int32(torch, t):
+    return (t if t.dtype is torch.int32 else t.to(torch.int32)).contiguous()
 
 
 def _stream_handle(stream):
@@ -611,27 +617,29 @@ def nsa_select_backward(q, k, v, block_idx, out, lse, dout, block_size: int = 64
     """
     import torch
 
-    _one_device("nsa_select_backward", q, k, v, block_idx, out, lse, dout, workspace)
+    dev = _one_device("nsa_select_backward", q, k, v, block_idx, out, lse, dout, workspace)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on_stream(torch, q.device, stream):
+            return nsa_select_backward(q, k, v, block_idx, out, lse, dout, block_size, workspace)
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or block_idx.dim() != 4:
         raise BsaError("q [B,Hq,T,D], k/v [B,Hkv,T,D], block_idx [B,Hkv,T,S] expected", 2)
     B, Hq, T, D = q.shape
     Hkv, S = k.shape[1], block_idx.shape[-1]
-    if (q.shape != out.shape or q.shape != dout.shape or tuple(lse.shape) != (B, Hq, T)
-            or tuple(k.shape) != (B, Hkv, T, D) or tuple(block_idx.shape) != (B, Hkv, T, S)):
+    if (q.shape != out.shape or q.shape != dout.shape or lse.shape != (B, Hq, T)
+            or k.shape != (B, Hkv, T, D) or block_idx.shape != (B, Hkv, T, S)):
         raise BsaError("q, out, dout [B,Hq,T,D], lse [B,Hq,T], k/v [B,Hkv,T,D], block_idx [B,Hkv,T,S] expected", 2)
     if any(t.dtype != torch.bfloat16 for t in (q, k, v, out, dout)) or lse.dtype != torch.float32:
         raise BsaError("nsa_select_backward takes bfloat16 q, k, v, out, dout and float32 lse", 3)
-    with _on_stream(torch, q.device, stream) as handle:
-        q, k, v, out, lse, dout = (t.contiguous() for t in (q, k, v, out, lse, dout))
-        idx = block_idx.to(torch.int32).contiguous()
+    q, k, v, out, lse, dout = (t.contiguous() for t in (q, k, v, out, lse, dout))
+    idx = _int32(torch, block_idx)
+    if workspace is None:
         need = nsa_select_backward_workspace_size(B, Hq, Hkv, T, D, block_size, S)
-        if workspace is None:
-            workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        st = nsa_select_backward_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(), out.data_ptr(),
-                                     lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B,
-                                     Hq, Hkv, T, D, block_size, S, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), handle)
+        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    st = nsa_select_backward_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq,
+                                 Hkv, T, D, block_size, S, workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream)
     _check(st, "nsa_select_backward")
     return dq, dk, dv
 
@@ -675,14 +683,13 @@ def nsa_select_attention(q, k, v, block_idx, block_size: int = 64):
 
 def _check_cache(torch, what, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, B, Hkv, D):
     """Shapes and types of the paged cache; returns (num_pages, page_size, max_pages)."""
-    if k_cache.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != B or tuple(cache_lens.shape) != (B,):
+    if k_cache.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != B or cache_lens.shape != (B,):
         raise BsaError(f"{what}: k_cache [pages,Hkv,page_size,D], page_table [B,max_pages], cache_lens [B] expected", 2)
-    pages, page_size = k_cache.shape[0], k_cache.shape[2]
-    codes = (torch.float8_e4m3fn, torch.uint8)
-    _in_place(what, "k_cache", k_cache, (pages, Hkv, page_size, D), *codes)
-    _in_place(what, "v_cache", v_cache, (pages, Hkv, page_size, D), *codes)
-    _in_place(what, "k_scale", k_scale, (pages, Hkv), torch.float32)
-    _in_place(what, "v_scale", v_scale, (pages, Hkv), torch.float32)
+    pages, _, page_size, _ = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _in_place(what, name, t, (pages, Hkv, page_size, D), torch.float8_e4m3fn, torch.uint8)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _in_place(what, name, t, (pages, Hkv), torch.float32)
     return pages, page_size, page_table.shape[1]
 
 
@@ -706,7 +713,12 @@ def nsa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache
     import torch
 
     what = "nsa_cache_append"
-    _one_device(what, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens, inv_freq, q, q_out)
+    dev = _one_device(what, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens, inv_freq, q,
+                      q_out)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on_stream(torch, k.device, stream):
+            return nsa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens,
+                                    inv_freq, interleaved, q, q_out)
     if k.dim() != 4 or k.shape != v.shape or (q is not None and q.dim() != 4):
         raise BsaError("k, v [B,Hkv,n,D] and q [B,Hq,n,D] expected", 2)
     B, Hkv, n, D = k.shape
@@ -715,33 +727,33 @@ def nsa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache
                                                B, Hkv, D)
     if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
         raise BsaError("k, v, q must share one dtype", 3)
-    if q is not None and tuple(q.shape) != (B, Hq, n, D):
+    if q is not None and q.shape != (B, Hq, n, D):
         raise BsaError("q must be [B,Hq,n,D] with k's B, n and D", 2)
     if q is None and q_out is not None:
         raise BsaError("q_out given without q")
     if q_out is not None:
         _in_place(what, "q_out", q_out, q.shape, q.dtype)
-    if new_lens is not None and tuple(new_lens.shape) != (B,):
+    if new_lens is not None and new_lens.shape != (B,):
         raise BsaError("new_lens must be [B]", 2)
     if inv_freq is not None and inv_freq.dim() != 1:
         raise BsaError("inv_freq must be [rotary_dim / 2]", 2)
     rotary = 0 if inv_freq is None else 2 * inv_freq.numel()
-    with _on_stream(torch, k.device, stream) as handle:
-        k, v = k.contiguous(), v.contiguous()
-        table, lens = page_table.to(torch.int32).contiguous(), cache_lens.to(torch.int32).contiguous()
-        news = None if new_lens is None else new_lens.to(torch.int32).contiguous()
-        freq = None if inv_freq is None else inv_freq.to(torch.float32).contiguous()
-        if q is not None:
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if news is None else torch.zeros(
-                    q.shape, dtype=q.dtype, device=q.device)
-            q = q.contiguous()
-        st = nsa_cache_append_raw(k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
-                                  None if q is None else q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                  k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(),
-                                  None if news is None else news.data_ptr(), None if freq is None else freq.data_ptr(),
-                                  B, Hq, Hkv, n, D, page_size, max_pages, pages, rotary, interleaved, _dtype_code(k),
-                                  handle)
+    k, v = k.contiguous(), v.contiguous()
+    table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
+    news = None if new_lens is None else _int32(torch, new_lens)
+    freq = None if inv_freq is None else inv_freq.to(torch.float32).contiguous()
+    q_ptr = out_ptr = None
+    if q is not None:
+        if q_out is None:
+            make = torch.empty if news is None else torch.zeros
+            q_out = make(q.shape, dtype=q.dtype, device=q.device)
+        q = q.contiguous()
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    st = nsa_cache_append_raw(k.data_ptr(), v.data_ptr(), q_ptr, out_ptr, k_cache.data_ptr(), v_cache.data_ptr(),
+                              k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                              None if news is None else news.data_ptr(), None if freq is None else freq.data_ptr(), B,
+                              Hq, Hkv, n, D, page_size, max_pages, pages, rotary, interleaved, _dtype_code(k),
+                              torch.cuda.current_stream(dev).cuda_stream)
     _check(st, what)
     return q_out
 
@@ -764,7 +776,12 @@ def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
     import torch
 
     what = "nsa_select_decode"
-    _one_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx, out, lse, workspace)
+    dev = _one_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx, out, lse,
+                      workspace)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on_stream(torch, q.device, stream):
+            return nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx, out,
+                                     lse, return_lse, workspace)
     if q.dim() != 4 or q.shape[2] != 1 or k_cache.dim() != 4:
         raise BsaError("q [B,Hq,1,D] and k_cache [pages,Hkv,page_size,D] expected", 2)
     if q.dtype != torch.bfloat16:
@@ -776,28 +793,28 @@ def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
     S = 0
     if block_idx is not None:
         S = block_idx.shape[-1]
-        if tuple(block_idx.shape) != (B, Hkv, 1, S):
+        if block_idx.shape != (B, Hkv, 1, S):
             raise BsaError("block_idx must be [B,Hkv,1,S]", 2)
     if out is not None:
         _in_place(what, "out", out, q.shape, torch.bfloat16)
     if lse is not None:
         _in_place(what, "lse", lse, (B, Hq, 1), torch.float32)
-    with _on_stream(torch, q.device, stream) as handle:
-        q = q.contiguous()
-        table, lens = page_table.to(torch.int32).contiguous(), cache_lens.to(torch.int32).contiguous()
-        idx = None if block_idx is None else block_idx.to(torch.int32).contiguous()
-        if workspace is None:
-            need = nsa_select_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S)
-            workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and return_lse:
-            lse = torch.empty((B, Hq, 1), device=q.device, dtype=torch.float32)
-        st = nsa_select_decode_raw(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                                   v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(),
-                                   None if idx is None else idx.data_ptr(), out.data_ptr(),
-                                   None if lse is None else lse.data_ptr(), B, Hq, Hkv, D, page_size, max_pages, pages,
-                                   S, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+    q = q.contiguous()
+    table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
+    idx = None if block_idx is None else _int32(torch, block_idx)
+    if workspace is None:
+        need = nsa_select_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S)
+        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and return_lse:
+        lse = torch.empty((B, Hq, 1), device=q.device, dtype=torch.float32)
+    st = nsa_select_decode_raw(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                               v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                               None if idx is None else idx.data_ptr(), out.data_ptr(),
+                               None if lse is None else lse.data_ptr(), B, Hq, Hkv, D, page_size, max_pages, pages, S,
+                               workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               torch.cuda.current_stream(dev).cuda_stream)
     _check(st, what)
     return (out, lse) if return_lse else out
 

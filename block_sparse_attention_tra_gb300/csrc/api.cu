@@ -393,8 +393,10 @@ int nsa_select_forward_fsa(const void* q, const void* k, const void* v, const in
 
 size_t nsa_select_backward_workspace_size(int B, int Hq, int Hkv, int T, int D, int block_size, int S) {
   if (check_nsa_shape(B, Hq, Hkv, T, D, block_size, S) != BSA_OK) return 0;
-  // list positions are 32-bit numbers; (batch, kv head) pairs run along a grid's second axis
-  if (static_cast<long long>(B) * Hkv * T * S >= (1LL << 31) || static_cast<long long>(B) * Hkv > 65535) return 0;
+  // list positions are 32-bit numbers, a query and its slot one of them; (batch, kv head) pairs run along a grid's second axis
+  if (static_cast<long long>(B) * Hkv * T * S >= (1LL << 31) || T >= (1 << 26) ||
+      static_cast<long long>(B) * Hkv > 65535)
+    return 0;
   return nsa_bwd_workspace_bytes(B, Hq, Hkv, T, D, block_size, S);
 }
 
@@ -535,9 +537,9 @@ int bsa_read_probe(const void* buf, size_t bytes, int reps, unsigned int* sink, 
 }
 
 int bsa_device_error(void) {
-  const unsigned codes[8] = {tra_bf16_device_error(), tra_f32_device_error(), nsa_device_error(),
+  const unsigned codes[9] = {tra_bf16_device_error(), tra_f32_device_error(), nsa_device_error(),
                              tra_bwd_device_error(), tra_diff_device_error(), nsa_fsa_device_error(),
-                             nsa_bwd_device_error(), selftest_device_error()};
+                             nsa_bwd_device_error(), nsa_bwd_tc_device_error(), selftest_device_error()};
   unsigned worst = 0;
   for (unsigned c : codes) {
     if (c == 0xffffffffu) return -1;

@@ -172,6 +172,7 @@ unsigned int tra_bwd_device_error();
 unsigned int tra_diff_device_error();
 unsigned int nsa_fsa_device_error();
 unsigned int nsa_bwd_device_error();
+unsigned int nsa_bwd_tc_device_error();
 unsigned int selftest_device_error();
 
 // Power class of the TRA epilogue: p == 1, p == 2, or the general exp2/log2

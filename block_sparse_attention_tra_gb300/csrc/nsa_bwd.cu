@@ -29,6 +29,7 @@
 
 #include "kernels.h"
 #include "mma_sync.cuh"
+#include "nsa_bwd.cuh"
 #include "nsa_slots.cuh"
 #include "ptx.cuh"
 
@@ -38,8 +39,6 @@ namespace {
 constexpr int QCHUNK = 128;      // query rows of one mark / fill block
 constexpr int MASKS = QCHUNK / 32;
 constexpr int BLK_TILE = 2048;   // blocks whose masks a mark / fill block holds
-constexpr int ITEM_QUERIES = 512;  // queries of a work item at most
-constexpr float LOG2E = 1.4426950408889634f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes = 16u) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
@@ -129,14 +128,14 @@ __global__ void __launch_bounds__(1024) bwd_prefix_kernel(int* __restrict__ coun
 constexpr int SCAN_THREADS = 1024;
 __global__ void __launch_bounds__(SCAN_THREADS) bwd_scan_kernel(const int* __restrict__ total, int* __restrict__ off,
                                                                 int* __restrict__ item_off, int4* __restrict__ items,
-                                                                int NB) {
+                                                                int NB, int item_queries) {
   __shared__ int wp[32], wi[32];
   const int per = (NB + SCAN_THREADS - 1) / SCAN_THREADS;
   const int lo = min(NB, static_cast<int>(threadIdx.x) * per), hi = min(NB, lo + per);
   int np = 0, ni = 0;
   for (int e = lo; e < hi; ++e) {
     np += total[e];
-    ni += (total[e] + ITEM_QUERIES - 1) / ITEM_QUERIES;
+    ni += (total[e] + item_queries - 1) / item_queries;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int sp = np, si = ni;
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) bwd_scan_kernel(const int* __res
   __syncthreads();
   int pb = sp - np + (warp > 0 ? wp[warp - 1] : 0), ib = si - ni + (warp > 0 ? wi[warp - 1] : 0);
   for (int e = lo; e < hi; ++e) {
-    const int c = total[e], k = (c + ITEM_QUERIES - 1) / ITEM_QUERIES;
+    const int c = total[e], k = (c + item_queries - 1) / item_queries;
     off[e] = pb;
     item_off[e] = ib;
     // equal shares, so that no item of a block is a short rest
@@ -190,10 +189,13 @@ __global__ void __launch_bounds__(QCHUNK) bwd_fill_kernel(const int32_t* __restr
   for (int s = 0; s < S; ++s) {
     const int blk = row[s];
     if (blk < blk0 || blk >= blk0 + nb || blk >= n_blk || blk * bs > i) continue;
+    bool again = false;  // a repeated block counts in its first slot
+    for (int x = 0; x < s; ++x) again |= row[x] == blk;
+    if (again) continue;
     const uint32_t* m = mask[blk - blk0];
     int rank = __popc(m[w] & below);
     for (int x = 0; x < w; ++x) rank += __popc(m[x]);
-    list[off[bh * n_blk + blk] + before[blk] + rank] = i;  // (a repeated block writes the same place twice)
+    list[off[bh * n_blk + blk] + before[blk] + rank] = i * 32 + s;
   }
 }
 
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(DQ_THREADS, dq_min_ctas<D>())
   const int g = lane >> 2, t = lane & 3, mat = lane >> 3, mrow = lane & 7;
   const int n_blk = T / bs;
   const uint32_t sKV = smem_u32(smem + warp * L::WARP_BYTES);
-  const float scale_log2 = scale * LOG2E;
+  const float scale_log2 = scale * NSA_LOG2E;
 
   const long long stride = static_cast<long long>(gridDim.x) * DQ_WARPS;
   for (long long qg = static_cast<long long>(blockIdx.x) * DQ_WARPS + warp; qg < n_queries; qg += stride) {
@@ -305,8 +307,8 @@ __global__ void __launch_bounds__(DQ_THREADS, dq_min_ctas<D>())
       delta0 += __shfl_xor_sync(0xffffffffu, delta0, 2);
       delta1 += __shfl_xor_sync(0xffffffffu, delta1, 1);
       delta1 += __shfl_xor_sync(0xffffffffu, delta1, 2);
-      lse0 *= LOG2E;
-      lse1 *= LOG2E;
+      lse0 *= NSA_LOG2E;
+      lse1 *= NSA_LOG2E;
       if (t == 0) {
         if (g < G) stats[qg * G + g] = make_float2(lse0, delta0);
         if (g + 8 < G) stats[qg * G + g + 8] = make_float2(lse1, delta1);
@@ -319,10 +321,8 @@ __global__ void __launch_bounds__(DQ_THREADS, dq_min_ctas<D>())
       for (int e = lane; e < 16 * CPR; e += 32) {
         const int r = e / CPR, c = e % CPR;
         const size_t off = static_cast<size_t>(debug_index(tok0 + r, 0, T)) * D + c * 8;
-        // tokens after the query come as zeros: 0 times what they hold could be NaN
-        const uint32_t bytes = tok0 + r <= i ? 16u : 0u;
-        cp_async16(dk + r * L::RB + c * 16, kb + off, bytes);
-        cp_async16(dv + r * L::RB + c * 16, vb + off, bytes);
+        cp_async16(dk + r * L::RB + c * 16, kb + off);
+        cp_async16(dv + r * L::RB + c * 16, vb + off);
       }
     };
     ChunkIter cur{nsa_live_slots(block_idx + qg * S, S, i, n_blk, bs), i, bs, 0, 0, 0, 0, false};
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(WARPS * 32)
   const long long bg = item.x / n_blk;
   const int first = item.y, nq = item.z;
   const int qpt = 16 / G, nt = (nq + qpt - 1) / qpt;
-  const float scale_log2 = scale * LOG2E;
+  const float scale_log2 = scale * NSA_LOG2E;
   const int tok0 = blk * BS + warp * 16;  // this warp's tokens
 
   // A fragments of this warp's 16 key and value rows
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(WARPS * 32)
         const int r = e / CPR, c = e % CPR;
         const int slot = x * qpt + r / G;
         const bool in = r < qpt * G && slot < nq;
-        const int i = in ? debug_index(list[first + slot], 0, T) : 0;
+        const int i = in ? debug_index(list[first + slot] >> 5, 0, T) : 0;
         const size_t off = ((static_cast<size_t>(bg) * G + (in ? r % G : 0)) * T + i) * D + c * 8;
         cp_async16(st + r * L::RB + c * 16, q + off, in ? 16u : 0u);
         cp_async16(st + L::TILE + r * L::RB + c * 16, dout + off, in ? 16u : 0u);
@@ -585,10 +585,14 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const float* __restrict__
 
 // ------------------------------------------------------------ workspace plan
 
+// The tcgen05 pass serves the shapes of the forward's TMA kernel.
+bool tc_shape(int D, int bs) { return bs == 64 && (D == 64 || D == 128); }
+
 struct BwdPlan {
   long long NB, max_items;
-  int chunks, n_blk;
-  size_t stats_off, list_off, count_off, total_off, off_off, ioff_off, item_off, part_off, total;
+  int chunks, n_blk, item_queries;
+  size_t stats_off, list_off, count_off, total_off, off_off, ioff_off, item_off, part_off, rows_off, dqp_off, dqs_off,
+      total;
 };
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -599,7 +603,14 @@ BwdPlan bwd_plan(int B, int Hq, int Hkv, int T, int D, int bs, int S) {
   p.n_blk = T / bs;
   p.NB = static_cast<long long>(B) * Hkv * p.n_blk;
   p.chunks = (T + QCHUNK - 1) / QCHUNK;
-  p.max_items = (slots + ITEM_QUERIES - 1) / ITEM_QUERIES + p.NB;
+  // Work items: a few for each of 152 SMs, not so short that the start of one
+  // (and its partial result) outweighs its tiles, not so long that the last
+  // ones run alone.  tcgen05 pass: four a SM, of 8 to 86 tiles of 96 / G
+  // queries; general kernels: eight a SM, of 32 to 512 queries.
+  const bool tc = tc_shape(D, bs);
+  const long long per_tile = tc ? 96 / (Hq / Hkv) : 1, share = slots / (152 * (tc ? 4 : 8));
+  p.item_queries = static_cast<int>(std::max((tc ? 8 : 32) * per_tile, std::min((tc ? 86 : 512) * per_tile, share)));
+  p.max_items = (slots + p.item_queries - 1) / p.item_queries + p.NB;
   size_t o = 0;
   p.stats_off = o;  o = align256(o + static_cast<size_t>(B) * Hq * T * sizeof(float2));
   p.list_off = o;   o = align256(o + static_cast<size_t>(slots) * sizeof(int));
@@ -609,52 +620,34 @@ BwdPlan bwd_plan(int B, int Hq, int Hkv, int T, int D, int bs, int S) {
   p.ioff_off = o;   o = align256(o + static_cast<size_t>(p.NB + 1) * sizeof(int));
   p.item_off = o;   o = align256(o + static_cast<size_t>(p.max_items) * sizeof(int4));
   p.part_off = o;   o = align256(o + static_cast<size_t>(p.max_items) * 2 * bs * D * sizeof(float));
+  p.rows_off = p.dqp_off = p.dqs_off = o;
+  if (tc_shape(D, bs)) {
+    const size_t rows = static_cast<size_t>(slots) * (Hq / Hkv);
+    // (one query of zeros behind the last)
+    o = align256(o + (static_cast<size_t>(B) * Hq * T + Hq / Hkv) * 2 * D * sizeof(__nv_bfloat16));
+    p.dqp_off = o;
+    o = align256(o + rows * D * sizeof(__half));
+    p.dqs_off = o;  o = align256(o + rows * sizeof(float));
+  }
   p.total = o;
   return p;
 }
 
-struct BwdArgs {
-  const __nv_bfloat16 *q, *k, *v, *out, *dout;
-  const int32_t* idx;
-  const float* lse;
-  __nv_bfloat16 *dq, *dk, *dv;
-  int B, Hq, Hkv, T, bs, S;
-};
-
 template <int D, int WARPS>
-int launch_dkdv(const BwdArgs& a, const BwdPlan& p, uint8_t* ws, cudaStream_t stream) {
+int launch_dkdv(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) {
   using L = KvLayout<D>;
   auto kern = nsa_bwd_dkdv_kernel<D, WARPS>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
     return ERR_LAUNCH;
-  kern<<<static_cast<unsigned>(p.max_items), WARPS * 32, L::BYTES, stream>>>(
-      a.q, a.k, a.v, a.dout, reinterpret_cast<const float2*>(ws + p.stats_off),
-      reinterpret_cast<const int*>(ws + p.list_off), reinterpret_cast<const int4*>(ws + p.item_off),
-      reinterpret_cast<const int*>(ws + p.ioff_off) + p.NB, reinterpret_cast<float*>(ws + p.part_off), a.dk, a.dv,
-      a.Hq / a.Hkv, a.T, p.n_blk, 1.0f / sqrtf(static_cast<float>(D)));
+  kern<<<static_cast<unsigned>(w.max_items), WARPS * 32, L::BYTES, stream>>>(
+      a.q, a.k, a.v, a.dout, w.stats, w.list, w.items, w.n_items, w.part, a.dk, a.dv, a.Hq / a.Hkv, a.T, a.T / a.bs,
+      1.0f / sqrtf(static_cast<float>(D)));
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
+// dq, then dk and dv (or their items' sums), by the general kernels.
 template <int D>
-int launch_bwd(const BwdArgs& a, uint8_t* ws, cudaStream_t stream) {
-  const BwdPlan p = bwd_plan(a.B, a.Hq, a.Hkv, a.T, D, a.bs, a.S);
-  if (p.max_items > 0x7fffffffLL) return ERR_SHAPE;
-  int* list = reinterpret_cast<int*>(ws + p.list_off);
-  int* counts = reinterpret_cast<int*>(ws + p.count_off);
-  int* total = reinterpret_cast<int*>(ws + p.total_off);
-  int* off = reinterpret_cast<int*>(ws + p.off_off);
-  int* ioff = reinterpret_cast<int*>(ws + p.ioff_off);
-  int4* items = reinterpret_cast<int4*>(ws + p.item_off);
-  const int bh = a.B * a.Hkv;
-
-  const dim3 grid(p.chunks, bh, (p.n_blk + BLK_TILE - 1) / BLK_TILE);
-  const size_t mask_bytes = static_cast<size_t>(std::min(p.n_blk, BLK_TILE)) * MASKS * sizeof(uint32_t);
-  bwd_mark_kernel<<<grid, QCHUNK, mask_bytes, stream>>>(a.idx, counts, a.T, a.S, p.n_blk, a.bs);
-  bwd_prefix_kernel<<<dim3((p.n_blk + 31) / 32, bh), dim3(32, 32), 0, stream>>>(counts, total, p.chunks, p.n_blk);
-  bwd_scan_kernel<<<1, SCAN_THREADS, 0, stream>>>(total, off, ioff, items, static_cast<int>(p.NB));
-  bwd_fill_kernel<<<grid, QCHUNK, mask_bytes, stream>>>(a.idx, counts, off, list, a.T, a.S, p.n_blk, a.bs);
-  if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
-
+int launch_general(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) {
   using L = DqLayout<D>;
   auto kern = nsa_bwd_dq_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
@@ -664,22 +657,54 @@ int launch_bwd(const BwdArgs& a, uint8_t* ws, cudaStream_t stream) {
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, DQ_THREADS, L::BYTES) != cudaSuccess || per_sm < 1)
     return ERR_LAUNCH;
-  const long long nq = static_cast<long long>(bh) * a.T;
+  const long long nq = static_cast<long long>(a.B) * a.Hkv * a.T;
   const long long need = (nq + DQ_WARPS - 1) / DQ_WARPS, cap = static_cast<long long>(sms) * per_sm;
   kern<<<static_cast<unsigned>(std::min(need, cap)), DQ_THREADS, L::BYTES, stream>>>(
-      a.q, a.k, a.v, a.idx, a.out, a.lse, a.dout, a.dq, reinterpret_cast<float2*>(ws + p.stats_off), a.Hq / a.Hkv, a.T, a.S, a.bs, nq, 1.0f / sqrtf(static_cast<float>(D)));
+      a.q, a.k, a.v, a.idx, a.out, a.lse, a.dout, a.dq, w.stats, a.Hq / a.Hkv, a.T, a.S, a.bs, nq,
+      1.0f / sqrtf(static_cast<float>(D)));
+  if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
+  switch (a.bs) {
+    case 16: return launch_dkdv<D, 1>(a, w, stream);
+    case 32: return launch_dkdv<D, 2>(a, w, stream);
+    case 64: return launch_dkdv<D, 4>(a, w, stream);
+    case 128: return launch_dkdv<D, 8>(a, w, stream);
+    default: return ERR_UNSUPPORTED;
+  }
+}
+
+template <int D>
+int launch_bwd(const NsaBwdArgs& a, uint8_t* ws, cudaStream_t stream) {
+  const BwdPlan p = bwd_plan(a.B, a.Hq, a.Hkv, a.T, D, a.bs, a.S);
+  if (p.max_items > 0x7fffffffLL) return ERR_SHAPE;
+  int* counts = reinterpret_cast<int*>(ws + p.count_off);
+  int* total = reinterpret_cast<int*>(ws + p.total_off);
+  int* off = reinterpret_cast<int*>(ws + p.off_off);
+  int* ioff = reinterpret_cast<int*>(ws + p.ioff_off);
+  NsaBwdScratch w{};
+  w.stats = reinterpret_cast<float2*>(ws + p.stats_off);
+  w.list = reinterpret_cast<int*>(ws + p.list_off);
+  w.items = reinterpret_cast<int4*>(ws + p.item_off);
+  w.n_items = ioff + p.NB;
+  w.part = reinterpret_cast<float*>(ws + p.part_off);
+  w.rows = reinterpret_cast<__nv_bfloat16*>(ws + p.rows_off);
+  w.dq_part = reinterpret_cast<__half*>(ws + p.dqp_off);
+  w.dq_scale = reinterpret_cast<float*>(ws + p.dqs_off);
+  w.max_items = p.max_items;
+  const int bh = a.B * a.Hkv;
+
+  const dim3 grid(p.chunks, bh, (p.n_blk + BLK_TILE - 1) / BLK_TILE);
+  const size_t mask_bytes = static_cast<size_t>(std::min(p.n_blk, BLK_TILE)) * MASKS * sizeof(uint32_t);
+  bwd_mark_kernel<<<grid, QCHUNK, mask_bytes, stream>>>(a.idx, counts, a.T, a.S, p.n_blk, a.bs);
+  bwd_prefix_kernel<<<dim3((p.n_blk + 31) / 32, bh), dim3(32, 32), 0, stream>>>(counts, total, p.chunks, p.n_blk);
+  bwd_scan_kernel<<<1, SCAN_THREADS, 0, stream>>>(total, off, ioff, w.items, static_cast<int>(p.NB), p.item_queries);
+  bwd_fill_kernel<<<grid, QCHUNK, mask_bytes, stream>>>(a.idx, counts, off, w.list, a.T, a.S, p.n_blk, a.bs);
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
 
-  int st = ERR_UNSUPPORTED;
-  switch (a.bs) {
-    case 16: st = launch_dkdv<D, 1>(a, p, ws, stream); break;
-    case 32: st = launch_dkdv<D, 2>(a, p, ws, stream); break;
-    case 64: st = launch_dkdv<D, 4>(a, p, ws, stream); break;
-    case 128: st = launch_dkdv<D, 8>(a, p, ws, stream); break;
-  }
+  int st;
+  if constexpr (D == 64 || D == 128) st = tc_shape(D, a.bs) ? launch_nsa_bwd_tc(a, w, D, stream) : launch_general<D>(a, w, stream);
+  else st = launch_general<D>(a, w, stream);
   if (st != OK) return st;
-  bwd_join_kernel<<<dim3(static_cast<unsigned>(p.NB), 2), 256, 0, stream>>>(
-      reinterpret_cast<const float*>(ws + p.part_off), ioff, a.dk, a.dv, a.bs * D);
+  bwd_join_kernel<<<dim3(static_cast<unsigned>(p.NB), 2), 256, 0, stream>>>(w.part, ioff, a.dk, a.dv, a.bs * D);
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
@@ -692,7 +717,7 @@ size_t nsa_bwd_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int block_s
 int launch_nsa_bwd(const void* q, const void* k, const void* v, const int32_t* block_idx, const void* out,
                    const float* lse, const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int T,
                    int D, int block_size, int S, void* workspace, cudaStream_t stream) {
-  BwdArgs a{};
+  NsaBwdArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = static_cast<const __nv_bfloat16*>(k);
   a.v = static_cast<const __nv_bfloat16*>(v);

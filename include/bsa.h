@@ -473,7 +473,10 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
  * A row that selects nothing has dq = 0 and adds nothing to dk and dv; a key
  * that no row reads has dk = dv = 0.  p and dS are rounded to bf16 before the
  * products with dout, q and k; every sum is fp32, in an order that does not
- * vary: results repeat bit for bit.
+ * vary: results repeat bit for bit.  Blocks that no row selects and rows that
+ * select nothing may hold anything; a NaN or an infinity elsewhere may reach
+ * every result of the blocks and rows it is paired with, tokens that the
+ * causal mask hides inside a selected block included (as in the forward).
  *
  *   q, out, dout, dq   : [B, Hq, T, D] bf16 (out as the forward wrote it).
  *   k, v, dk, dv       : [B, Hkv, T, D] bf16.

@@ -43,7 +43,9 @@ def test_backward_refusals():
 def test_backward_workspace_size():
     size = bsa.nsa_select_backward_workspace_size
     assert size(1, 16, 1, 128, 128, 64, 4) % 256 == 0
-    assert size(2, 32, 2, 8192, 128, 64, 16) < 1 << 30
+    rows = 2 * 32 * 8192 * 16  # f16 dQ rows of 64-token blocks of 64 or 128 dims
+    assert rows * 256 < size(2, 32, 2, 8192, 128, 64, 16) < rows * 256 + (1 << 29)
+    assert size(2, 32, 2, 8192, 32, 64, 16) < 1 << 28
     assert size(1, 16, 1, 100, 128, 64, 4) == 0 and size(1, 16, 1, 128, 96, 64, 4) == 0
     assert size(70000, 1, 1, 16, 16, 16, 1) == 0  # (batch, kv head) pairs past a grid's second axis
     assert bwd(B=70000, Hq=1, T=16, D=16, bs=16, S=1) == 2
