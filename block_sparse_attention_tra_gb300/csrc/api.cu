@@ -97,6 +97,8 @@ int check_cache_shape(int B, int Hq, int Hkv, int D, int page_size, int max_page
     return BSA_ERR_SHAPE;
   if (static_cast<long long>(num_pages) * Hkv >= (1LL << 40) / (static_cast<long long>(page_size) * D))
     return BSA_ERR_SHAPE;
+  // (page, head) pairs of the pool are a tensor map's coordinate
+  if (static_cast<long long>(num_pages) * Hkv > 0x7fffffffLL) return BSA_ERR_SHAPE;
   if (D != 16 && D != 32 && D != 64 && D != 128) return BSA_ERR_UNSUPPORTED;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return BSA_ERR_UNSUPPORTED;
   if (Hq / Hkv > 16) return BSA_ERR_UNSUPPORTED;
@@ -127,6 +129,20 @@ int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1,
   const cuuint32_t box[3] = {box0, box1, box2};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? OK : ERR_SHAPE;
+}
+
+int encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                       uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1, uint32_t box2) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return ERR_DEVICE;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
+  const cuuint32_t box[3] = {box0, box1, box2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? OK : ERR_SHAPE;
@@ -537,9 +553,9 @@ int bsa_read_probe(const void* buf, size_t bytes, int reps, unsigned int* sink, 
 }
 
 int bsa_device_error(void) {
-  const unsigned codes[9] = {tra_bf16_device_error(), tra_f32_device_error(), nsa_device_error(),
+  const unsigned codes[10] = {tra_bf16_device_error(), tra_f32_device_error(), nsa_device_error(),
                              tra_bwd_device_error(), tra_diff_device_error(), nsa_fsa_device_error(),
-                             nsa_bwd_device_error(), nsa_bwd_tc_device_error(), selftest_device_error()};
+                             nsa_bwd_device_error(), nsa_bwd_tc_device_error(), nsa_decode_device_error(), selftest_device_error()};
   unsigned worst = 0;
   for (unsigned c : codes) {
     if (c == 0xffffffffu) return -1;

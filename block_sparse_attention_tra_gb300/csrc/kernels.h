@@ -27,6 +27,9 @@ enum Status : int {
 int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                    uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1,
                    uint32_t box2);
+// The same for bytes.
+int encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                      uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1, uint32_t box2);
 // Rank-2 fp32 tensor map (d0 innermost), 128-byte swizzle: used for TMA
 // stores of fp32 rows from shared memory.
 int encode_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t stride1_bytes,
@@ -173,6 +176,7 @@ unsigned int tra_diff_device_error();
 unsigned int nsa_fsa_device_error();
 unsigned int nsa_bwd_device_error();
 unsigned int nsa_bwd_tc_device_error();
+unsigned int nsa_decode_device_error();
 unsigned int selftest_device_error();
 
 // Power class of the TRA epilogue: p == 1, p == 2, or the general exp2/log2

@@ -222,8 +222,10 @@ def check_decode(got, lse, q, pool, lens, idx):
                                   None if idx is None else idx.cpu().numpy())
     x = got.double().cpu().numpy()
     n = max(1, max(lens))
-    # f16 probabilities; scores and sums in fp32 (numerator and denominator); subnormal probabilities; the result
-    bound = (1 + BF) * (2.0 ** -11 * sums["p"] + U * (sums["e"] + 2 * n * sums["p"]) + 2.0 ** -25 * sums["v"])
+    # f16 probabilities; scores and sums in fp32 (numerator and denominator); the result.  An f16 below 2^-14 is off by
+    # up to 2^-25; probabilities (largest 1) are rounded times their page's scale over a unit that is at most 2^3 of
+    # it, so that is 2^-22 of a probability of 1 (pages further off the unit are rounded on their own)
+    bound = (1 + BF) * (2.0 ** -11 * sums["p"] + U * (sums["e"] + 2 * n * sums["p"]) + 2.0 ** -22 * sums["v"])
     bound += BF * np.abs(out)
     assert np.isfinite(x).all()
     assert (np.abs(x - out) - bound).max() <= 1e-30, f"{(np.abs(x - out) - bound).max():.3e} over its bound"
