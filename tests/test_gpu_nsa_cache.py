@@ -303,6 +303,54 @@ def test_decode_selection_is_a_set():
     assert not out[1, 2:].any() and (lse[1, 2:] == -1.0e9).all()
 
 
+def many(B, page, longest, seed):
+    """Lengths of B sequences: empty ones, single tokens, whole pages and anything else."""
+    n = np.random.default_rng(seed).integers(0, longest + 1, B)
+    n[::7], n[3::11], n[5::13] = 0, 1, longest // page * page
+    return [int(x) for x in n]
+
+
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_decode_selected_pages_of_many_sequences(D, page):
+    run_decode(311, 3, 1, D, page, many(311, page, 6 * page, D), S=5, seed=D + page)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,S", [(400, 1, 1, 1), (170, 32, 2, 3), (77, 20, 4, 16), (310, 5, 1, 2), (21, 240, 15, 9)])
+def test_decode_selected_pages_of_many_heads(B, Hq, Hkv, S):
+    run_decode(B, Hq, Hkv, 64, 16, many(B, 16, 200, B), S=S, seed=S)
+
+
+@pytest.mark.parametrize("D,page,S", [(128, 64, 4), (32, 16, 32), (64, 128, 3), (16, 32, 7)])
+def test_decode_many_selections_with_repeats_and_dead_slots(D, page, S):
+    B, Hkv, pages = 320, 1, 40
+    r = np.random.default_rng(S)
+
+    def odd(idx):
+        a = r.integers(-2, pages // 2, (B, Hkv, 1, S)).astype(np.int32)  # -1, -2, repeats, blocks past the sequence
+        a[::5] = -1                                                      # nothing at all
+        a[1::9, :, :, 1:] = a[1::9, :, :, :1]                            # one page throughout
+        a[2::17, :, :, 0] = 2 ** 31 - 1
+        a[3::17, :, :, -1] = -2 ** 31
+        return torch.from_numpy(a).cuda()
+
+    run_decode(B, 4, Hkv, D, page, many(B, page, 8 * page + 5, S), S=S, seed=S, change=odd)
+
+
+def test_decode_many_sequences_with_garbage_and_bad_pages():
+    B, Hkv, D, page, last = 330, 1, 64, 32, 3
+    lens = [40 + b % 50 for b in range(B)]
+    pool = Pool(B, Hkv, D, page, last + 1, seed=7).clean()
+    for b, n in enumerate(lens):
+        for c in (pool.k, pool.v):
+            c[pool.table[b, n // page].item(), :, n % page:] = 0x7F  # NaN codes behind the last token
+            c[pool.table[b, last].item()] = 0x7F
+    pool.ks[pool.table[:, last].long()] = float("nan")
+    pool.table[::6, 0] = pool.pages
+    pool.table[1::6, 1] = -9
+    run_decode(B, 4, Hkv, D, page, lens, S=4, pool=pool, seed=8)
+
+
 def test_decode_garbage_behind_the_end_and_bad_pages():
     B, Hkv, D, page, lens = 2, 2, 64, 64, [70, 130]
     pool = Pool(B, Hkv, D, page, 4, seed=7).clean()
