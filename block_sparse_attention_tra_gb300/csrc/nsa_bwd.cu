@@ -15,16 +15,30 @@
 //   2. prefix  per block: where each 128 rows' share of its list starts
 //   3. scan    where each block's list starts; lists cut into work items
 //   4. fill    the lists: for each block the queries that select it, ascending
+// then, for 64-token blocks of 64 or 128 dims (nsa_bwd_tc.cu, on tcgen05),
+//   5. pack    Q and dO by query; (lse, delta) of every row
+//   6. tc      one work item at a time: a block's keys and values stay, its
+//              queries stream past; every slot's row of dq, the items' dk, dv
+//   7. dq sum  the slots' rows, in slot order
+// and for any other shape (mma.sync)
 //   5. dq      one query group at a time, gathering its blocks' keys and
 //              values; leaves (lse, delta) of its rows for 6
 //   6. dkdv    one work item at a time: a block's keys and values stay in
 //              registers, the items' query rows stream past
-//   7. join    blocks cut into several items: the items' sums, in order
+// and last, for blocks cut into several items,
+//   8. join    the items' sums, in order
 // The order of every sum is fixed (lists are ranked with bit masks, not with
 // atomic cursors), so results repeat bit for bit.
 //
 // dq and dkdv each form the scores: 14 instead of 10 D flops per pair, for no
-// atomic additions and no fp32 dq in memory.
+// atomic additions and no rows of dq in memory.  The tcgen05 pass forms them
+// once and writes a row of dq per slot: on one 4096-token sequence of 32 heads
+// of 128 the two general kernels took 980 us, pack, pass and sum take 352.
+//
+// Where the sizes are small every step is a few microseconds of latency (256
+// tokens of 8 heads of 32: 25 us of kernels in the 45 us that eight launches
+// and the call cost).  Mark and fill, four threads a row, take 3 and 5 us for
+// 4096 tokens of 16 slots (one a row: 3 and 12).
 #include <algorithm>
 
 #include "kernels.h"
@@ -38,6 +52,8 @@ namespace {
 
 constexpr int QCHUNK = 128;      // query rows of one mark / fill block
 constexpr int MASKS = QCHUNK / 32;
+constexpr int SLOT_PARTS = 4;    // threads of a row there, each with every fourth slot
+constexpr int LIST_THREADS = QCHUNK * SLOT_PARTS;
 constexpr int BLK_TILE = 2048;   // blocks whose masks a mark / fill block holds
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes = 16u) {
@@ -57,30 +73,33 @@ __device__ __forceinline__ void cp_async_wait() {
 // Bit q of mask[blk - blk0] for every row q of this block's 128 that selects
 // blk: the live rule of nsa_slots.cuh (a repeated block sets the same bit).
 __device__ __forceinline__ void mark_rows(uint32_t (*mask)[MASKS], const int32_t* __restrict__ block_idx, long long bh,
-                                          int i, int T, int S, int n_blk, int bs, int blk0, int nb) {
-  for (int e = threadIdx.x; e < nb * MASKS; e += QCHUNK) mask[e / MASKS][e % MASKS] = 0u;
+                                          int T, int S, int n_blk, int bs, int blk0, int nb) {
+  for (int e = threadIdx.x; e < nb * MASKS; e += LIST_THREADS) mask[e / MASKS][e % MASKS] = 0u;
   __syncthreads();
+  const int q = threadIdx.x / SLOT_PARTS, i = blockIdx.x * QCHUNK + q;
   if (i < T) {
     const int32_t* row = block_idx + (bh * T + i) * S;
-    for (int s = 0; s < S; ++s) {
+#pragma unroll 4
+    for (int s = threadIdx.x % SLOT_PARTS; s < S; s += SLOT_PARTS) {
       const int blk = row[s];
       if (blk >= blk0 && blk < blk0 + nb && blk < n_blk && blk * bs <= i)
-        atomicOr(&mask[blk - blk0][threadIdx.x >> 5], 1u << (threadIdx.x & 31));
+        atomicOr(&mask[blk - blk0][q >> 5], 1u << (q & 31));
     }
   }
   __syncthreads();
 }
 
 // grid (chunks of 128 rows, B * Hkv, tiles of blocks).  counts[bh][chunk][blk].
-__global__ void __launch_bounds__(QCHUNK) bwd_mark_kernel(const int32_t* __restrict__ block_idx,
-                                                          int* __restrict__ counts, int T, int S, int n_blk, int bs) {
+__global__ void __launch_bounds__(LIST_THREADS) bwd_mark_kernel(const int32_t* __restrict__ block_idx,
+                                                                int* __restrict__ counts, int T, int S, int n_blk,
+                                                                int bs) {
   extern __shared__ uint32_t mask_raw[];
   uint32_t(*mask)[MASKS] = reinterpret_cast<uint32_t(*)[MASKS]>(mask_raw);
   const int blk0 = blockIdx.z * BLK_TILE, nb = min(BLK_TILE, n_blk - blk0);
   const long long bh = blockIdx.y;
-  mark_rows(mask, block_idx, bh, blockIdx.x * QCHUNK + threadIdx.x, T, S, n_blk, bs, blk0, nb);
+  mark_rows(mask, block_idx, bh, T, S, n_blk, bs, blk0, nb);
   int* dst = counts + (bh * gridDim.x + blockIdx.x) * n_blk + blk0;
-  for (int e = threadIdx.x; e < nb; e += QCHUNK) {
+  for (int e = threadIdx.x; e < nb; e += LIST_THREADS) {
     int c = 0;
 #pragma unroll
     for (int w = 0; w < MASKS; ++w) c += __popc(mask[e][w]);
@@ -172,21 +191,22 @@ __global__ void __launch_bounds__(SCAN_THREADS) bwd_scan_kernel(const int* __res
 
 // grid as mark: query i goes to place (start of the block's list) + (queries
 // of earlier chunks) + (its rank in the chunk's mask).
-__global__ void __launch_bounds__(QCHUNK) bwd_fill_kernel(const int32_t* __restrict__ block_idx,
-                                                          const int* __restrict__ counts, const int* __restrict__ off,
-                                                          int* __restrict__ list, int T, int S, int n_blk, int bs) {
+__global__ void __launch_bounds__(LIST_THREADS) bwd_fill_kernel(const int32_t* __restrict__ block_idx,
+                                                                const int* __restrict__ counts,
+                                                                const int* __restrict__ off, int* __restrict__ list,
+                                                                int T, int S, int n_blk, int bs) {
   extern __shared__ uint32_t mask_raw[];
   uint32_t(*mask)[MASKS] = reinterpret_cast<uint32_t(*)[MASKS]>(mask_raw);
   const int blk0 = blockIdx.z * BLK_TILE, nb = min(BLK_TILE, n_blk - blk0);
   const long long bh = blockIdx.y;
-  const int i = blockIdx.x * QCHUNK + threadIdx.x;
-  mark_rows(mask, block_idx, bh, i, T, S, n_blk, bs, blk0, nb);
+  mark_rows(mask, block_idx, bh, T, S, n_blk, bs, blk0, nb);
+  const int q = threadIdx.x / SLOT_PARTS, i = blockIdx.x * QCHUNK + q;
   if (i >= T) return;
   const int32_t* row = block_idx + (bh * T + i) * S;
   const int* before = counts + (bh * gridDim.x + blockIdx.x) * n_blk;
-  const int w = threadIdx.x >> 5;
-  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
-  for (int s = 0; s < S; ++s) {
+  const int w = q >> 5;
+  const uint32_t below = (1u << (q & 31)) - 1u;
+  for (int s = threadIdx.x % SLOT_PARTS; s < S; s += SLOT_PARTS) {
     const int blk = row[s];
     if (blk < blk0 || blk >= blk0 + nb || blk >= n_blk || blk * bs > i) continue;
     bool again = false;  // a repeated block counts in its first slot
@@ -559,8 +579,10 @@ __global__ void __launch_bounds__(WARPS * 32)
   }
 }
 
-// grid (blocks, dk / dv): sums a block's items in order; zeros for a block
-// that no query selects.
+// grid (blocks, dk / dv, 1024 elements of the block): sums a block's items in
+// order; zeros for a block that no query selects.  A block that every query
+// selects has up to a hundred items: with one CTA for all of its elements the
+// join took 46 us where 4096 tokens share two kv heads.
 __global__ void __launch_bounds__(256) bwd_join_kernel(const float* __restrict__ part,
                                                        const int* __restrict__ item_off,
                                                        __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
@@ -570,8 +592,10 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const float* __restrict__
   // (blocks of all heads follow each other as their tokens do)
   __nv_bfloat16* dst = (blockIdx.y ? dv : dk) + static_cast<size_t>(blockIdx.x) * n;
   const float* src = part + (static_cast<size_t>(it0) * 2 + blockIdx.y) * n;
-  for (int e = threadIdx.x * 4; e < n; e += 1024) {
+  const int e = blockIdx.z * 1024 + threadIdx.x * 4;
+  if (e < n) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int x = 0; x < k; ++x) {
       const float4 y = *reinterpret_cast<const float4*>(src + static_cast<size_t>(x) * 2 * n + e);
       s.x += y.x;
@@ -694,17 +718,19 @@ int launch_bwd(const NsaBwdArgs& a, uint8_t* ws, cudaStream_t stream) {
 
   const dim3 grid(p.chunks, bh, (p.n_blk + BLK_TILE - 1) / BLK_TILE);
   const size_t mask_bytes = static_cast<size_t>(std::min(p.n_blk, BLK_TILE)) * MASKS * sizeof(uint32_t);
-  bwd_mark_kernel<<<grid, QCHUNK, mask_bytes, stream>>>(a.idx, counts, a.T, a.S, p.n_blk, a.bs);
+  bwd_mark_kernel<<<grid, LIST_THREADS, mask_bytes, stream>>>(a.idx, counts, a.T, a.S, p.n_blk, a.bs);
   bwd_prefix_kernel<<<dim3((p.n_blk + 31) / 32, bh), dim3(32, 32), 0, stream>>>(counts, total, p.chunks, p.n_blk);
   bwd_scan_kernel<<<1, SCAN_THREADS, 0, stream>>>(total, off, ioff, w.items, static_cast<int>(p.NB), p.item_queries);
-  bwd_fill_kernel<<<grid, QCHUNK, mask_bytes, stream>>>(a.idx, counts, off, w.list, a.T, a.S, p.n_blk, a.bs);
+  bwd_fill_kernel<<<grid, LIST_THREADS, mask_bytes, stream>>>(a.idx, counts, off, w.list, a.T, a.S, p.n_blk, a.bs);
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
 
   int st;
   if constexpr (D == 64 || D == 128) st = tc_shape(D, a.bs) ? launch_nsa_bwd_tc(a, w, D, stream) : launch_general<D>(a, w, stream);
   else st = launch_general<D>(a, w, stream);
   if (st != OK) return st;
-  bwd_join_kernel<<<dim3(static_cast<unsigned>(p.NB), 2), 256, 0, stream>>>(w.part, ioff, a.dk, a.dv, a.bs * D);
+  const int elements = a.bs * D;
+  bwd_join_kernel<<<dim3(static_cast<unsigned>(p.NB), 2, (elements + 1023) / 1024), 256, 0, stream>>>(
+      w.part, ioff, a.dk, a.dv, elements);
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 

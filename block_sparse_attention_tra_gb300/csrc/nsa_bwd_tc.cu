@@ -3,13 +3,14 @@
 //
 // Formulas as in nsa_bwd.cu.  One CTA per work item (a key block and a share
 // of the queries that select it); K and V of the block stay in shared memory,
-// the queries pass in tiles of 128 rows = 128 / G queries x G heads, gathered
-// by bulk copies (G = 8, 16: one of G rows per query and 64-column panel) or
-// by cp.async from rows that a first kernel has packed by query.  Per tile, all accumulators fp32 in TMEM:
-//     S  = Q K^T, dP = dO V^T                [128 rows x 64 keys]
+// the queries pass in tiles of 96 rows = 96 / G queries x G heads, gathered by
+// bulk copies (G = 8, 16: one of G rows per query and 64-column panel) or by
+// cp.async from rows that a first kernel has packed by query.  Per tile, all
+// accumulators fp32 in TMEM:
+//     S  = Q K^T, dP = dO V^T                [96 rows x 64 keys]
 //     P  = exp2(S c log2e - lse2), dS = c P (dP - delta)     (epilogue, bf16)
 //     dV^T += dO^T P, dK^T += Q^T dS         [D x 64 keys]
-//     dQ = dS K                              [128 rows x D]
+//     dQ = dS K                              [96 rows x D]
 // Every product has 128 rows of A this way (64 keys as M would run the tensor
 // cores at half rate): dV and dK are accumulated transposed, the dO and Q
 // tiles read MN-major as A, P and dS read MN-major as B and dS once more
@@ -25,15 +26,25 @@
 // order in which CTAs run.  Adding fp32 rows to dq in L2 instead would move
 // twice the bytes through the L2's atomic units and not repeat bit for bit.
 //
-// Within a row of the f16 partials the 16-byte chunks are permuted by the
-// row's head (chunk ^ (g & 7)): the drain threads, one a row, then write their
-// stage without bank conflicts, and the copies out stay contiguous.
+// The drain threads, one a row, store their rows straight from registers, 32
+// bytes (a whole sector) at a time: what a stage for them would take of the
+// shared memory is a second buffer of P and dS, without which a tile's
+// epilogue could not begin to store before the tile before's products ended.
 //
 // Tiles have 96 rows, not the 128 an MMA takes: what the stages of Q and dO
 // then leave of the shared memory is a third stage, and with two the gathers
 // (2 to 4 thousand cycles under load) stood in the way of every tile.  Two
 // warps issue MMAs, one the scores' and one the gradients', because issuing
 // one costs about what it takes to run.
+//
+// Bound by shared memory.  With 64 keys on the N side an MMA reads 6 KB of
+// operands for 32 cycles of arithmetic (48.5 measured; 65 for N = 128, which
+// is both bounds at once).  A tile of D = 128 reads 200 KB, the gather writes
+// 48 KB and the epilogue 24 KB: 2140 cycles at 128 bytes a cycle of the 2700
+// that it takes.  Two sequences of 8192 tokens, 32 query and 2 kv heads of 128,
+// 16 slots: 922 us, 0.68 PFLOP/s at the 10 D flops a (query, key) pair needs,
+// besides 103 us to pack (6.5 TB/s) and 357 us to sum dQ (6.4 TB/s).  With one
+// buffer of P and dS, and a stage for the dQ rows, the pass took 976 us.
 #include <algorithm>
 
 #include "kernels.h"
@@ -56,9 +67,6 @@ constexpr int tc_threads() {
 }
 constexpr int PANEL = ROWS * 128;   // 96 rows x 128 bytes
 constexpr int KV_PANEL = BS * 128;
-#ifndef BSA_TC_UNROLL
-#define BSA_TC_UNROLL 1
-#endif
 
 template <int D>
 struct TcLayout {
@@ -66,24 +74,22 @@ struct TcLayout {
   static constexpr int NS = D == 128 ? 3 : 5;    // stages of dO and Q
   static constexpr int TILE = NP * PANEL;        // 96 rows x D
   static constexpr int KV_TILE = NP * KV_PANEL;
-  static constexpr int K_OFF = 0, V_OFF = KV_TILE;
-  static constexpr int ST_OFF = 2 * KV_TILE;     // stages of dO, then Q
-  static constexpr int STAGE = 2 * TILE;
-  static constexpr int P_OFF = ST_OFF + NS * STAGE;  // P, then dS: 96 rows x 64 keys bf16
+  static constexpr int STAGE = 2 * TILE;         // dO, then Q
+  static constexpr int P_OFF = NS * STAGE;       // two buffers of P, then dS: 96 rows x 64 keys bf16
   static constexpr int DS_OFF = P_OFF + PANEL;
-  static constexpr int DQ_ROW = D * 2;           // bytes of an f16 row
-  static constexpr int DQ_OFF = DS_OFF + PANEL;  // 96 f16 rows
-  static constexpr int SUM_OFF = DQ_OFF + ROWS * DQ_ROW;  // float[2 tiles][2 halves][96]: sums of |dS|
+  static constexpr int PDS = 2 * PANEL;          // bytes of a buffer
+  static constexpr int K_OFF = P_OFF + 2 * PDS, V_OFF = K_OFF + KV_TILE;
+  static constexpr int SUM_OFF = V_OFF + KV_TILE;  // float[2 tiles][2 halves][96]: sums of |dS|
   static constexpr int KMAX_OFF = SUM_OFF + 4 * ROWS * 4;  // float[8]
   static constexpr int BAR_OFF = KMAX_OFF + 8 * 4;
-  // kv_full | pds_ready | pds_free | dq_full | dq_empty | acc_full | sp_full[2] | sum_full[2] |
+  // kv_full | dq_full | dq_empty | acc_full | pds_ready[2] | pds_free[2] | sp_full[2] | sum_full[2] | sum_free[2] |
   // sp_empty[2] | mma_done[2] | q_full[NS] | q_empty[NS] | do_full[NS] | do_empty[NS]
-  static constexpr int NBAR = 14 + 4 * NS;
+  static constexpr int NBAR = 18 + 4 * NS;
   static constexpr int TPTR_OFF = BAR_OFF + NBAR * 8;
   static constexpr int ALLOC = TPTR_OFF + 16 + 1024;
   static_assert(ALLOC <= 232448, "shared memory");
   // An MMA reads 128 rows of A: the 32 behind a tile's last lie in what follows it, and their results are not read.
-  static_assert(DS_OFF + 128 * 128 <= ALLOC - 1024 && P_OFF + PANEL <= ALLOC - 1024, "rows behind the last tile");
+  static_assert(128 * 128 - PANEL <= PDS && 128 * 128 - PANEL <= 2 * KV_TILE, "rows behind the last tile");
   // TMEM columns: S[2], dP[2], dV^T, dK^T, dQ
   static constexpr uint32_t TS = 0, TP = 128, TV = 256, TK = 320, TQ = 384;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -110,15 +116,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
-// Shared -> global copy of `bytes` (a multiple of 16, both sides 16-byte aligned), bulk-group completion.  The lines are
-// the first to leave L2: the f16 rows are read once, by a later kernel, while the packed rows are read S times.
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .b64 pol;\n\t"
-      "createpolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
-      "cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, pol;\n\t}" ::"l"(dst),
-      "r"(src), "r"(bytes)
-      : "memory");
+// 32 bytes of an f16 row.  The lines are the first to leave L2: the rows are
+// read once, by a later kernel, while the packed rows are read S times.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // The MMA issuer's operands as the low words of 128-byte-swizzle descriptors
@@ -159,10 +162,10 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
-  uint64_t *kv_full = bars, *pds_ready = bars + 1, *pds_free = bars + 2, *dq_full = bars + 3, *dq_empty = bars + 4,
-           *acc_full = bars + 5, *sp_full = bars + 6, *sum_full = bars + 8, *sp_empty = bars + 10,
-           *mma_done = bars + 12, *q_full = bars + 14, *q_empty = q_full + L::NS, *do_full = q_empty + L::NS,
-           *do_empty = do_full + L::NS;
+  uint64_t *kv_full = bars, *dq_full = bars + 1, *dq_empty = bars + 2, *acc_full = bars + 3, *pds_ready = bars + 4,
+           *pds_free = bars + 6, *sp_full = bars + 8, *sum_full = bars + 10, *sum_free = bars + 12,
+           *sp_empty = bars + 14, *mma_done = bars + 16, *q_full = bars + 18, *q_empty = q_full + L::NS,
+           *do_full = q_empty + L::NS, *do_empty = do_full + L::NS;
   uint32_t* tptr = reinterpret_cast<uint32_t*>(smem + L::TPTR_OFF);
   float* sums = reinterpret_cast<float*>(smem + L::SUM_OFF);
   float* km = reinterpret_cast<float*>(smem + L::KMAX_OFF);
@@ -185,10 +188,11 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
       mbar_init(&sp_full[x], 1);
       mbar_init(&mma_done[x], 1);
       mbar_init(&sum_full[x], 2 * GROUP);
+      mbar_init(&sum_free[x], GROUP);
       mbar_init(&sp_empty[x], 2 * GROUP);
+      mbar_init(&pds_ready[x], 2 * GROUP);
+      mbar_init(&pds_free[x], 1);
     }
-    mbar_init(pds_ready, 2 * GROUP);
-    mbar_init(pds_free, 1);
     mbar_init(dq_full, 1);
     mbar_init(dq_empty, GROUP);
     mbar_init(acc_full, 1);
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
           // rows of the tile that takes this stage next: on their way to L2 while the stage is in use
           if (lane < qpt && (t + L::NS) * qpt + lane < npairs)
             bulk_prefetch(rows + query_of((t + L::NS) * qpt + lane) * (2 * G * D), 4 * G * D);
-          uint8_t* st = smem + L::ST_OFF + x * L::STAGE + lane * G * 128;
+          uint8_t* st = smem + x * L::STAGE + lane * G * 128;
           const uint32_t par = ((t / L::NS) & 1) ^ 1;
           if (lane == 0 && (ok = mbar_wait(&q_empty[x], par))) mbar_arrive_expect_tx(&q_full[x], L::TILE);
           if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
         const uint32_t par = ((t / L::NS) & 1) ^ 1;
         const uint32_t run = next;
         next = run_of(t + 1);  // (its list entry is on its way while this tile is copied)
-        const uint32_t st = smem_u32(smem + L::ST_OFF + x * L::STAGE);
+        const uint32_t st = smem_u32(smem + x * L::STAGE);
         // (bounded waits: on a failure nothing new is issued, and all copies issued land below)
         if (!mbar_wait(&q_empty[x], par) || !mbar_wait(&do_empty[x], par)) break;
         __syncwarp();
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
     constexpr uint32_t ID_S = idesc_bf16_f32(128, BS, 0, 0);
     const uint32_t tm = uniform(tmem), base = uniform(smem_u32(smem));
     const uint32_t kK = desc_lo(base + L::K_OFF, 16), kV = desc_lo(base + L::V_OFF, 16);
-    const uint32_t kDO = desc_lo(base + L::ST_OFF, 16);
+    const uint32_t kDO = desc_lo(base, 16);
     bool ok = mbar_wait(kv_full, 0);
     for (int t = 0; t < nt && ok; ++t) {
       const int x = t % L::NS, b = t & 1;  // stage, TMEM buffer
@@ -373,15 +377,17 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
     const uint32_t tm = uniform(tmem), base = uniform(smem_u32(smem));
     // MN-major operands (a step of 16 rows is 2048 bytes), and dS K-major
     const uint32_t mK = desc_lo(base + L::K_OFF, L::NP > 1 ? KV_PANEL : 1024);
-    const uint32_t mP = desc_lo(base + L::P_OFF, D == 128 ? 1024 : PANEL);
-    const uint32_t mDS = desc_lo(base + L::DS_OFF, 1024), kDS = desc_lo(base + L::DS_OFF, 16);
-    const uint32_t mDO = desc_lo(base + L::ST_OFF, PANEL);
+    constexpr uint32_t PDS16 = L::PDS >> 4;
+    const uint32_t m0 = desc_lo(base + L::P_OFF, D == 128 ? 1024 : PANEL);
+    const uint32_t m1 = desc_lo(base + L::DS_OFF, 1024), k1 = desc_lo(base + L::DS_OFF, 16);
+    const uint32_t mDO = desc_lo(base, PANEL);
     bool ok = mbar_wait(kv_full, 0);
     for (int t = 0; t < nt && ok; ++t) {
       const int x = t % L::NS;
       const uint32_t aDO = uniform(mDO + x * STAGE16), aQ = uniform(mDO + x * STAGE16 + TILE16);
       const uint32_t more = uniform(t > 0 ? 1u : 0u);
-      if (!(ok = mbar_wait(pds_ready, t & 1))) break;
+      const uint32_t buf = (t & 1) * PDS16, mP = uniform(m0 + buf), mDS = uniform(m1 + buf), kDS = uniform(k1 + buf);
+      if (!(ok = mbar_wait(&pds_ready[t & 1], (t >> 1) & 1))) break;
       tc_fence_after();
       __syncwarp();
       if (leader) {
@@ -411,7 +417,7 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
         for (int kk = 0; kk < BS / 16; ++kk)
           mma_lo(tm + L::TQ, kDS + kk * 2, mK + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
         mma_commit(dq_full);
-        mma_commit(pds_free);
+        mma_commit(&pds_free[t & 1]);
       }
       __syncwarp();
     }
@@ -425,11 +431,7 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
     const int r = threadIdx.x - DRAIN_WARP * 32;
     const uint32_t tQ = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::TQ;
     const int qi = r / G, g = r % G;
-    const uint32_t row = smem_u32(smem + L::DQ_OFF) + r * L::DQ_ROW;
-    const bool by_query = 32 % G == 0;  // a query's rows lie in one warp: one copy for them all
-    const uint32_t bytes = by_query ? G * L::DQ_ROW : L::DQ_ROW;
     Pair next = pair_of(qi < qpt ? qi : npairs);
-    bool sent = false;
     float kmax = 0.0f;
     for (int t = 0; t < nt; ++t) {
       const Pair p = next;
@@ -441,19 +443,20 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
         for (int j = 0; j < GROUP; ++j) kmax = fmaxf(kmax, fmaxf(km[j], km[4 + j]));
       const float* sm = sums + (t & 1) * 2 * ROWS + r;
       const float bound = (sm[0] + sm[ROWS]) * kmax * 1.01f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sum_free[t & 1]);
       const int ex = static_cast<int>(__float_as_uint(bound) >> 23) - 127;
       const int e = bound > 0.0f && ex < 128 ? min(14 - ex, 126) : 0;
       const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      if (p.valid)
-        dq_scale[((static_cast<size_t>(bg) * T + p.i) * S + p.s) * G + g] =
-            __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const size_t to = ((static_cast<size_t>(bg) * T + p.i) * S + p.s) * G + g;
+      if (p.valid) dq_scale[to] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      __half* row = dq_part + to * D;
       if (!mbar_wait(dq_full, t & 1)) break;
       tc_fence_after();
-      if (sent) bulk_wait_read<0>();  // the row's last copy has left the stage
-      __syncwarp();
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
+        __syncwarp();
         tmem_ld32(tQ + c * 32, v);
         tmem_wait_ld();
         if (c == D / 32 - 1) {
@@ -461,27 +464,17 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(dq_empty);
         }
+        if (p.valid)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t w[4];
+          for (int x = 0; x < 2; ++x) {
+            uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_f16x2(__uint_as_float(v[8 * x + 2 * e]) * f, __uint_as_float(v[8 * x + 2 * e + 1]) * f);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + (((4 * c + x) ^ (g & 7)) << 4)), "r"(w[0]),
-                       "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (p.valid && (!by_query || g == 0)) {
-        bulk_store(dq_part + ((static_cast<size_t>(bg) * T + p.i) * S + p.s) * G * D + (by_query ? 0 : g * D), row,
-                   bytes);
-        bulk_commit();
-        sent = true;
+            for (int e = 0; e < 8; ++e)
+              w[e] = pack_f16x2(__uint_as_float(v[16 * x + 2 * e]) * f, __uint_as_float(v[16 * x + 2 * e + 1]) * f);
+            store32(row + 32 * c + 16 * x, w);
+          }
       }
     }
-    if (sent) bulk_wait_all();  // never leave the CTA while a copy still reads its stage
   } else {  // warps 0..2, 4..6
     // ---- epilogue half w: keys 32w .. 32w + 31; thread = row of the tile
     const int w = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -539,21 +532,23 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
         pk[c] = pack_bf16x2(pp[0], pp[1]);
         dk2[c] = pack_bf16x2(dd[0], dd[1]);
       }
-      // the previous tile's products have read P and dS (and its drain the sums of the tile before)
-      if (t > 0 && !(ok = mbar_wait(pds_free, (t - 1) & 1))) break;
+      // the products of the tile before the last have read this buffer, and its drain the sums
+      const uint32_t past = ((t >> 1) - 1) & 1;
+      if (t >= 2 && !(ok = mbar_wait(&pds_free[t & 1], past) && mbar_wait(&sum_free[t & 1], past))) break;
+      uint8_t* pds = smem + L::P_OFF + (t & 1) * L::PDS;
       sums[((t & 1) * 2 + w) * ROWS + r] = sum;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const uint32_t off = r * 128 + (((4 * w + x) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(smem + L::P_OFF + off) =
+        *reinterpret_cast<uint4*>(pds + off) =
             make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
-        *reinterpret_cast<uint4*>(smem + L::DS_OFF + off) =
+        *reinterpret_cast<uint4*>(pds + PANEL + off) =
             make_uint4(dk2[4 * x], dk2[4 * x + 1], dk2[4 * x + 2], dk2[4 * x + 3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(pds_ready);
+        mbar_arrive(&pds_ready[t & 1]);
         mbar_arrive(&sum_full[t & 1]);
       }
     }
@@ -660,7 +655,7 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
   const bool in = row < n_rows;
   const int g = static_cast<int>(row % G);
   const long long query = in ? row / G : 0;
-  const __half* src = dq_part + (query * S * G + g) * D + ((c ^ (g & 7)) << 3);
+  const __half* src = dq_part + (query * S * G + g) * D + (c << 3);
   const float* sc = dq_scale + query * S * G + g;
   float o[8];
 #pragma unroll
