@@ -8,12 +8,8 @@
 //     lse = ln sum_t exp(s_t)          (no token: out 0, lse -1e9),
 // c the codes' values, exact in f16, so no key or value is rounded on the way.
 //
-// Bound by the cache's bytes.  A warp takes chunks of C = 32 tokens of a page
-// (16 where pages hold 16); its lanes bring the chunk's codes by cp.async into
-// their own places of a ring in shared memory -- each lane copies exactly what
-// it will read itself, so the ring needs no barrier and has no bank conflicts,
-// and serves as several chunks' worth of registers -- in the order that
-// mma.sync.m16n8k16 wants:
+// The arithmetic, per warp and 16 or 32 tokens, by mma.sync.m16n8k16 (16 query
+// rows fill one M tile; a tcgen05 tile would be 7/8 padding):
 //  - scores: D is summed over, so its order is free: lane (g, t) takes the
 //    bytes of token row g that lie in its own share of the row, and the query
 //    fragments are gathered in that order once.
@@ -23,17 +19,39 @@
 // The query rows (heads of the group, 16 with zero rows behind the last) go to
 // f16 under a power-of-two factor of their own that brings their largest
 // element near 2^14: exact for what is not 2^-28 of it.  Probabilities are
-// rounded to f16 (2^-11); each chunk's product is taken on its own and added
-// in fp32 under its page's scale.
+// rounded to f16 (2^-11): their products with the codes then are exact in the
+// tensor cores, and the error is an eighth of the final bf16 rounding.
 //
-// Selected pages: the slots of a (sequence, kv head) are shared out over a
-// cluster of 1, 2, 4 or 8 blocks, which joins its blocks' (max, sum,
-// accumulator) through distributed shared memory: one launch.  Every page: the
-// list of (sequence, kv head, page) in that order is cut into equal contiguous
-// ranges, one a block, so that ragged lengths cost nothing; a block writes the
-// (sequence, kv head) pairs that it covers whole, and of the ones it starts or
-// ends in the middle of leaves (max, sum, accumulator) in the workspace, which
-// a second kernel joins in order.
+// Two kernels.
+//
+// Selected pages: one block a (sequence, kv head) pair, or with few pairs a
+// cluster of 2, 4 or 8 that shares out its slots and joins the blocks' (max,
+// sum, accumulator) through distributed shared memory: one launch.  A warp
+// takes chunks of 32 tokens of a page (16 where pages hold 16); its lanes
+// bring the chunk's codes by cp.async into their own places of a ring in
+// shared memory -- each lane copies what it will read itself, so the ring
+// needs no barrier and has no bank conflicts.  One sequence, 16 pages of 64
+// tokens, 32 query and 2 kv heads of 128: 6.2 us, the latency of a chain of
+// loads (slots, table, codes).  128 sequences of 64 query and 4 kv heads: 134
+// MB in 39.4 us, of which every further block on a SM costs 7 us (6.3 TB/s)
+// and the first 13: what bounds it is that chain and the second, half empty
+// wave of 512 blocks.  (Cutting the pairs into equal ranges for the kernel
+// below took 46.5 us, and two to three times as long on smaller heads.)
+//
+// Every page: persistent blocks, a producer warp that brings stages of 128
+// tokens by TMA and eight consumer warps with 16 tokens of a stage each.  The
+// list of (sequence, kv head, stage) in that order is cut into equal
+// contiguous ranges, one a block, so that ragged lengths cost nothing; a block
+// writes the pairs that it covers whole, and of the ones it starts or ends in
+// the middle of leaves (max, sum, accumulator) in the workspace, which a
+// second kernel joins in order.  Bound by the cache's bytes on paper: four
+// sequences of up to 131072 tokens are 155 MB, 43 us (3.6 TB/s; the first
+// kernel alone 39.5).  What holds it
+// there is the consumers' latency: a slice of 16 tokens is 1450 cycles of
+// load, product, maximum, exponential, product, and the registers of eight
+// warps (168 each) leave two a scheduler to hide it (issue slots 31% busy).
+// Slices of 32 tokens on two teams of warps, and score sums split over two
+// accumulators, were no faster.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -45,7 +63,6 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int CTAS = 2;     // blocks of a SM (cluster kernel)
 constexpr int STAGE_TOK = 128;  // tokens of a stage (stream kernel)
 constexpr int ROWS = 16;    // heads of a group, padded
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
@@ -66,7 +83,11 @@ struct DecodeArgs {
 
 template <int D, int C>
 struct Dec {
-  static constexpr int RING = 96 / C;  // chunks of a warp in flight or in use
+  // Blocks of a SM, and the tokens that a warp's ring holds.  D = 128: the accumulators (64 registers), query fragments
+  // (32) and scores leave two blocks, three chunks of 32 tokens a warp; at D = 64 four blocks of two chunks take 27.8
+  // us where three of three take 32.2 (256 sequences, 4 kv heads, 16 pages of 64).
+  static constexpr int CTAS = D == 128 ? 2 : 4;
+  static constexpr int RING = (D == 128 ? 96 : 64) / C;  // chunks of a warp in flight or in use
   static constexpr int KC = D / 4 < 16 ? D / 4 : 16;  // bytes of one piece of a key row
   static constexpr int KN = D / 4 / KC;               // such pieces of a lane
   static constexpr int VB = D / 8;                    // bytes of a lane's run of a value row
@@ -152,11 +173,6 @@ __device__ __forceinline__ int tokens_of(const DecodeArgs& a, int b) {
 }
 __device__ __forceinline__ int stages_of(const DecodeArgs& a, int b) {
   return (tokens_of(a, b) + STAGE_TOK - 1) / STAGE_TOK;
-}
-
-// Stages of a selection with every slot live.
-__device__ __forceinline__ int selected_stages(const DecodeArgs& a) {
-  return (a.S * a.page + STAGE_TOK - 1) / STAGE_TOK;
 }
 
 // The units (a stage of one kv head) before sequence `upto`; a block-wide call,
@@ -521,9 +537,8 @@ struct StreamLayout {
 // Byte `off` of a tile of 128-byte lines that TMA wrote with 128-byte swizzle (1024-byte aligned).
 __device__ __forceinline__ uint32_t swz128(uint32_t off) { return off ^ ((off >> 3) & 0x70u); }
 
-// Persistent blocks, each on one contiguous range of the (sequence, kv head, stage) list.  a.block_idx null: stage k
-// holds tokens 128 k .. of the sequence.  Otherwise it holds tokens 128 k .. of the live slots' pages, one behind
-// another, and every pair is counted with the stages of S live slots.
+// Persistent blocks, each on one contiguous range of the (sequence, kv head, stage) list; stage k holds tokens 128 k ..
+// of the sequence.
 template <int D>
 __global__ void __launch_bounds__(STREAM_THREADS, 1)
     nsa_decode_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -677,100 +692,44 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
       return {id, a.k_scale[at], a.v_scale[at]};
     };
 
-    if (a.block_idx != nullptr) {
-      // A pair's pages take a chain of loads (slots, table, scales): each link is issued a pair ahead, while this
-      // pair's stages are put up.
-      const int n_items = a.B * a.Hkv;
-      auto slots_of = [&](int item) {
-        return item < n_items && lane < a.S ? __ldg(a.block_idx + static_cast<size_t>(item) * a.S + lane) : -1;
-      };
-      struct Pages {
-        int n_live, tok, id;  // live slots; this lane's page of them: first token, pool page
-      };
-      auto pages_of = [&](int item, int blk_lane) -> Pages {
-        if (item >= n_items) return {0, 0, -1};
-        const int b = item / a.Hkv, len = tokens_of(a, b);
-        const SlotRow sel = nsa_live_slots_of(blk_lane, len - 1, (len + a.page - 1) / a.page, a.page);
-        // lane l takes the l-th live slot's page
-        const int n_live = __popc(sel.live);
-        unsigned rest = sel.live;
-        int from = 0;
-        for (int k = 0; k < n_live; ++k, rest &= rest - 1)
-          if (k == lane) from = __ffs(rest) - 1;
-        const int blk = __shfl_sync(0xffffffffu, sel.blk_lane, from);
-        return {n_live, blk << page_log,
-                lane < n_live ? a.table[static_cast<size_t>(b) * a.max_pages + blk] : -1};
-      };
-      const int per = selected_stages(a);
-      const long long units = static_cast<long long>(n_items) * per;
-      const long long u0 = range_start(units, blockIdx.x, a.ranges), u1 = range_start(units, blockIdx.x + 1, a.ranges);
-      if (u0 < u1) {
-        int item = static_cast<int>(u0 / per), s0 = static_cast<int>(u0 % per);
-        Pages cur = pages_of(item, slots_of(item));
-        Page pg = scales_of(cur.id, item % a.Hkv);
-        int ahead = slots_of(item + 1);
-        QRows q = load_q(item / a.Hkv, item % a.Hkv);
-        for (long long u = u0; u < u1 && ok; ++item) {
-          const int s1 = static_cast<int>(min(static_cast<long long>(per), s0 + (u1 - u)));
-          const int b = item / a.Hkv, h = item % a.Hkv;
-          open_window(pg.id, cur.tok, pg.ks, pg.vs);
-          const Pages next = pages_of(item + 1, ahead);
-          ahead = slots_of(item + 2);
-          const SegmentHead sg{b, h, tokens_of(a, b), 2 * static_cast<int>(blockIdx.x) + (u != u0 ? 1 : 0)};
-          const int whole = s0 == 0 && s1 == per ? SEG_WHOLE : 0;
-          // the stages that live slots fill; none of them here: one without tokens, which makes the segment known
-          const int filled = (cur.n_live * a.page + STAGE_TOK - 1) / STAGE_TOK;
-          const int end = max(s0 + 1, min(s1, filled)), half = (s0 + end) / 2;
-          open_segment(sg, q);
-          put_all(sg, whole, s0, end, s0, half, 0, cur.n_live);
-          pg = scales_of(next.id, (item + 1) % a.Hkv);
-          if (item + 1 < n_items) q = load_q((item + 1) / a.Hkv, (item + 1) % a.Hkv);
-          put_all(sg, whole, s0, end, half, end, 0, cur.n_live);
-          cur = next;
-          u += s1 - s0;
-          s0 = 0;
+    const long long units = units_of_warp(a);
+    const long long u0 = range_start(units, blockIdx.x, a.ranges), u1 = range_start(units, blockIdx.x + 1, a.ranges);
+    if (u0 < u1) {
+      long long before;
+      int b = sequence_of(a, u0, &before);
+      int n_st = stages_of(a, b);
+      int h = static_cast<int>((u0 - before) / n_st), s0 = static_cast<int>((u0 - before) % n_st);
+      QRows q = load_q(b, h);
+      for (long long u = u0; u < u1 && ok;) {
+        const int s1 = static_cast<int>(min(static_cast<long long>(n_st), s0 + (u1 - u)));
+        const int len = tokens_of(a, b), n_pages = (len + a.page - 1) >> page_log;
+        const int whole = s0 == 0 && s1 == n_st ? SEG_WHOLE : 0;
+        const SegmentHead sg{b, h, len, 2 * static_cast<int>(blockIdx.x) + (u != u0 ? 1 : 0)};
+        // The window in use, the next one with its scales, and the pool pages of the one behind that: no stage
+        // waits for a chain of loads.
+        const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
+        auto pool_page = [&](int w0) { return w0 + lane < n_pages ? row[w0 + lane] : -1; };
+        int w0 = s0 * STAGE_TOK >> page_log;  // first page of the window
+        Page next = scales_of(pool_page(w0), h);
+        int behind = pool_page(w0 + 32);
+        open_segment(sg, q);
+        for (int s = s0; s < s1 && ok;) {
+          open_window(next.id, (w0 + lane) << page_log, next.ks, next.vs);
+          next = scales_of(behind, h);
+          behind = pool_page(w0 + 64);
+          const int end = min(s1, ((w0 + 32) << page_log) / STAGE_TOK);  // stages of this window
+          put_all(sg, whole, s0, s1, s, end, w0 << page_log, 32);
+          s = end;
+          w0 += 32;
         }
-      }
-    } else {
-      const long long units = units_of_warp(a);
-      const long long u0 = range_start(units, blockIdx.x, a.ranges), u1 = range_start(units, blockIdx.x + 1, a.ranges);
-      if (u0 < u1) {
-        long long before;
-        int b = sequence_of(a, u0, &before);
-        int n_st = stages_of(a, b);
-        int h = static_cast<int>((u0 - before) / n_st), s0 = static_cast<int>((u0 - before) % n_st);
-        QRows q = load_q(b, h);
-        for (long long u = u0; u < u1 && ok;) {
-          const int s1 = static_cast<int>(min(static_cast<long long>(n_st), s0 + (u1 - u)));
-          const int len = tokens_of(a, b), n_pages = (len + a.page - 1) >> page_log;
-          const int whole = s0 == 0 && s1 == n_st ? SEG_WHOLE : 0;
-          const SegmentHead sg{b, h, len, 2 * static_cast<int>(blockIdx.x) + (u != u0 ? 1 : 0)};
-          // The window in use, the next one with its scales, and the pool pages of the one behind that: no stage
-          // waits for a chain of loads.
-          const int32_t* row = a.table + static_cast<size_t>(b) * a.max_pages;
-          auto pool_page = [&](int w0) { return w0 + lane < n_pages ? row[w0 + lane] : -1; };
-          int w0 = s0 * STAGE_TOK >> page_log;  // first page of the window
-          Page next = scales_of(pool_page(w0), h);
-          int behind = pool_page(w0 + 32);
-          open_segment(sg, q);
-          for (int s = s0; s < s1 && ok;) {
-            open_window(next.id, (w0 + lane) << page_log, next.ks, next.vs);
-            next = scales_of(behind, h);
-            behind = pool_page(w0 + 64);
-            const int end = min(s1, ((w0 + 32) << page_log) / STAGE_TOK);  // stages of this window
-            put_all(sg, whole, s0, s1, s, end, w0 << page_log, 32);
-            s = end;
-            w0 += 32;
-          }
-          u += s1 - s0;
-          s0 = 0;
-          if (u < u1 && ++h == a.Hkv) {
-            h = 0;
-            do n_st = stages_of(a, ++b);
-            while (n_st == 0);
-          }
-          if (u < u1) q = load_q(b, h);
+        u += s1 - s0;
+        s0 = 0;
+        if (u < u1 && ++h == a.Hkv) {
+          h = 0;
+          do n_st = stages_of(a, ++b);
+          while (n_st == 0);
         }
+        if (u < u1) q = load_q(b, h);
       }
     }
     if (lane == 0) {
@@ -1024,7 +983,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
 
 // Selected pages: a cluster for each (sequence, kv head), its slots shared out over the cluster's blocks.
 template <int D, int C>
-__global__ void __launch_bounds__(THREADS, CTAS) nsa_decode_select_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(THREADS, (Dec<D, C>::CTAS)) nsa_decode_select_kernel(const DecodeArgs a) {
   using L = Dec<D, C>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float ml[WARPS][ROWS][2];
@@ -1079,9 +1038,11 @@ __global__ void __launch_bounds__(THREADS, CTAS) nsa_decode_select_kernel(const 
 }
 
 // Joins the parts of a (sequence, kv head) that several ranges cover, and
-// answers for a sequence without tokens.  One block for four rows of it, four
-// warps a row: each takes every fourth part, and the four are joined last.
-constexpr int JOIN_ROWS = 4, JOIN_WARPS = 4, JOIN_THREADS = JOIN_ROWS * JOIN_WARPS * 32;
+// answers for a sequence without tokens.  One block for two rows of it, eight
+// warps a row: each takes every eighth part, and the eight are joined last (a
+// pair of long sequences has tens of parts: with four warps a row four
+// sequences of up to 131072 tokens took 44.1 us, with one 48.9, now 43.2).
+constexpr int JOIN_ROWS = 2, JOIN_WARPS = 8, JOIN_THREADS = JOIN_ROWS * JOIN_WARPS * 32;
 template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS) nsa_decode_join_kernel(const DecodeArgs a) {
   constexpr int V = D / 32 > 0 ? D / 32 : 1, LANES = D / V;  // dims of a lane, lanes of a row
@@ -1090,31 +1051,17 @@ __global__ void __launch_bounds__(JOIN_THREADS) nsa_decode_join_kernel(const Dec
   __shared__ float2 state[JOIN_ROWS][JOIN_WARPS];
   __shared__ float rows[JOIN_ROWS][JOIN_WARPS][D];
   const int groups = (a.G + JOIN_ROWS - 1) / JOIN_ROWS;
-  int item = blockIdx.x / groups;
-  if (a.block_idx != nullptr) {
-    // Selected pages: where the ranges end is known, so the blocks stand for the ends, and one that cuts no pair, or
-    // is not its pair's first, has nothing to do.
-    const int per = selected_stages(a), c = item + 1;
-    const long long units = static_cast<long long>(a.B) * a.Hkv * per, cut = range_start(units, c, a.ranges);
-    item = static_cast<int>(cut / per);
-    if (cut % per == 0 || range_start(units, c - 1, a.ranges) > static_cast<long long>(item) * per) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      return;
-    }
-  }
+  const int item = blockIdx.x / groups;
   const int b = item / a.Hkv, h = item % a.Hkv;
-  const int np = a.block_idx != nullptr ? selected_stages(a) : stages_of(a, b);
+  const int np = stages_of(a, b);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp / JOIN_WARPS, w4 = warp % JOIN_WARPS, row = blockIdx.x % groups * JOIN_ROWS + sub;
   float M = -INFINITY, sum = 0.0f, o[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) o[e] = 0.0f;
   if (np > 0) {
-    const bool sel = a.block_idx != nullptr;
-    const long long units = sel ? static_cast<long long>(a.B) * a.Hkv * np : units_before(a, a.B, scratch);
-    const long long u0 = sel ? static_cast<long long>(item) * np
-                             : units_before(a, b, scratch) + static_cast<long long>(h) * np;
-    const long long u1 = u0 + np;
+    const long long units = units_before(a, a.B, scratch);
+    const long long u0 = units_before(a, b, scratch) + static_cast<long long>(h) * np, u1 = u0 + np;
     if (threadIdx.x < 2) ends[threadIdx.x] = range_of(units, threadIdx.x ? u1 - 1 : u0, a.ranges);
     __syncthreads();
     const int c0 = ends[0], c1 = ends[1];
@@ -1200,9 +1147,11 @@ template <int D, int C>
 int launch_cluster(const DecodeArgs& a, cudaStream_t stream) {
   using L = Dec<D, C>;
   const long long items = static_cast<long long>(a.B) * a.Hkv;
-  // Blocks of a cluster: enough that the SMs have twice their blocks, of whole slots.
+  // Blocks of a cluster: as many, of whole slots, as leave each a SM.  More share the SMs without a gain (32 sequences
+  // of 4 kv heads and 16 pages of 64 tokens: one block a pair 13.4 us, two 15.4, eight 29.7); fewer leave some idle
+  // (one sequence of 2 kv heads: eight blocks 6.2 us, one 12.7).
   int cs = 1;
-  while (cs < 8 && 2 * cs <= a.S && items * cs < 2LL * CTAS * sm_count()) cs *= 2;
+  while (cs < 8 && 2 * cs <= a.S && 2 * items * cs <= sm_count()) cs *= 2;
   auto kern = nsa_decode_select_kernel<D, C>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
     return ERR_LAUNCH;
@@ -1232,8 +1181,7 @@ int launch_stream(DecodeArgs a, cudaStream_t stream) {
   int st = encode_tmap_3d_u8(&mk, a.k, 128, lines, heads, 128, lines * 128, 128, static_cast<uint32_t>(lines), 1);
   if (st == OK) st = encode_tmap_3d_u8(&mv, a.v, 128, lines, heads, 128, lines * 128, 128, static_cast<uint32_t>(lines), 1);
   if (st != OK) return st;
-  const long long pages = a.block_idx != nullptr ? a.S : a.max_pages;
-  const long long units = items * ((pages * a.page + STAGE_TOK - 1) / STAGE_TOK);
+  const long long units = items * ((static_cast<long long>(a.max_pages) * a.page + STAGE_TOK - 1) / STAGE_TOK);
   const long long most = sms < DECODE_MAX_RANGES ? sms : DECODE_MAX_RANGES;
   a.ranges = static_cast<int>(units < most ? units : most);
   if (cudaFuncSetAttribute(nsa_decode_stream_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) !=
@@ -1242,10 +1190,8 @@ int launch_stream(DecodeArgs a, cudaStream_t stream) {
   nsa_decode_stream_kernel<D><<<static_cast<unsigned>(a.ranges), STREAM_THREADS, L::BYTES, stream>>>(mk, mv, a);
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
   // started while the first kernel's last blocks run (its blocks wait before they read a part)
-  const long long joins =
-      (a.block_idx != nullptr ? a.ranges - 1 : items) * static_cast<long long>((a.G + JOIN_ROWS - 1) / JOIN_ROWS);
+  const long long joins = items * ((a.G + JOIN_ROWS - 1) / JOIN_ROWS);
   if (joins > 0x7fffffffLL) return ERR_SHAPE;
-  if (joins == 0) return OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(joins));
   cfg.blockDim = dim3(JOIN_THREADS);
@@ -1260,8 +1206,7 @@ int launch_stream(DecodeArgs a, cudaStream_t stream) {
 
 template <int D>
 int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
-  if (a.block_idx == nullptr || static_cast<long long>(a.B) * a.Hkv >= 2LL * sm_count())
-    return launch_stream<D>(a, stream);
+  if (a.block_idx == nullptr) return launch_stream<D>(a, stream);
   // chunks of 32 tokens (half the work for masks, maxima and scales per token) where a page holds them
   return a.page >= 32 ? launch_cluster<D, 32>(a, stream) : launch_cluster<D, 16>(a, stream);
 }

@@ -22,18 +22,13 @@ struct SlotRow {
   int blk_lane;
 };
 
-// The same from the slot values: `blk` is this lane's, -1 for lanes >= S.
-__device__ __forceinline__ SlotRow nsa_live_slots_of(int blk, int i, int n_blk, int bs) {
+__device__ __forceinline__ SlotRow nsa_live_slots(const int32_t* __restrict__ sel, int S, int i, int n_blk, int bs) {
   const int lane = static_cast<int>(threadIdx.x & 31u);
+  const int blk = lane < S ? __ldg(sel + lane) : -1;
   const bool causal = blk >= 0 && blk < n_blk && blk * bs <= i;
   const uint32_t same = __match_any_sync(0xffffffffu, blk);          // lanes holding the same value
   const bool first = (same & ((1u << lane) - 1u)) == 0u;             // no earlier slot holds it
   return {__ballot_sync(0xffffffffu, causal && first), blk};
-}
-
-__device__ __forceinline__ SlotRow nsa_live_slots(const int32_t* __restrict__ sel, int S, int i, int n_blk, int bs) {
-  const int lane = static_cast<int>(threadIdx.x & 31u);
-  return nsa_live_slots_of(lane < S ? __ldg(sel + lane) : -1, i, n_blk, bs);
 }
 
 // Block held by slot s of a row (every lane of the warp calls it).
