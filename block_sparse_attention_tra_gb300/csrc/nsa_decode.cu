@@ -31,12 +31,13 @@
 // bring the chunk's codes by cp.async into their own places of a ring in
 // shared memory -- each lane copies what it will read itself, so the ring
 // needs no barrier and has no bank conflicts.  One sequence, 16 pages of 64
-// tokens, 32 query and 2 kv heads of 128: 6.2 us, the latency of a chain of
+// tokens, 32 query and 2 kv heads of 128: 6.5 us, the latency of a chain of
 // loads (slots, table, codes).  128 sequences of 64 query and 4 kv heads: 134
-// MB in 39.4 us, of which every further block on a SM costs 7 us (6.3 TB/s)
-// and the first 13: what bounds it is that chain and the second, half empty
-// wave of 512 blocks.  (Cutting the pairs into equal ranges for the kernel
-// below took 46.5 us, and two to three times as long on smaller heads.)
+// MB in 39.5 us (3.4 TB/s); what keeps it from the cache's bytes is that chain
+// at the start of each block and the second, two thirds full wave of 512
+// blocks.  (Cutting the pairs into equal ranges for the kernel below took 46.6
+// us, and up to two and a half times as long on smaller heads, as it joins
+// warps and blocks once a pair.)
 //
 // Every page: persistent blocks, a producer warp that brings stages of 128
 // tokens by TMA and eight consumer warps with 16 tokens of a stage each.  The
@@ -45,13 +46,12 @@
 // writes the pairs that it covers whole, and of the ones it starts or ends in
 // the middle of leaves (max, sum, accumulator) in the workspace, which a
 // second kernel joins in order.  Bound by the cache's bytes on paper: four
-// sequences of up to 131072 tokens are 155 MB, 43 us (3.6 TB/s; the first
-// kernel alone 39.5).  What holds it
-// there is the consumers' latency: a slice of 16 tokens is 1450 cycles of
-// load, product, maximum, exponential, product, and the registers of eight
-// warps (168 each) leave two a scheduler to hide it (issue slots 31% busy).
-// Slices of 32 tokens on two teams of warps, and score sums split over two
-// accumulators, were no faster.
+// sequences of up to 131072 tokens are 155 MB, 42.4 us (3.7 TB/s; the first
+// kernel alone 39.5).  What holds it there is the consumers' latency: a slice
+// of 16 tokens is 1450 cycles of load, product, maximum, exponential, product,
+// and the registers of eight warps (168 each) leave two a scheduler to hide it
+// (issue slots 31% busy).  Slices of 32 tokens on two teams of warps, and score
+// sums split over two accumulators, were no faster.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -85,7 +85,7 @@ template <int D, int C>
 struct Dec {
   // Blocks of a SM, and the tokens that a warp's ring holds.  D = 128: the accumulators (64 registers), query fragments
   // (32) and scores leave two blocks, three chunks of 32 tokens a warp; at D = 64 four blocks of two chunks take 27.8
-  // us where three of three take 32.2 (256 sequences, 4 kv heads, 16 pages of 64).
+  // us where three of three take 32.2 (256 sequences, 4 kv heads, 16 pages of 64, codes in L2).
   static constexpr int CTAS = D == 128 ? 2 : 4;
   static constexpr int RING = (D == 128 ? 96 : 64) / C;  // chunks of a warp in flight or in use
   static constexpr int KC = D / 4 < 16 ? D / 4 : 16;  // bytes of one piece of a key row
@@ -1147,9 +1147,9 @@ template <int D, int C>
 int launch_cluster(const DecodeArgs& a, cudaStream_t stream) {
   using L = Dec<D, C>;
   const long long items = static_cast<long long>(a.B) * a.Hkv;
-  // Blocks of a cluster: as many, of whole slots, as leave each a SM.  More share the SMs without a gain (32 sequences
-  // of 4 kv heads and 16 pages of 64 tokens: one block a pair 13.4 us, two 15.4, eight 29.7); fewer leave some idle
-  // (one sequence of 2 kv heads: eight blocks 6.2 us, one 12.7).
+  // Blocks of a cluster: as many, of whole slots, as leave each a SM.  More share the SMs without a gain (24 sequences
+  // of 4 kv heads and 16 pages of 64 tokens, with cold caches: one block a pair 18.8 us, two 22.5, four 27.9); fewer
+  // leave some idle (one sequence of 2 kv heads: eight blocks 12.3 us, one 18.4; of each, 5 us are the timing's).
   int cs = 1;
   while (cs < 8 && 2 * cs <= a.S && 2 * items * cs <= sm_count()) cs *= 2;
   auto kern = nsa_decode_select_kernel<D, C>;
