@@ -24,14 +24,13 @@
 // its tokens are rotated into registers, their maximum reduced over the block,
 // then written as codes: each input is read once, each code written once.
 // Further blocks rotate the queries, each thread keeping the sines of its row
-// over eight heads: with four, 128 tokens take 14.4 us in place of 12.2; with
-// sixteen a prompt takes 205 us in place of 210, four chunks of 512 tokens
-// 12.8 in place of 9.8.  A thread holds two units of 16 values: with four, at
-// half the warps a SM, the prompt took 276 us.
+// over eight heads: with sixteen a prompt takes 205 us in place of 209, four
+// chunks of 1031 fp32 tokens 12.8 in place of 9.5.  A thread holds two units
+// of 16 values: with four, at half the warps a SM, the prompt took 276 us.
 //
-// Bound by memory for long prompts: 32768 tokens of 64 query and 8 kv heads of
-// 128 in bf16 are 1174 MB, 210 us (5.6 TB/s); by the latency of one round trip
-// through load, reduction and store for single tokens (5 us).
+// Bound by memory for long prompts: 32768 tokens of 64 query and 4 kv heads of
+// 128 in bf16 are 1174 MB, 209 us (5.6 TB/s); for single tokens by the latency
+// of one trip through load, reduction and store (4.4 us; 128 sequences 6.1).
 #include <cuda_fp8.h>
 
 #include "kernels.h"
@@ -231,10 +230,19 @@ __device__ void append_kv(const AppendArgs& a, const uint64_t* turns, float* red
     s = exp2i(scale_exponent(amax));
     if (threadIdx.x == 0) *scale = s;
     const float f = old / s;  // the codes already held move to the larger scale
-    for (int e = threadIdx.x; e < r0 * (a.D / 16); e += blockDim.x) {
-      uint4* p = reinterpret_cast<uint4*>(dst) + e;
-      const uint4 u = *p;
-      *p = make_uint4(recode4(u.x, f), recode4(u.y, f), recode4(u.z, f), recode4(u.w, f));
+    uint4* p = reinterpret_cast<uint4*>(dst);
+    const int held16 = r0 * (a.D / 16);
+    constexpr int AHEAD = 2;  // loads in flight
+    for (int e0 = threadIdx.x; e0 < held16; e0 += AHEAD * blockDim.x) {
+      uint4 u[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (e0 + i * static_cast<int>(blockDim.x) < held16) u[i] = p[e0 + i * blockDim.x];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (e0 + i * static_cast<int>(blockDim.x) < held16)
+          p[e0 + i * blockDim.x] =
+              make_uint4(recode4(u[i].x, f), recode4(u[i].y, f), recode4(u[i].z, f), recode4(u[i].w, f));
     }
   }
   const float inv = 1.0f / s;
@@ -314,8 +322,11 @@ int launch_nsa_cache_append(const void* k, const void* v, const void* q, void* q
   const long long seq_pages = (static_cast<long long>(n) + page - 2) / page + 1;
   a.seq_pages = static_cast<int>(seq_pages < max_pages ? seq_pages : max_pages);
   a.kv_blocks = 2LL * B * a.seq_pages * Hkv;
-  int threads = page * D / (UNIT * KV_UNITS);
-  threads = threads < 64 ? 64 : threads > MAX_THREADS ? MAX_THREADS : threads;
+  // threads for the tokens that a page takes at most: single tokens need a warp (128 of them 6.2 us, with a thread for
+  // every unit of a page 11.9)
+  const int few = n < page ? n : page;
+  int threads = (few * D / (UNIT * KV_UNITS) + 31) / 32 * 32;
+  threads = threads < 32 ? 32 : threads > MAX_THREADS ? MAX_THREADS : threads;
   const int upr = D / UNIT;
   a.q_rows = threads / upr < n ? threads / upr : n;
   a.q_chunks = (n + a.q_rows - 1) / a.q_rows;

@@ -1179,7 +1179,8 @@ int launch_stream(DecodeArgs a, cudaStream_t stream) {
   CUtensorMap mk, mv;
   const uint64_t lines = static_cast<uint64_t>(a.page) * D / 128, heads = static_cast<uint64_t>(a.num_pages) * a.Hkv;
   int st = encode_tmap_3d_u8(&mk, a.k, 128, lines, heads, 128, lines * 128, 128, static_cast<uint32_t>(lines), 1);
-  if (st == OK) st = encode_tmap_3d_u8(&mv, a.v, 128, lines, heads, 128, lines * 128, 128, static_cast<uint32_t>(lines), 1);
+  if (st == OK)
+    st = encode_tmap_3d_u8(&mv, a.v, 128, lines, heads, 128, lines * 128, 128, static_cast<uint32_t>(lines), 1);
   if (st != OK) return st;
   const long long units = items * ((static_cast<long long>(a.max_pages) * a.page + STAGE_TOK - 1) / STAGE_TOK);
   const long long most = sms < DECODE_MAX_RANGES ? sms : DECODE_MAX_RANGES;
