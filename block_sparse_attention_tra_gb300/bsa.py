@@ -685,11 +685,16 @@ def _check_cache(torch, what, k_cache, v_cache, k_scale, v_scale, page_table, ca
     """Shapes and types of the paged cache; returns (num_pages, page_size, max_pages)."""
     if k_cache.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != B or cache_lens.shape != (B,):
         raise BsaError(f"{what}: k_cache [pages,Hkv,page_size,D], page_table [B,max_pages], cache_lens [B] expected", 2)
-    pages, _, page_size, _ = k_cache.shape
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _in_place(what, name, t, (pages, Hkv, page_size, D), torch.float8_e4m3fn, torch.uint8)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _in_place(what, name, t, (pages, Hkv), torch.float32)
+    pages, _, page_size, _ = shape = k_cache.shape
+    if not (shape[1] == Hkv and shape[3] == D and v_cache.shape == shape and k_scale.shape == (pages, Hkv)
+            and v_scale.shape == k_scale.shape and k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+            and v_cache.dtype in (torch.uint8, torch.float8_e4m3fn) and k_scale.dtype is torch.float32
+            and v_scale.dtype is torch.float32 and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous()):  # (all of it at once: half the time)
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            _in_place(what, name, t, (pages, Hkv, page_size, D), torch.float8_e4m3fn, torch.uint8)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _in_place(what, name, t, (pages, Hkv), torch.float32)
     return pages, page_size, page_table.shape[1]
 
 

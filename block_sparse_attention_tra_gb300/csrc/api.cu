@@ -465,7 +465,7 @@ int nsa_cache_append(const void* k, const void* v, const void* q, void* q_out, v
 
 size_t nsa_select_decode_workspace_size(int B, int Hq, int Hkv, int D, int page_size, int max_pages, int S) {
   if (S < 0 || S > 32 || check_cache_shape(B, Hq, Hkv, D, page_size, max_pages, 1) != BSA_OK) return 0;
-  return nsa_decode_workspace_bytes(D);
+  return nsa_decode_workspace_bytes(D, S);
 }
 
 int nsa_select_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

@@ -151,7 +151,7 @@ int launch_nsa_cache_append(const void* k, const void* v, const void* q, void* q
 // bytes, 16-byte aligned: the partial results of at most DECODE_MAX_RANGES
 // ranges of the work list.
 constexpr int DECODE_MAX_RANGES = 512;
-size_t nsa_decode_workspace_bytes(int D);
+size_t nsa_decode_workspace_bytes(int D, int S);
 int launch_nsa_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                       const float* v_scale, const int32_t* table, const int32_t* lens, const int32_t* block_idx,
                       void* out, float* lse, int B, int Hq, int Hkv, int D, int page, int max_pages, int num_pages,

@@ -1214,9 +1214,9 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// The partials of the most ranges (the size does not depend on the device).
-size_t nsa_decode_workspace_bytes(int D) {
-  return 2 * static_cast<size_t>(DECODE_MAX_RANGES) * part_floats(D) * sizeof(float);
+// The partials of the most ranges (the size does not depend on the device); selected pages leave none.
+size_t nsa_decode_workspace_bytes(int D, int S) {
+  return S > 0 ? 256 : 2 * static_cast<size_t>(DECODE_MAX_RANGES) * part_floats(D) * sizeof(float);
 }
 
 int launch_nsa_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
