@@ -677,8 +677,15 @@ def _nsa_function():
 def nsa_select_attention(q, k, v, block_idx, block_size: int = 64):
     """NSA selection-branch attention with autograd: ``nsa_select_forward``
     whose gradients with respect to q, k and v come from
-    ``nsa_select_backward`` (arguments as for ``nsa_select_forward``)."""
-    return _nsa_function().apply(q, k, v, block_idx, block_size)
+    ``nsa_select_backward`` (arguments as for ``nsa_select_forward``).  Runs on
+    the current stream of the tensors' device, whichever device is current.  To
+    capture a training step into a CUDA graph, capture forward and backward
+    together, with no graph of the same leaves left from outside the capture.
+    """
+    import torch
+
+    with torch.cuda.device(_one_device("nsa_select_attention", q, k, v, block_idx)):
+        return _nsa_function().apply(q, k, v, block_idx, block_size)
 
 
 def _check_cache(torch, what, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, B, Hkv, D):

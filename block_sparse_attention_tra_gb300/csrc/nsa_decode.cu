@@ -1191,8 +1191,7 @@ int launch_stream(DecodeArgs a, cudaStream_t stream) {
   nsa_decode_stream_kernel<D><<<static_cast<unsigned>(a.ranges), STREAM_THREADS, L::BYTES, stream>>>(mk, mv, a);
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
   // started while the first kernel's last blocks run (its blocks wait before they read a part)
-  const long long joins = items * ((a.G + JOIN_ROWS - 1) / JOIN_ROWS);
-  if (joins > 0x7fffffffLL) return ERR_SHAPE;
+  const long long joins = items * ((a.G + JOIN_ROWS - 1) / JOIN_ROWS);  // (no more than B * Hq)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(joins));
   cfg.blockDim = dim3(JOIN_THREADS);

@@ -9,8 +9,10 @@
  *
  * plus the TRA backward, the differential TRA, the NSA selection forward
  * in the page's block-outer split-K form (nsa_select_forward_fsa, which works
- * in a caller-provided workspace) and tra_forward_host, which takes host
- * buffers and streams them through the GPU.
+ * in a caller-provided workspace) and its gradients (nsa_select_backward, in a
+ * workspace too), tra_forward_host, which takes host buffers and streams them
+ * through the GPU, and for serving a paged e4m3 cache: nsa_cache_append writes
+ * new tokens into it, nsa_select_decode attends to it with one query token.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -462,7 +464,8 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
  *
  * The page "nsa_selection_kernel.py" defines the operation; this differentiates
  * it.  With c = D^-0.5, row i's set J of nsa_select_forward, and that call's
- * out and lse:
+ * out and lse (block_size 64 with D 64 or 128 runs on tcgen05, the other
+ * shapes of the forward on mma.sync kernels):
  *
  *   p_ij  = exp(c q_i . k_j - lse_i)            (recomputed; nothing is stored)
  *   dS_ij = c p_ij (dout_i . v_j - dout_i . out_i)
@@ -473,7 +476,10 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
  * A row that selects nothing has dq = 0 and adds nothing to dk and dv; a key
  * that no row reads has dk = dv = 0.  p and dS are rounded to bf16 before the
  * products with dout, q and k; every sum is fp32, in an order that does not
- * vary: results repeat bit for bit.  Blocks that no row selects and rows that
+ * vary: results repeat bit for bit.  (The tcgen05 pass keeps each block's row
+ * of dq as f16 under a power-of-two factor of its own, 2^-11 of an element,
+ * until the blocks are summed: workspace of B * Hq * T * S * (2 D + 4) bytes
+ * and B * Hq * T * 4 D for q and dout packed by query.)  Blocks that no row selects and rows that
  * select nothing may hold anything; a NaN or an infinity elsewhere may reach
  * every result of the blocks and rows it is paired with, tokens that the
  * causal mask hides inside a selected block included (as in the forward).
@@ -491,9 +497,9 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
  *
  * Errors: as for nsa_select_forward, plus BSA_ERR_NULLPTR for any NULL
  * pointer, BSA_ERR_ALIGN for a misaligned workspace, BSA_ERR_SCRATCH_LIMIT for
- * one that is too small, and BSA_ERR_SHAPE for B * Hkv * T * S >= 2^31 or
- * B * Hkv > 65535 (for which the size function returns 0, as for any sizes
- * that are not accepted).
+ * one that is too small, and BSA_ERR_SHAPE for B * Hkv * T * S >= 2^31,
+ * T >= 2^26 or B * Hkv > 65535 (for which the size function returns 0, as for
+ * any sizes that are not accepted).
  */
 BSA_API size_t nsa_select_backward_workspace_size(int B, int Hq, int Hkv,
                                                   int T, int D, int block_size,
@@ -556,8 +562,9 @@ BSA_API int nsa_select_backward(const void* q, const void* k, const void* v,
  *   inv_freq   : [rotary_dim / 2] fp32, finite; may be NULL if rotary_dim is 0.
  *   rotary_dim : a multiple of 16 from 0 (no rotation) to D.
  *   dtype      : BSA_BF16 or BSA_F32.
- *   Tokens past max_pages * page_size are left out.  No two sequences may
- *   write the same pool page in one call.
+ *   Tokens past max_pages * page_size are left out.  No pool page may be
+ *   written through two entries of page_table in one call, and cache_lens[b] +
+ *   n <= 2^31 - 1.
  *
  * cache_lens is not advanced: add the new tokens before the next call and
  * before the decode, which takes lengths that include the query's own token.
@@ -600,7 +607,8 @@ BSA_API int nsa_cache_append(const void* k, const void* v, const void* q,
  *   cache_lens : [B] int32; 0 (or less) is an empty sequence, and lengths past
  *                max_pages * page_size count as that.
  *   workspace  : caller-owned device memory of at least
- *                nsa_select_decode_workspace_size(...) bytes, 16-byte aligned;
+ *                nsa_select_decode_workspace_size(...) bytes (256 where pages
+ *                are selected), 16-byte aligned;
  *                overwritten, in use until the work on `stream` completes (one
  *                workspace per concurrent call).
  *

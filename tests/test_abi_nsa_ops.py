@@ -106,6 +106,8 @@ def test_binding_has_no_cpu_path():
     with pytest.raises(BsaError, match="no CPU path"):
         bsa.nsa_select_backward(x, x, x, i, x, torch.zeros(1, 1, 64), x)
     with pytest.raises(BsaError, match="no CPU path"):
+        bsa.nsa_select_attention(x, x, x, i, 64)
+    with pytest.raises(BsaError, match="no CPU path"):
         bsa.nsa_cache_append(x, x, c, c, s, s, t, n)
     with pytest.raises(BsaError, match="no CPU path"):
         bsa.nsa_select_decode(x[:, :, :1], c, c, s, s, t, n)

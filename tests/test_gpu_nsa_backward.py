@@ -209,3 +209,33 @@ def test_autograd_with_a_broadcast_key_head():
     o, lse = bsa.nsa_select_forward(q, k[:, :1].expand(-1, 2, -1, -1).contiguous(), v, idx, bs, return_lse=True)
     _, dk, _ = bsa.nsa_select_backward(q, k[:, :1].expand(-1, 2, -1, -1), v, idx, o, lse, dout, bs)
     assert torch.equal(k1.grad, dk.sum(1, keepdim=True))
+
+
+@pytest.mark.parametrize("D,bs", [(64, 64), (32, 32)])
+def test_a_captured_training_step_and_an_eager_one_on_another_stream(D, bs):
+    """Forward and backward replayed from a graph on new inputs while other calls run beside it."""
+    shape = (1, 8, 2, 512, D)
+    batches = [inputs(*shape, bs, 4, seed=s) for s in (31, 32)]
+    other = inputs(*shape, bs, 4, seed=33)
+
+    def step(q, k, v, idx, do):
+        leaves = [t.detach().requires_grad_() for t in (q, k, v)]
+        return torch.autograd.grad(bsa.nsa_select_attention(*leaves, idx, bs), leaves, do)
+
+    want = [step(*b) for b in batches]
+    beside = step(*other)
+    static = [t.clone() for t in batches[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grads = step(*static)
+    side = torch.cuda.Stream()
+    for b, w in zip(batches, want):
+        for s, t in zip(static, b):
+            s.copy_(t)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            again = step(*other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(grads, w))
+        assert all(torch.equal(x, y) for x, y in zip(again, beside))
