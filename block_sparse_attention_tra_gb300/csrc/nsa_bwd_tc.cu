@@ -59,11 +59,18 @@ constexpr int BS = 64;     // tokens per block
 constexpr int ROWS = 96;   // rows per tile (queries x heads) of the 128 that an MMA takes
 constexpr int GROUP = ROWS / 32;    // warps of one epilogue half, and of the drain
 // Warps 0-2 and 4-6 epilogue (left and right 32 keys), 8-10 drain (warp w reads TMEM lanes 32 (w & 3) ..), 7 issues the
-// scores' MMAs, 12 the gradients'; 3 gathers by bulk copies, or 3, 11 and 13 by cp.async, 32 rows each.
-constexpr int PROD_WARP = 3, MMA_WARP = 7, DRAIN_WARP = 8, PROD2_WARP = 11, GRAD_WARP = 12, PROD3_WARP = 13;
-template <bool TMA_IN>
+// scores' MMAs, 11 or 12 the gradients'; 3 gathers by bulk copies, or 3, the other of 11 and 12, and 13 by cp.async, 32
+// rows each.  At D = 64 the gradients' MMAs are issued from the scheduler that has no epilogue warp (2 x 4096 tokens,
+// 32 heads in groups of 16: 497 us for the call in place of 511); at D = 128, where an MMA stands longer in the queue
+// than it takes to issue, that scheduler is left to the gather and the scores (1416 us in place of 1428).
+constexpr int PROD_WARP = 3, MMA_WARP = 7, DRAIN_WARP = 8, PROD3_WARP = 13, WARPS = 14;
+template <int D>
+constexpr int GRAD_WARP = D == 64 ? 11 : 12;
+template <int D>
+constexpr int PROD2_WARP = 23 - GRAD_WARP<D>;
+template <int D, bool TMA_IN>
 constexpr int tc_threads() {
-  return (TMA_IN ? GRAD_WARP + 1 : PROD3_WARP + 1) * 32;
+  return (TMA_IN ? GRAD_WARP<D> + 1 : WARPS) * 32;
 }
 constexpr int PANEL = ROWS * 128;   // 96 rows x 128 bytes
 constexpr int KV_PANEL = BS * 128;
@@ -71,7 +78,7 @@ constexpr int KV_PANEL = BS * 128;
 template <int D>
 struct TcLayout {
   static constexpr int NP = D / 64;
-  static constexpr int NS = D == 128 ? 3 : 5;    // stages of dO and Q
+  static constexpr int NS = D == 128 ? 3 : 6;    // stages of dO and Q
   static constexpr int TILE = NP * PANEL;        // 96 rows x D
   static constexpr int KV_TILE = NP * KV_PANEL;
   static constexpr int STAGE = 2 * TILE;         // dO, then Q
@@ -150,7 +157,7 @@ struct Pair {
 };
 
 template <int D, bool TMA_IN>
-__global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
+__global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
     nsa_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __nv_bfloat16* __restrict__ rows, const float2* __restrict__ stats,
                       const int* __restrict__ list, const int4* __restrict__ items,
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
     return {debug_index(e >> 5, 0, T), e & 31, true};
   };
 
-  if (warp == PROD_WARP || warp == PROD2_WARP || warp == PROD3_WARP) {
+  if (warp == PROD_WARP || warp == PROD2_WARP<D> || warp == PROD3_WARP) {
     if constexpr (TMA_IN) {
       if (warp == PROD_WARP) {
         // Lane l copies query l of the tile: per panel G rows (G = 8, 16: whole
@@ -265,8 +272,7 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
     } else {
       // Lane l resolves row 32 x + l of the tile (x: which gathering warp); rows are copied by 8 consecutive lanes
       // to a panel, so that a warp instruction reads whole runs of 128 bytes.
-      constexpr int DEFER = L::NS - 2;  // tiles whose copies stay in flight
-      const int row0 = warp == PROD_WARP ? 0 : warp == PROD2_WARP ? 32 : 64;
+      const int row0 = warp == PROD_WARP ? 0 : warp == PROD2_WARP<D> ? 32 : 64;
       const int rr = row0 + lane, rq = rr / G < qpt ? rr / G : -1, rg = rr % G;
       const uint32_t panels = 2 * L::NP * G;  // 128-byte runs of a query
       auto run_of = [&](int t) -> uint32_t {  // first run of this lane's row of tile t; all ones: no row
@@ -278,7 +284,6 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
       uint32_t keys = 0u;
 #pragma unroll
       for (int k = 0; k < 8; ++k) keys |= static_cast<uint32_t>(((row0 + 4 * k + (lane >> 3)) % G) & 7) << (3 * k);
-      int issued = 0;
       uint32_t next = run_of(0);
       for (int t = 0; t < nt; ++t) {
         const int x = t % L::NS;
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
         const uint32_t run = next;
         next = run_of(t + 1);  // (its list entry is on its way while this tile is copied)
         const uint32_t st = smem_u32(smem + x * L::STAGE);
-        // (bounded waits: on a failure nothing new is issued, and all copies issued land below)
+        // (bounded waits: on a failure nothing new is issued, and every copy issued has landed)
         if (!mbar_wait(&q_empty[x], par) || !mbar_wait(&do_empty[x], par)) break;
         __syncwarp();
 #pragma unroll
@@ -304,22 +309,13 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
           }
         }
         cp_async_commit();
-        issued = t + 1;
-        if (t >= DEFER) {  // tile t - DEFER has landed; those behind it may be in flight
-          const int y = (t - DEFER) % L::NS;
-          cp_async_wait<DEFER>();
-          fence_proxy_async_smem();
-          mbar_arrive(&q_full[y]);
-          mbar_arrive(&do_full[y]);
-        }
-      }
-      cp_async_wait<0>();  // never leave a copy landing in a finished CTA
-      if (issued == nt) {
+        // A tile is announced before the next is issued: behind that it would wait for the next one's stage, and so for
+        // the products of a tile before it (one more in flight: 4096 tokens of 16 heads of 64 in groups of four 2%
+        // longer, all but two of the stages 8%).
+        cp_async_wait<0>();
         fence_proxy_async_smem();
-        for (int t = nt > DEFER ? nt - DEFER : 0; t < nt; ++t) {
-          mbar_arrive(&q_full[t % L::NS]);
-          mbar_arrive(&do_full[t % L::NS]);
-        }
+        mbar_arrive(&q_full[x]);
+        mbar_arrive(&do_full[x]);
       }
     }
   } else if (warp == MMA_WARP) {
@@ -369,7 +365,7 @@ __global__ void __launch_bounds__(tc_threads<TMA_IN>(), 1)
       mma_commit(&mma_done[0]);
       mbar_wait(&mma_done[0], 0);
     }
-  } else if (warp == GRAD_WARP) {
+  } else if (warp == GRAD_WARP<D>) {
     // (the scores of a tile are complete before its gradients' inputs are: what this warp commits frees the stage)
     const bool leader = lane == 0;
     constexpr uint32_t ID_ACC = idesc_bf16_f32(128, D == 128 ? BS : 2 * BS, 1, 1);
@@ -725,7 +721,7 @@ int launch_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) 
   auto kern = bulk ? nsa_bwd_tc_kernel<D, true> : nsa_bwd_tc_kernel<D, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC) != cudaSuccess)
     return ERR_LAUNCH;
-  kern<<<static_cast<unsigned>(w.max_items), bulk ? tc_threads<true>() : tc_threads<false>(), L::ALLOC, stream>>>(
+  kern<<<static_cast<unsigned>(w.max_items), bulk ? tc_threads<D, true>() : tc_threads<D, false>(), L::ALLOC, stream>>>(
       mk, mv, w.rows, w.stats, w.list, w.items, w.n_items, w.part, w.dq_part, w.dq_scale, a.dk, a.dv, G, a.T, a.S,
       n_blk, static_cast<int>(bh), 1.0f / sqrtf(static_cast<float>(D)));
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
