@@ -629,10 +629,12 @@ BwdPlan bwd_plan(int B, int Hq, int Hkv, int T, int D, int bs, int S) {
   p.chunks = (T + QCHUNK - 1) / QCHUNK;
   // Work items: a few for each of 152 SMs, not so short that the start of one
   // (and its partial result) outweighs its tiles, not so long that the last
-  // ones run alone.  tcgen05 pass: four a SM, of 8 to 86 tiles of 96 / G
-  // queries; general kernels: eight a SM, of 32 to 512 queries.
+  // ones run alone.  tcgen05 pass: three a SM, of 8 to 86 tiles of 96 / G
+  // queries (4096 tokens of 16 heads of 64 in groups of four: two a SM 146 us,
+  // three 140, four 149, six 155); general kernels: eight a SM, of 32 to 512
+  // queries.
   const bool tc = tc_shape(D, bs);
-  const long long per_tile = tc ? 96 / (Hq / Hkv) : 1, share = slots / (152 * (tc ? 4 : 8));
+  const long long per_tile = tc ? 96 / (Hq / Hkv) : 1, share = slots / (152 * (tc ? 3 : 8));
   p.item_queries = static_cast<int>(std::max((tc ? 8 : 32) * per_tile, std::min((tc ? 86 : 512) * per_tile, share)));
   p.max_items = (slots + p.item_queries - 1) / p.item_queries + p.NB;
   size_t o = 0;
