@@ -15,7 +15,8 @@
 //   2. prefix  per block: where each 128 rows' share of its list starts
 //   3. scan    where each block's list starts; lists cut into work items
 //   4. fill    the lists: for each block the queries that select it, ascending
-// then, for 64-token blocks of 64 or 128 dims (nsa_bwd_tc.cu, on tcgen05),
+// then, for blocks of 64 or 128 tokens of 64 or 128 dims (nsa_bwd_tc.cu, on
+// tcgen05),
 //   5. pack    Q and dO by query; (lse, delta) of every row
 //   6. tc      one work item at a time: a block's keys and values stay, its
 //              queries stream past; every slot's row of dq, the items' dk, dv
@@ -609,8 +610,8 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const float* __restrict__
 
 // ------------------------------------------------------------ workspace plan
 
-// The tcgen05 pass serves the shapes of the forward's TMA kernel.
-bool tc_shape(int D, int bs) { return bs == 64 && (D == 64 || D == 128); }
+// The tcgen05 pass takes 64 keys at a time.
+bool tc_shape(int D, int bs) { return (bs == 64 || bs == 128) && (D == 64 || D == 128); }
 
 struct BwdPlan {
   long long NB, max_items;
@@ -634,7 +635,8 @@ BwdPlan bwd_plan(int B, int Hq, int Hkv, int T, int D, int bs, int S) {
   // three 140, four 149, six 155); general kernels: eight a SM, of 32 to 512
   // queries.
   const bool tc = tc_shape(D, bs);
-  const long long per_tile = tc ? 96 / (Hq / Hkv) : 1, share = slots / (152 * (tc ? 3 : 8));
+  const int halves = tc ? bs / 64 : 1;  // (each of them a CTA)
+  const long long per_tile = tc ? 96 / (Hq / Hkv) : 1, share = halves * slots / (152 * (tc ? 3 : 8));
   p.item_queries = static_cast<int>(std::max((tc ? 8 : 32) * per_tile, std::min((tc ? 86 : 512) * per_tile, share)));
   p.max_items = (slots + p.item_queries - 1) / p.item_queries + p.NB;
   size_t o = 0;
@@ -647,8 +649,8 @@ BwdPlan bwd_plan(int B, int Hq, int Hkv, int T, int D, int bs, int S) {
   p.item_off = o;   o = align256(o + static_cast<size_t>(p.max_items) * sizeof(int4));
   p.part_off = o;   o = align256(o + static_cast<size_t>(p.max_items) * 2 * bs * D * sizeof(float));
   p.rows_off = p.dqp_off = p.dqs_off = o;
-  if (tc_shape(D, bs)) {
-    const size_t rows = static_cast<size_t>(slots) * (Hq / Hkv);
+  if (tc) {
+    const size_t rows = static_cast<size_t>(slots) * halves * (Hq / Hkv);
     // (one query of zeros behind the last)
     o = align256(o + (static_cast<size_t>(B) * Hq * T + Hq / Hkv) * 2 * D * sizeof(__nv_bfloat16));
     p.dqp_off = o;
@@ -692,16 +694,16 @@ int launch_general(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t str
   switch (a.bs) {
     case 16: return launch_dkdv<D, 1>(a, w, stream);
     case 32: return launch_dkdv<D, 2>(a, w, stream);
-    case 64: return launch_dkdv<D, 4>(a, w, stream);
-    case 128: return launch_dkdv<D, 8>(a, w, stream);
-    default: return ERR_UNSUPPORTED;
+    default: break;
   }
+  if constexpr (D < 64) return a.bs == 64 ? launch_dkdv<D, 4>(a, w, stream) : launch_dkdv<D, 8>(a, w, stream);
+  return ERR_UNSUPPORTED;  // (tc_shape)
 }
 
 template <int D>
 int launch_bwd(const NsaBwdArgs& a, uint8_t* ws, cudaStream_t stream) {
   const BwdPlan p = bwd_plan(a.B, a.Hq, a.Hkv, a.T, D, a.bs, a.S);
-  if (p.max_items > 0x7fffffffLL) return ERR_SHAPE;
+  if (p.max_items > 0x3fffffffLL) return ERR_SHAPE;
   int* counts = reinterpret_cast<int*>(ws + p.count_off);
   int* total = reinterpret_cast<int*>(ws + p.total_off);
   int* off = reinterpret_cast<int*>(ws + p.off_off);

@@ -1,8 +1,9 @@
 // nsa_bwd_tc.cu -- the block-outer pass of the NSA selection attention's
-// backward for 64-token blocks of 64 or 128 dims, on tcgen05.
+// backward for blocks of 64 or 128 tokens of 64 or 128 dims, on tcgen05.
 //
 // Formulas as in nsa_bwd.cu.  One CTA per work item (a key block and a share
-// of the queries that select it); K and V of the block stay in shared memory,
+// of the queries that select it; a block of 128 tokens is two of 64 with the
+// same queries); K and V of the block stay in shared memory,
 // the queries pass in tiles of 96 rows = 96 / G queries x G heads, gathered by
 // bulk copies (G = 8, 16: one of G rows per query and 64-column panel) or by
 // cp.async from rows that a first kernel has packed by query.  Per tile, all
@@ -55,7 +56,7 @@
 namespace bsa {
 namespace {
 
-constexpr int BS = 64;     // tokens per block
+constexpr int BS = 64;     // tokens of a CTA's key block
 constexpr int ROWS = 96;   // rows per tile (queries x heads) of the 128 that an MMA takes
 constexpr int GROUP = ROWS / 32;    // warps of one epilogue half, and of the drain
 // Warps 0-2 and 4-6 epilogue (left and right 32 keys), 8-10 drain (warp w reads TMEM lanes 32 (w & 3) ..), 7 issues the
@@ -163,9 +164,11 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
                       const int* __restrict__ list, const int4* __restrict__ items,
                       const int* __restrict__ n_items, float* __restrict__ part, __half* __restrict__ dq_part,
                       float* __restrict__ dq_scale, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
-                      int G, int T, int S, int n_blk, int n_bh, float scale) {
+                      int G, int T, int S, int n_blk, int n_bh, int two, float scale) {
   using L = TcLayout<D>;
-  if (static_cast<int>(blockIdx.x) >= *n_items) return;  // fewer items than the launch bound
+  // two = 1: selected blocks of 128 tokens, the items' two halves beside one another
+  const int item_no = static_cast<int>(blockIdx.x) >> two, half = static_cast<int>(blockIdx.x) & two;
+  if (item_no >= *n_items) return;  // fewer items than the launch bound
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
@@ -177,8 +180,8 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
   float* sums = reinterpret_cast<float*>(smem + L::SUM_OFF);
   float* km = reinterpret_cast<float*>(smem + L::KMAX_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 item = items[blockIdx.x];
-  const int bg = item.x / n_blk, blk = item.x % n_blk;
+  const int4 item = items[item_no];
+  const int bg = item.x / n_blk, blk = (item.x % n_blk << two) + half;  // blk: in blocks of 64
   const int first = item.y, npairs = item.z;
   const int qpt = ROWS / G;                    // queries per tile
   const int nt = (npairs + qpt - 1) / qpt;
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
   } else if (warp == MMA_WARP) {
     const bool leader = lane == 0;
     if (leader) {
-      debug_check(blk >= 0 && blk < n_blk);
+      debug_check(blk >= 0 && blk < n_blk << two);
       mbar_arrive_expect_tx(kv_full, 2 * L::KV_TILE);
 #pragma unroll
       for (int p = 0; p < L::NP; ++p) {
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
       const int ex = static_cast<int>(__float_as_uint(bound) >> 23) - 127;
       const int e = bound > 0.0f && ex < 128 ? min(14 - ex, 126) : 0;
       const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      const size_t to = ((static_cast<size_t>(bg) * T + p.i) * S + p.s) * G + g;
+      const size_t to = ((((static_cast<size_t>(bg) * T + p.i) * S + p.s) << two) + half) * G + g;
       if (p.valid) dq_scale[to] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       __half* row = dq_part + to * D;
       if (!mbar_wait(dq_full, t & 1)) break;
@@ -563,7 +566,7 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
       const uint32_t tA =
           tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (which ? L::TK : L::TV) + c0;
       __nv_bfloat16* dst = (which ? dk : dv) + (static_cast<size_t>(bg) * T + static_cast<size_t>(blk) * BS) * D + d;
-      float* pd = part + (static_cast<size_t>(blockIdx.x) * 2 + (which ? 0 : 1)) * BS * D + d;
+      float* pd = part + (((static_cast<size_t>(item_no) * 2 + (which ? 0 : 1)) << two) + half) * BS * D + d;
 #pragma unroll
       for (int h = 0; h < (D == 128 ? 2 : 1); ++h) {
         uint32_t v[32];
@@ -643,7 +646,7 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
                                                              const __half* __restrict__ dq_part,
                                                              const float* __restrict__ dq_scale,
                                                              __nv_bfloat16* __restrict__ dq, long long n_rows, int G,
-                                                             int T, int S, int n_blk) {
+                                                             int T, int S, int n_blk, int two) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows a warp
   const int lane = threadIdx.x & 31, c = lane % LPR;
   const long long row0 = (blockIdx.x * 8LL + (threadIdx.x >> 5)) * RPW;  // the warp's first row
@@ -651,8 +654,9 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
   const bool in = row < n_rows;
   const int g = static_cast<int>(row % G);
   const long long query = in ? row / G : 0;
-  const __half* src = dq_part + (query * S * G + g) * D + (c << 3);
-  const float* sc = dq_scale + query * S * G + g;
+  const int n = S << two;  // rows of a query: one for each 64 tokens of each slot
+  const __half* src = dq_part + (query * n * G + g) * D + (c << 3);
+  const float* sc = dq_scale + query * n * G + g;
   float o[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = 0.0f;
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
   // Rows are loaded before it is known which slots are live (those of dead
   // slots hold anything and are not added).
   auto load = [&](int x, int s) {
-    if (in && s < S) {
+    if (in && s < n) {
       u[x] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<size_t>(s) * G * D));
       f[x] = sc[s * G];
     }
@@ -676,13 +680,13 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
     const long long r = row0 + x;
     if (r >= n_rows) break;
     const long long y = r / G;
-    const uint32_t m = nsa_live_slots(block_idx + y * S, S, static_cast<int>(y % T), n_blk, BS).live;
+    const uint32_t m = nsa_live_slots(block_idx + y * S, S, static_cast<int>(y % T), n_blk, BS << two).live;
     if (lane / LPR == x) live = m;
   }
-  for (int s0 = 0; s0 < S; s0 += AHEAD) {
+  for (int s0 = 0; s0 < n; s0 += AHEAD) {
 #pragma unroll
     for (int x = 0; x < AHEAD; ++x) {
-      if (in && s0 + x < S && ((live >> (s0 + x)) & 1u)) {
+      if (in && s0 + x < n && ((live >> ((s0 + x) >> two)) & 1u)) {
         const uint32_t w[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -703,7 +707,7 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
 template <int D>
 int launch_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) {
   using L = TcLayout<D>;
-  const int G = a.Hq / a.Hkv, n_blk = a.T / BS;
+  const int G = a.Hq / a.Hkv, n_blk = a.T / a.bs, two = a.bs / BS - 1;
   const long long bh = static_cast<long long>(a.B) * a.Hkv, rows = bh * G * a.T;
   CUtensorMap mk, mv;
   const uint64_t rs = static_cast<uint64_t>(D) * 2, hs = rs * a.T;
@@ -721,13 +725,14 @@ int launch_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) 
   auto kern = bulk ? nsa_bwd_tc_kernel<D, true> : nsa_bwd_tc_kernel<D, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC) != cudaSuccess)
     return ERR_LAUNCH;
-  kern<<<static_cast<unsigned>(w.max_items), bulk ? tc_threads<D, true>() : tc_threads<D, false>(), L::ALLOC, stream>>>(
+  kern<<<static_cast<unsigned>(w.max_items << two), bulk ? tc_threads<D, true>() : tc_threads<D, false>(), L::ALLOC,
+         stream>>>(
       mk, mv, w.rows, w.stats, w.list, w.items, w.n_items, w.part, w.dq_part, w.dq_scale, a.dk, a.dv, G, a.T, a.S,
-      n_blk, static_cast<int>(bh), 1.0f / sqrtf(static_cast<float>(D)));
+      n_blk, static_cast<int>(bh), two, 1.0f / sqrtf(static_cast<float>(D)));
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
   const long long sum_blocks = (rows + BLOCK_ROWS - 1) / BLOCK_ROWS;
   nsa_bwd_dq_sum_kernel<D><<<static_cast<unsigned>(sum_blocks), 256, 0, stream>>>(a.idx, w.dq_part, w.dq_scale, a.dq,
-                                                                                  rows, G, a.T, a.S, n_blk);
+                                                                                  rows, G, a.T, a.S, n_blk, two);
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
