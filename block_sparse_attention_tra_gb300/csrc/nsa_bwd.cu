@@ -15,13 +15,12 @@
 //   2. prefix  per block: where each 128 rows' share of its list starts
 //   3. scan    where each block's list starts; lists cut into work items
 //   4. fill    the lists: for each block the queries that select it, ascending
-// then, for blocks of 64 or 128 tokens of 64 or 128 dims (nsa_bwd_tc.cu, on
-// tcgen05),
+// then, for 64 and 128 dims (nsa_bwd_tc.cu, on tcgen05),
 //   5. pack    Q and dO by query; (lse, delta) of every row
 //   6. tc      one work item at a time: a block's keys and values stay, its
 //              queries stream past; every slot's row of dq, the items' dk, dv
 //   7. dq sum  the slots' rows, in slot order
-// and for any other shape (mma.sync)
+// and for 16 and 32 dims (mma.sync)
 //   5. dq      one query group at a time, gathering its blocks' keys and
 //              values; leaves (lse, delta) of its rows for 6
 //   6. dkdv    one work item at a time: a block's keys and values stay in
@@ -33,8 +32,11 @@
 //
 // dq and dkdv each form the scores: 14 instead of 10 D flops per pair, for no
 // atomic additions and no rows of dq in memory.  The tcgen05 pass forms them
-// once and writes a row of dq per slot: on one 4096-token sequence of 32 heads
-// of 128 the two general kernels took 980 us, pack, pass and sum take 352.
+// once and writes a row of dq per slot.  The whole call on 4096 tokens, 32
+// heads of 128 in groups of 16, with 1024 tokens selected in blocks of 128, 64
+// and 32 (512 in blocks of 16): 865, 1040, 1167 and 1260 us by kernels of the
+// second kind, 394, 371, 681 and 675 by the first.  At D = 32 (64-token
+// blocks, 337 us) a tcgen05 tile would be half empty.
 //
 // Where the sizes are small every step is a few microseconds of latency (256
 // tokens of 8 heads of 32: 25 us of kernels in the 45 us that eight launches
@@ -251,6 +253,7 @@ struct ChunkIter {
 
 constexpr int DQ_WARPS = 4;
 constexpr int DQ_THREADS = DQ_WARPS * 32;
+constexpr int DQ_CTAS = 5;  // blocks of a SM
 
 template <int D>
 struct DqLayout {
@@ -261,15 +264,10 @@ struct DqLayout {
   static constexpr int BYTES = DQ_WARPS * WARP_BYTES;
 };
 
-template <int D>
-constexpr int dq_min_ctas() {
-  return D == 128 ? 2 : D == 64 ? 3 : 5;
-}
-
 // One warp per query group (persistent grid), K and V chunks through its own
 // double-buffered shared memory.
 template <int D>
-__global__ void __launch_bounds__(DQ_THREADS, dq_min_ctas<D>())
+__global__ void __launch_bounds__(DQ_THREADS, DQ_CTAS)
     nsa_bwd_dq_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
                       const __nv_bfloat16* __restrict__ v, const int32_t* __restrict__ block_idx,
                       const __nv_bfloat16* __restrict__ out, const float* __restrict__ lse,
@@ -610,8 +608,8 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const float* __restrict__
 
 // ------------------------------------------------------------ workspace plan
 
-// The tcgen05 pass takes 64 keys at a time.
-bool tc_shape(int D, int bs) { return (bs == 64 || bs == 128) && (D == 64 || D == 128); }
+// Head dims that the tcgen05 pass serves.
+constexpr bool tc_dim(int D) { return D >= 64; }
 
 struct BwdPlan {
   long long NB, max_items;
@@ -634,8 +632,8 @@ BwdPlan bwd_plan(int B, int Hq, int Hkv, int T, int D, int bs, int S) {
   // queries (4096 tokens of 16 heads of 64 in groups of four: two a SM 146 us,
   // three 140, four 149, six 155); general kernels: eight a SM, of 32 to 512
   // queries.
-  const bool tc = tc_shape(D, bs);
-  const int halves = tc ? bs / 64 : 1;  // (each of them a CTA)
+  const bool tc = tc_dim(D);
+  const int halves = tc && bs == 128 ? 2 : 1;  // (each of them a CTA)
   const long long per_tile = tc ? 96 / (Hq / Hkv) : 1, share = halves * slots / (152 * (tc ? 3 : 8));
   p.item_queries = static_cast<int>(std::max((tc ? 8 : 32) * per_tile, std::min((tc ? 86 : 512) * per_tile, share)));
   p.max_items = (slots + p.item_queries - 1) / p.item_queries + p.NB;
@@ -694,10 +692,10 @@ int launch_general(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t str
   switch (a.bs) {
     case 16: return launch_dkdv<D, 1>(a, w, stream);
     case 32: return launch_dkdv<D, 2>(a, w, stream);
-    default: break;
+    case 64: return launch_dkdv<D, 4>(a, w, stream);
+    case 128: return launch_dkdv<D, 8>(a, w, stream);
+    default: return ERR_UNSUPPORTED;
   }
-  if constexpr (D < 64) return a.bs == 64 ? launch_dkdv<D, 4>(a, w, stream) : launch_dkdv<D, 8>(a, w, stream);
-  return ERR_UNSUPPORTED;  // (tc_shape)
 }
 
 template <int D>
@@ -729,7 +727,7 @@ int launch_bwd(const NsaBwdArgs& a, uint8_t* ws, cudaStream_t stream) {
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
 
   int st;
-  if constexpr (D == 64 || D == 128) st = tc_shape(D, a.bs) ? launch_nsa_bwd_tc(a, w, D, stream) : launch_general<D>(a, w, stream);
+  if constexpr (tc_dim(D)) st = launch_nsa_bwd_tc(a, w, D, stream);
   else st = launch_general<D>(a, w, stream);
   if (st != OK) return st;
   const int elements = a.bs * D;

@@ -1,5 +1,5 @@
 // nsa_bwd_tc.cu -- the block-outer pass of the NSA selection attention's
-// backward for blocks of 64 or 128 tokens of 64 or 128 dims, on tcgen05.
+// backward for 64 and 128 dims, on tcgen05.
 //
 // Formulas as in nsa_bwd.cu.  One CTA per work item (a key block and a share
 // of the queries that select it; a block of 128 tokens is two of 64 with the
@@ -56,7 +56,7 @@
 namespace bsa {
 namespace {
 
-constexpr int BS = 64;     // tokens of a CTA's key block
+constexpr int BS = 64;     // tokens of a CTA's key tile
 constexpr int ROWS = 96;   // rows per tile (queries x heads) of the 128 that an MMA takes
 constexpr int GROUP = ROWS / 32;    // warps of one epilogue half, and of the drain
 // Warps 0-2 and 4-6 epilogue (left and right 32 keys), 8-10 drain (warp w reads TMEM lanes 32 (w & 3) ..), 7 issues the
@@ -157,7 +157,10 @@ struct Pair {
   bool valid;
 };
 
-template <int D, bool TMA_IN>
+// KEYS: tokens of the CTA's key block, 64, 32 or 16.  Below 64 the products are narrower (N = KEYS, and K = KEYS for dQ);
+// of the 64-key tiles only that part is read (at D = 64 zeros behind it), and half of the epilogue has only zeros to
+// write.  An MMA then reads the same A for less arithmetic: a tile takes about as long, for half or a quarter of the keys.
+template <int D, int KEYS, bool TMA_IN>
 __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
     nsa_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __nv_bfloat16* __restrict__ rows, const float2* __restrict__ stats,
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
                       float* __restrict__ dq_scale, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
                       int G, int T, int S, int n_blk, int n_bh, int two, float scale) {
   using L = TcLayout<D>;
-  // two = 1: selected blocks of 128 tokens, the items' two halves beside one another
+  // two = 1: selected blocks of 128 tokens, an item's two halves beside one another
   const int item_no = static_cast<int>(blockIdx.x) >> two, half = static_cast<int>(blockIdx.x) & two;
   if (item_no >= *n_items) return;  // fewer items than the launch bound
   extern __shared__ uint8_t smem_raw[];
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
   float* km = reinterpret_cast<float*>(smem + L::KMAX_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 item = items[item_no];
-  const int bg = item.x / n_blk, blk = (item.x % n_blk << two) + half;  // blk: in blocks of 64
+  const int bg = item.x / n_blk, key0 = ((item.x % n_blk << two) + half) * KEYS;  // the first key's token
   const int first = item.y, npairs = item.z;
   const int qpt = ROWS / G;                    // queries per tile
   const int nt = (npairs + qpt - 1) / qpt;
@@ -324,15 +327,15 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
   } else if (warp == MMA_WARP) {
     const bool leader = lane == 0;
     if (leader) {
-      debug_check(blk >= 0 && blk < n_blk << two);
-      mbar_arrive_expect_tx(kv_full, 2 * L::KV_TILE);
+      debug_check(key0 >= 0 && key0 + KEYS <= T);
+      mbar_arrive_expect_tx(kv_full, 2 * L::NP * KEYS * 128);
 #pragma unroll
       for (int p = 0; p < L::NP; ++p) {
-        tma_load_3d(smem + L::K_OFF + p * KV_PANEL, &tmK, kv_full, 64 * p, blk * BS, bg);
-        tma_load_3d(smem + L::V_OFF + p * KV_PANEL, &tmV, kv_full, 64 * p, blk * BS, bg);
+        tma_load_3d(smem + L::K_OFF + p * KV_PANEL, &tmK, kv_full, 64 * p, key0, bg);
+        tma_load_3d(smem + L::V_OFF + p * KV_PANEL, &tmV, kv_full, 64 * p, key0, bg);
       }
     }
-    constexpr uint32_t ID_S = idesc_bf16_f32(128, BS, 0, 0);
+    constexpr uint32_t ID_S = idesc_bf16_f32(128, KEYS, 0, 0);
     const uint32_t tm = uniform(tmem), base = uniform(smem_u32(smem));
     const uint32_t kK = desc_lo(base + L::K_OFF, 16), kV = desc_lo(base + L::V_OFF, 16);
     const uint32_t kDO = desc_lo(base, 16);
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
   } else if (warp == GRAD_WARP<D>) {
     // (the scores of a tile are complete before its gradients' inputs are: what this warp commits frees the stage)
     const bool leader = lane == 0;
-    constexpr uint32_t ID_ACC = idesc_bf16_f32(128, D == 128 ? BS : 2 * BS, 1, 1);
+    constexpr uint32_t ID_ACC = idesc_bf16_f32(128, D == 128 ? KEYS : 2 * BS, 1, 1);
     constexpr uint32_t ID_Q = idesc_bf16_f32(128, D, 0, 1);
     const uint32_t tm = uniform(tmem), base = uniform(smem_u32(smem));
     // MN-major operands (a step of 16 rows is 2048 bytes), and dS K-major
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
       __syncwarp();
       if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < BS / 16; ++kk)
+        for (int kk = 0; kk < KEYS / 16; ++kk)
           mma_lo(tm + L::TQ, kDS + kk * 2, mK + kk * 128, ID_Q, kk > 0 ? 1u : 0u);
         mma_commit(dq_full);
         mma_commit(&pds_free[t & 1]);
@@ -485,8 +488,8 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
     {
       const uint4* kt = reinterpret_cast<const uint4*>(smem + L::K_OFF);
       uint32_t m = 0u;
-      for (int e = r + w * ROWS; e < L::KV_TILE / 16; e += 2 * ROWS) {
-        const uint4 u = kt[e];
+      for (int e = r + w * ROWS; e < L::NP * KEYS * 8; e += 2 * ROWS) {
+        const uint4 u = kt[e / (KEYS * 8) * (KV_PANEL / 16) + e % (KEYS * 8)];
         const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) m = max(m, max((x[j] & 0x7fffu) << 16, x[j] & 0x7fff0000u));
@@ -500,7 +503,8 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
     Pair p = pair_of(qi < qpt ? qi : npairs), p2 = pair_of(qi < qpt ? qpt + qi : npairs);
     float2 ld = stats_of(p);
     for (int t = 0; t < nt && ok; ++t) {
-      const int lim = p.valid ? p.i - blk * BS - 32 * w : -1;  // this half's keys c <= lim are causal
+      const int lim = p.valid ? min(p.i - key0 - 32 * w, KEYS - 1) : -1;  // this half's keys c <= lim are causal
+      const bool none = KEYS < 64 && w == 1;                              // a half without keys
       const float lse2 = ld.x, delta = ld.y;
       p = p2;  // the next tile's row: its numbers are on their way before this tile's arithmetic
       ld = stats_of(p);
@@ -508,9 +512,11 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
       if (!(ok = mbar_wait(&sp_full[t & 1], (t >> 1) & 1))) break;
       tc_fence_after();
       uint32_t sv[32], pv[32];
-      tmem_ld32(lane_base + L::TS + (t & 1) * BS, sv);
-      tmem_ld32(lane_base + L::TP + (t & 1) * BS, pv);
-      tmem_wait_ld();
+      if (!none) {
+        tmem_ld32(lane_base + L::TS + (t & 1) * BS, sv);
+        tmem_ld32(lane_base + L::TP + (t & 1) * BS, pv);
+        tmem_wait_ld();
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sp_empty[t & 1]);  // the next but one tile's scores may overwrite these
@@ -518,6 +524,10 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
       float sum = 0.0f;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
+        if (none) {
+          pk[c] = dk2[c] = 0u;
+          continue;
+        }
         float pp[2], dd[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -565,15 +575,16 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
       const int c0 = D == 128 ? 0 : w * 32;
       const uint32_t tA =
           tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (which ? L::TK : L::TV) + c0;
-      __nv_bfloat16* dst = (which ? dk : dv) + (static_cast<size_t>(bg) * T + static_cast<size_t>(blk) * BS) * D + d;
-      float* pd = part + (((static_cast<size_t>(item_no) * 2 + (which ? 0 : 1)) << two) + half) * BS * D + d;
+      __nv_bfloat16* dst = (which ? dk : dv) + (static_cast<size_t>(bg) * T + key0) * D + d;
+      float* pd = part + (((static_cast<size_t>(item_no) * 2 + (which ? 0 : 1)) << two) + half) * KEYS * D + d;
 #pragma unroll
-      for (int h = 0; h < (D == 128 ? 2 : 1); ++h) {
+      for (int h = 0; h < (D == 128 && KEYS == 64 ? 2 : 1); ++h) {
+        if (c0 >= KEYS) break;
         uint32_t v[32];
         tmem_ld32(tA + 32 * h, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
+        for (int c = 0; c < (KEYS < 32 ? KEYS : 32); ++c) {
           const int tok = c0 + 32 * h + c;
           if (item.w == 1) dst[tok * D] = __float2bfloat16_rn(__uint_as_float(v[c]));
           else pd[tok * D] = __uint_as_float(v[c]);
@@ -646,7 +657,7 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
                                                              const __half* __restrict__ dq_part,
                                                              const float* __restrict__ dq_scale,
                                                              __nv_bfloat16* __restrict__ dq, long long n_rows, int G,
-                                                             int T, int S, int n_blk, int two) {
+                                                             int T, int S, int n_blk, int bs, int two) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows a warp
   const int lane = threadIdx.x & 31, c = lane % LPR;
   const long long row0 = (blockIdx.x * 8LL + (threadIdx.x >> 5)) * RPW;  // the warp's first row
@@ -654,7 +665,7 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
   const bool in = row < n_rows;
   const int g = static_cast<int>(row % G);
   const long long query = in ? row / G : 0;
-  const int n = S << two;  // rows of a query: one for each 64 tokens of each slot
+  const int n = S << two;  // rows of a query: one for each slot, or each half of a slot's 128 tokens
   const __half* src = dq_part + (query * n * G + g) * D + (c << 3);
   const float* sc = dq_scale + query * n * G + g;
   float o[8];
@@ -680,7 +691,7 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
     const long long r = row0 + x;
     if (r >= n_rows) break;
     const long long y = r / G;
-    const uint32_t m = nsa_live_slots(block_idx + y * S, S, static_cast<int>(y % T), n_blk, BS << two).live;
+    const uint32_t m = nsa_live_slots(block_idx + y * S, S, static_cast<int>(y % T), n_blk, bs).live;
     if (lane / LPR == x) live = m;
   }
   for (int s0 = 0; s0 < n; s0 += AHEAD) {
@@ -704,15 +715,15 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
       make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
 }
 
-template <int D>
+template <int D, int KEYS>
 int launch_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) {
   using L = TcLayout<D>;
-  const int G = a.Hq / a.Hkv, n_blk = a.T / a.bs, two = a.bs / BS - 1;
+  const int G = a.Hq / a.Hkv, n_blk = a.T / a.bs, two = a.bs / KEYS - 1;
   const long long bh = static_cast<long long>(a.B) * a.Hkv, rows = bh * G * a.T;
   CUtensorMap mk, mv;
   const uint64_t rs = static_cast<uint64_t>(D) * 2, hs = rs * a.T;
-  int st = encode_tmap_3d(&mk, a.k, D, a.T, bh, rs, hs, 64, BS, 1);
-  if (st == OK) st = encode_tmap_3d(&mv, a.v, D, a.T, bh, rs, hs, 64, BS, 1);
+  int st = encode_tmap_3d(&mk, a.k, D, a.T, bh, rs, hs, 64, KEYS, 1);
+  if (st == OK) st = encode_tmap_3d(&mv, a.v, D, a.T, bh, rs, hs, 64, KEYS, 1);
   if (st != OK) return st;
 
   constexpr int BLOCK_ROWS = 256 / (D / 8);  // rows of one block of the two row kernels
@@ -722,7 +733,7 @@ int launch_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) 
                                                                                  w.stats, rows, G, a.T);
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
   const bool bulk = G == 8 || G == 16;
-  auto kern = bulk ? nsa_bwd_tc_kernel<D, true> : nsa_bwd_tc_kernel<D, false>;
+  auto kern = bulk ? nsa_bwd_tc_kernel<D, KEYS, true> : nsa_bwd_tc_kernel<D, KEYS, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC) != cudaSuccess)
     return ERR_LAUNCH;
   kern<<<static_cast<unsigned>(w.max_items << two), bulk ? tc_threads<D, true>() : tc_threads<D, false>(), L::ALLOC,
@@ -732,14 +743,16 @@ int launch_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) 
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
   const long long sum_blocks = (rows + BLOCK_ROWS - 1) / BLOCK_ROWS;
   nsa_bwd_dq_sum_kernel<D><<<static_cast<unsigned>(sum_blocks), 256, 0, stream>>>(a.idx, w.dq_part, w.dq_scale, a.dq,
-                                                                                  rows, G, a.T, a.S, n_blk, two);
+                                                                                  rows, G, a.T, a.S, n_blk, a.bs, two);
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
 }  // namespace
 
 int launch_nsa_bwd_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, int D, cudaStream_t stream) {
-  return D == 128 ? launch_tc<128>(a, w, stream) : launch_tc<64>(a, w, stream);
+  if (a.bs == 16) return D == 128 ? launch_tc<128, 16>(a, w, stream) : launch_tc<64, 16>(a, w, stream);
+  if (a.bs == 32) return D == 128 ? launch_tc<128, 32>(a, w, stream) : launch_tc<64, 32>(a, w, stream);
+  return D == 128 ? launch_tc<128, 64>(a, w, stream) : launch_tc<64, 64>(a, w, stream);
 }
 
 unsigned int nsa_bwd_tc_device_error() { return read_and_clear_device_error(); }

@@ -464,8 +464,7 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
  *
  * The page "nsa_selection_kernel.py" defines the operation; this differentiates
  * it.  With c = D^-0.5, row i's set J of nsa_select_forward, and that call's
- * out and lse (blocks of 64 or 128 tokens with D 64 or 128 run on tcgen05, the
- * other shapes of the forward on mma.sync kernels):
+ * out and lse (D 64 and 128 run on tcgen05, 16 and 32 on mma.sync kernels):
  *
  *   p_ij  = exp(c q_i . k_j - lse_i)            (recomputed; nothing is stored)
  *   dS_ij = c p_ij (dout_i . v_j - dout_i . out_i)
@@ -478,10 +477,10 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
  * products with dout, q and k; every sum is fp32, in an order that does not
  * vary: results repeat bit for bit.  (The tcgen05 pass keeps each block's row
  * of dq as f16 under a power-of-two factor of its own, 2^-11 of an element,
- * until the blocks are summed: workspace of B * Hq * T * S * (2 D + 4) bytes
- * for every 64 tokens of a block, and B * Hq * T * 4 D for q and dout packed
- * by query.)  Blocks that no row selects and rows that
- * select nothing may hold anything; a NaN or an infinity elsewhere may reach
+ * until the blocks are summed: workspace of B * Hq * T * S * (2 D + 4) bytes,
+ * twice that for blocks of 128 tokens, and B * Hq * T * 4 D for q and dout
+ * packed by query.)  Blocks that no row selects and rows that select nothing
+ * may hold anything; a NaN or an infinity elsewhere may reach
  * every result of the blocks and rows it is paired with, tokens that the
  * causal mask hides inside a selected block included (as in the forward).
  *
