@@ -113,6 +113,28 @@ def test_empty_rows_repeats_and_a_block_every_row_reads(D, bs, Hq, Hkv):
     assert not dq[:, :, : T // 8].any()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bs", [16, 32, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(3, 1), (16, 1), (16, 2), (10, 2)])
+def test_lists_of_several_items_at_every_block_size(D, bs, Hq, Hkv):
+    T = 1024
+    run(1, Hq, Hkv, T, D, bs, 6, seed=D + bs + Hq, change=lambda i: odd_rows(i, T // bs))
+
+
+@pytest.mark.parametrize("D,bs,Hq", [(64, 16, 8), (128, 16, 3), (64, 32, 3), (128, 32, 16), (64, 128, 8), (128, 128, 5)])
+def test_a_block_beside_garbage(D, bs, Hq):
+    """Every other block is selected by nobody and holds NaN and infinities: nothing of it is read."""
+    q, k, v, idx, dout = inputs(1, Hq, 1, 1024, D, bs, 4, seed=D + bs)
+    idx = torch.where(idx >= 0, idx // 2 * 2, idx)
+    out, lse = forward(q, k, v, idx, bs)
+    clean = bsa.nsa_select_backward(q, k, v, idx, out, lse, dout, bs)
+    for t, x in ((k, float("nan")), (v, float("inf"))):
+        t.view(1, 1, -1, 2, bs, D)[:, :, :, 1] = x
+    got = bsa.nsa_select_backward(q, k, v, idx, out, lse, dout, bs)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, clean))
+
+
 def test_blocks_no_row_reads_get_zero():
     T, bs = 512, 64
     only = lambda idx: torch.full_like(idx, -1).index_fill_(3, torch.tensor([1], device="cuda"), 2)  # noqa: E731
