@@ -409,8 +409,10 @@ int nsa_select_forward_fsa(const void* q, const void* k, const void* v, const in
 
 size_t nsa_select_backward_workspace_size(int B, int Hq, int Hkv, int T, int D, int block_size, int S) {
   if (check_nsa_shape(B, Hq, Hkv, T, D, block_size, S) != BSA_OK) return 0;
-  // list positions are 32-bit numbers, a query and its slot one of them; (batch, kv head) pairs run along a grid's second axis
+  // list positions and rows are 32-bit numbers, a query and its slot one of them; (batch, kv head) pairs run along a
+  // grid's second axis
   if (static_cast<long long>(B) * Hkv * T * S >= (1LL << 31) || T >= (1 << 26) ||
+      static_cast<long long>(B) * Hq * T >= (1LL << 31) ||
       static_cast<long long>(B) * Hkv > 65535)
     return 0;
   return nsa_bwd_workspace_bytes(B, Hq, Hkv, T, D, block_size, S);

@@ -615,22 +615,21 @@ __global__ void __launch_bounds__(256) nsa_bwd_pack_kernel(const __nv_bfloat16* 
                                                            const __nv_bfloat16* __restrict__ dout,
                                                            const float* __restrict__ lse,
                                                            __nv_bfloat16* __restrict__ rows,
-                                                           float2* __restrict__ stats, long long n_rows, int G, int T) {
+                                                           float2* __restrict__ stats, uint32_t n_rows, int G, int T) {
   constexpr int LPR = D / 8;
-  const long long row = (blockIdx.x * 256LL + threadIdx.x) / LPR;  // ((b, kv head), i, g)
+  const uint32_t row = blockIdx.x * (256u / LPR) + threadIdx.x / LPR, heads = G;  // ((b, kv head), i, g)
   const int c = threadIdx.x % LPR;
-  const int g = static_cast<int>(row % G);
-  const long long query = row / G;
+  const uint32_t g = row % heads, query = row / heads;
   uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a, o = a;
-  const long long bg = query / T, i = query % T;
-  const size_t src = ((bg * G + g) * T + i) * D + c * 8;
+  const uint32_t bg = query / T, i = query % T;
+  const size_t src = (static_cast<size_t>(bg * heads + g) * T + i) * D + c * 8;
   if (row < n_rows) {
     a = *reinterpret_cast<const uint4*>(dout + src);
     b = *reinterpret_cast<const uint4*>(q + src);
     o = *reinterpret_cast<const uint4*>(out + src);
   }
   if (row < n_rows + G) {
-    __nv_bfloat16* dst = rows + query * (2 * G * D) + ((c >> 3) * G + g) * 64 + (((c & 7) ^ (g & 7)) << 3);
+    __nv_bfloat16* dst = rows + static_cast<size_t>(query) * (2 * G * D) + ((c >> 3) * G + g) * 64 + (((c & 7) ^ (g & 7)) << 3);
     *reinterpret_cast<uint4*>(dst) = a;
     *reinterpret_cast<uint4*>(dst + G * D) = b;
   }
@@ -643,7 +642,7 @@ __global__ void __launch_bounds__(256) nsa_bwd_pack_kernel(const __nv_bfloat16* 
   }
 #pragma unroll
   for (int d = LPR / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  if (row < n_rows && c == 0) stats[row] = make_float2(lse[(bg * G + g) * T + i] * NSA_LOG2E, s);
+  if (row < n_rows && c == 0) stats[row] = make_float2(lse[static_cast<size_t>(bg * heads + g) * T + i] * NSA_LOG2E, s);
 }
 
 // dq of every row: the f16 rows of its query's live slots under their
@@ -656,15 +655,15 @@ template <int D>
 __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* __restrict__ block_idx,
                                                              const __half* __restrict__ dq_part,
                                                              const float* __restrict__ dq_scale,
-                                                             __nv_bfloat16* __restrict__ dq, long long n_rows, int G,
+                                                             __nv_bfloat16* __restrict__ dq, uint32_t n_rows, int G,
                                                              int T, int S, int n_blk, int bs, int two) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows a warp
   const int lane = threadIdx.x & 31, c = lane % LPR;
-  const long long row0 = (blockIdx.x * 8LL + (threadIdx.x >> 5)) * RPW;  // the warp's first row
-  const long long row = row0 + lane / LPR;
+  const uint32_t row0 = (blockIdx.x * 8u + (threadIdx.x >> 5)) * RPW;  // the warp's first row
+  const uint32_t row = row0 + lane / LPR, heads = G;
   const bool in = row < n_rows;
-  const int g = static_cast<int>(row % G);
-  const long long query = in ? row / G : 0;
+  const uint32_t g = row % heads;
+  const size_t query = in ? row / heads : 0;
   const int n = S << two;  // rows of a query: one for each slot, or each half of a slot's 128 tokens
   const __half* src = dq_part + (query * n * G + g) * D + (c << 3);
   const float* sc = dq_scale + query * n * G + g;
@@ -684,16 +683,14 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
   };
 #pragma unroll
   for (int x = 0; x < AHEAD; ++x) load(x, x);
-  // live slots of the warp's queries: its rows may belong to several (the warp steps them together)
+  // live slots of the warp's queries (the warp steps them together); mostly its rows are one query's
   uint32_t live = 0u;
-#pragma unroll
-  for (int x = 0; x < RPW; ++x) {
-    const long long r = row0 + x;
-    if (r >= n_rows) break;
-    const long long y = r / G;
-    const uint32_t m = nsa_live_slots(block_idx + y * S, S, static_cast<int>(y % T), n_blk, bs).live;
-    if (lane / LPR == x) live = m;
-  }
+  const uint32_t y0 = row0 / heads, y1 = (min(row0 + RPW, n_rows) - 1) / heads;
+  if (row0 < n_rows)
+    for (uint32_t y = y0; y <= y1; ++y) {
+      const uint32_t m = nsa_live_slots(block_idx + static_cast<size_t>(y) * S, S, static_cast<int>(y % T), n_blk, bs).live;
+      if (query == y) live = m;
+    }
   for (int s0 = 0; s0 < n; s0 += AHEAD) {
 #pragma unroll
     for (int x = 0; x < AHEAD; ++x) {
@@ -710,8 +707,8 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
     }
   }
   if (!in) return;
-  const long long bg = query / T, i = query % T;
-  *reinterpret_cast<uint4*>(dq + ((bg * G + g) * T + i) * D + c * 8) =
+  const uint32_t bg = row / heads / T, i = row / heads % T;
+  *reinterpret_cast<uint4*>(dq + (static_cast<size_t>(bg * heads + g) * T + i) * D + c * 8) =
       make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
 }
 
@@ -727,10 +724,11 @@ int launch_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) 
   if (st != OK) return st;
 
   constexpr int BLOCK_ROWS = 256 / (D / 8);  // rows of one block of the two row kernels
+  if (rows > 0x7fffffffLL) return ERR_SHAPE;  // (no such sizes reach this; the row kernels count in 32 bits)
+  const uint32_t n_rows = static_cast<uint32_t>(rows);
   const long long pack_blocks = (rows + G + BLOCK_ROWS - 1) / BLOCK_ROWS;
-  if (pack_blocks > 0x7fffffffLL) return ERR_SHAPE;
   nsa_bwd_pack_kernel<D><<<static_cast<unsigned>(pack_blocks), 256, 0, stream>>>(a.q, a.out, a.dout, a.lse, w.rows,
-                                                                                 w.stats, rows, G, a.T);
+                                                                                 w.stats, n_rows, G, a.T);
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
   const bool bulk = G == 8 || G == 16;
   auto kern = bulk ? nsa_bwd_tc_kernel<D, KEYS, true> : nsa_bwd_tc_kernel<D, KEYS, false>;
@@ -743,7 +741,7 @@ int launch_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) 
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
   const long long sum_blocks = (rows + BLOCK_ROWS - 1) / BLOCK_ROWS;
   nsa_bwd_dq_sum_kernel<D><<<static_cast<unsigned>(sum_blocks), 256, 0, stream>>>(a.idx, w.dq_part, w.dq_scale, a.dq,
-                                                                                  rows, G, a.T, a.S, n_blk, a.bs, two);
+                                                                                  n_rows, G, a.T, a.S, n_blk, a.bs, two);
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 

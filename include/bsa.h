@@ -498,8 +498,8 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
  * Errors: as for nsa_select_forward, plus BSA_ERR_NULLPTR for any NULL
  * pointer, BSA_ERR_ALIGN for a misaligned workspace, BSA_ERR_SCRATCH_LIMIT for
  * one that is too small, and BSA_ERR_SHAPE for B * Hkv * T * S >= 2^31,
- * T >= 2^26 or B * Hkv > 65535 (for which the size function returns 0, as for
- * any sizes that are not accepted).
+ * B * Hq * T >= 2^31, T >= 2^26 or B * Hkv > 65535 (for which the size function
+ * returns 0, as for any sizes that are not accepted).
  */
 BSA_API size_t nsa_select_backward_workspace_size(int B, int Hq, int Hkv,
                                                   int T, int D, int block_size,
