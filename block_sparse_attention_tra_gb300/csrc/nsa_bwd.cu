@@ -35,11 +35,11 @@
 // once and writes a row of dq per slot.  The whole call on 4096 tokens, 32
 // heads of 128 in groups of 16, with 1024 tokens selected in blocks of 128, 64
 // and 32 (512 in blocks of 16): 865, 1040, 1167 and 1260 us by kernels of the
-// second kind, 394, 371, 681 and 675 by the first.  At D = 32 (64-token
-// blocks, 337 us) a tcgen05 tile would be half empty.
+// second kind, 394, 367, 675 and 668 by the first.  At D = 32 (64-token
+// blocks, 340 us) a tcgen05 tile would be half empty.
 //
 // Where the sizes are small every step is a few microseconds of latency (256
-// tokens of 8 heads of 32: 25 us of kernels in the 45 us that eight launches
+// tokens of 8 heads of 32: 23 us of kernels in the 45 us that seven launches
 // and the call cost).  Mark and fill, four threads a row, take 3 and 5 us for
 // 4096 tokens of 16 slots (one a row: 3 and 12).
 #include <algorithm>

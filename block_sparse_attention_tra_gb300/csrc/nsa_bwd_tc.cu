@@ -44,7 +44,7 @@
 // 48 KB and the epilogue 24 KB: 2140 cycles at 128 bytes a cycle of the 2700
 // that it takes.  Two sequences of 8192 tokens, 32 query and 2 kv heads of 128,
 // 16 slots: 922 us, 0.68 PFLOP/s at the 10 D flops a (query, key) pair needs,
-// besides 103 us to pack (6.5 TB/s) and 357 us to sum dQ (6.4 TB/s).  With one
+// besides 102 us to pack (6.6 TB/s) and 345 us to sum dQ (6.6 TB/s).  With one
 // buffer of P and dS, and a stage for the dQ rows, the pass took 976 us.
 #include <algorithm>
 
@@ -648,9 +648,10 @@ __global__ void __launch_bounds__(256) nsa_bwd_pack_kernel(const __nv_bfloat16* 
 // dq of every row: the f16 rows of its query's live slots under their
 // factors, in slot order.  D / 8 lanes a row, the heads of a query beside one
 // another, so that a slot's G rows are read as one run.
-// Four rows ahead in 64 registers (four blocks a SM) read 2.2 GB at 6.4 TB/s
-// (358 us); eight ahead in 85 take as long, and either in fewer registers
-// spills.
+// Four rows ahead in 64 registers (four blocks a SM) read 2.2 GB at 6.6 TB/s
+// (345 us); eight ahead in 85 took as long, and either in fewer registers
+// spills.  Row numbers are 32 bits: 64-bit quotients by G and T took a third of
+// the instructions (29 us in place of 25 for 134 MB of rows of 64).
 template <int D>
 __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* __restrict__ block_idx,
                                                              const __half* __restrict__ dq_part,
