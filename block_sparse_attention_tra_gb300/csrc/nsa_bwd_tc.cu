@@ -127,8 +127,8 @@ __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
 // 32 bytes of an f16 row.  The lines are the first to leave L2: the rows are
 // read once, by a later kernel, while the packed rows are read S times.
 __device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
-  asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+  asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
 
@@ -157,9 +157,10 @@ struct Pair {
   bool valid;
 };
 
-// KEYS: tokens of the CTA's key block, 64, 32 or 16.  Below 64 the products are narrower (N = KEYS, and K = KEYS for dQ);
-// of the 64-key tiles only that part is read (at D = 64 zeros behind it), and half of the epilogue has only zeros to
-// write.  An MMA then reads the same A for less arithmetic: a tile takes about as long, for half or a quarter of the keys.
+// KEYS: tokens of the CTA's key block, 64, 32 or 16.  Below 64 the products are narrower (N = KEYS, and K = KEYS for
+// dQ); of the 64-key tiles only that part is read (at D = 64 zeros behind it), and half of the epilogue has only zeros
+// to write.  An MMA then reads the same A for less arithmetic: a tile takes about as long, for half or a quarter of
+// the keys.
 template <int D, int KEYS, bool TMA_IN>
 __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
     nsa_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -629,7 +630,8 @@ __global__ void __launch_bounds__(256) nsa_bwd_pack_kernel(const __nv_bfloat16* 
     o = *reinterpret_cast<const uint4*>(out + src);
   }
   if (row < n_rows + G) {
-    __nv_bfloat16* dst = rows + static_cast<size_t>(query) * (2 * G * D) + ((c >> 3) * G + g) * 64 + (((c & 7) ^ (g & 7)) << 3);
+    __nv_bfloat16* dst = rows + static_cast<size_t>(query) * (2 * G * D) + ((c >> 3) * G + g) * 64 +
+                         (((c & 7) ^ (g & 7)) << 3);
     *reinterpret_cast<uint4*>(dst) = a;
     *reinterpret_cast<uint4*>(dst + G * D) = b;
   }
@@ -650,8 +652,8 @@ __global__ void __launch_bounds__(256) nsa_bwd_pack_kernel(const __nv_bfloat16* 
 // another, so that a slot's G rows are read as one run.
 // Four rows ahead in 64 registers (four blocks a SM) read 2.2 GB at 6.6 TB/s
 // (345 us); eight ahead in 85 took as long, and either in fewer registers
-// spills.  Row numbers are 32 bits: 64-bit quotients by G and T took a third of
-// the instructions (29 us in place of 25 for 134 MB of rows of 64).
+// spills.  With 64-bit row numbers, and the live slots read once a row where
+// the warp's rows are one query's, 134 MB of rows of 64 took 29 us, now 25.
 template <int D>
 __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* __restrict__ block_idx,
                                                              const __half* __restrict__ dq_part,
@@ -689,7 +691,8 @@ __global__ void __launch_bounds__(256, 4) nsa_bwd_dq_sum_kernel(const int32_t* _
   const uint32_t y0 = row0 / heads, y1 = (min(row0 + RPW, n_rows) - 1) / heads;
   if (row0 < n_rows)
     for (uint32_t y = y0; y <= y1; ++y) {
-      const uint32_t m = nsa_live_slots(block_idx + static_cast<size_t>(y) * S, S, static_cast<int>(y % T), n_blk, bs).live;
+      const int i = static_cast<int>(y % T);
+      const uint32_t m = nsa_live_slots(block_idx + static_cast<size_t>(y) * S, S, i, n_blk, bs).live;
       if (query == y) live = m;
     }
   for (int s0 = 0; s0 < n; s0 += AHEAD) {
@@ -741,8 +744,8 @@ int launch_tc(const NsaBwdArgs& a, const NsaBwdScratch& w, cudaStream_t stream) 
       n_blk, static_cast<int>(bh), two, 1.0f / sqrtf(static_cast<float>(D)));
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
   const long long sum_blocks = (rows + BLOCK_ROWS - 1) / BLOCK_ROWS;
-  nsa_bwd_dq_sum_kernel<D><<<static_cast<unsigned>(sum_blocks), 256, 0, stream>>>(a.idx, w.dq_part, w.dq_scale, a.dq,
-                                                                                  n_rows, G, a.T, a.S, n_blk, a.bs, two);
+  nsa_bwd_dq_sum_kernel<D><<<static_cast<unsigned>(sum_blocks), 256, 0, stream>>>(
+      a.idx, w.dq_part, w.dq_scale, a.dq, n_rows, G, a.T, a.S, n_blk, a.bs, two);
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
