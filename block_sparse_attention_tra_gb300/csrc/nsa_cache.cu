@@ -187,6 +187,7 @@ __device__ void append_kv(const AppendArgs& a, const uint64_t* turns, float* red
 
   const int upr = a.D / UNIT;
   const int units = (t1 - t0) * upr;
+  debug_check(units <= KV_UNITS * static_cast<int>(blockDim.x));
   const T* src = static_cast<const T*>(kv ? a.v : a.k) + ((static_cast<size_t>(b) * a.Hkv + h) * a.n + t0) * a.D;
   float x[KV_UNITS][UNIT];
   float amax = 0.0f;
@@ -324,10 +325,9 @@ int launch_nsa_cache_append(const void* k, const void* v, const void* q, void* q
   a.kv_blocks = 2LL * B * a.seq_pages * Hkv;
   // threads for the tokens that a page takes at most: single tokens need a warp (128 of them 6.2 us, with a thread for
   // every unit of a page 11.9)
-  const int few = n < page ? n : page;
-  int threads = (few * D / (UNIT * KV_UNITS) + 31) / 32 * 32;
-  threads = threads < 32 ? 32 : threads > MAX_THREADS ? MAX_THREADS : threads;
-  const int upr = D / UNIT;
+  const int upr = D / UNIT, units = (n < page ? n : page) * upr;
+  const int threads = ((units + KV_UNITS - 1) / KV_UNITS + 31) / 32 * 32;
+  static_assert(128 * (128 / UNIT) <= MAX_THREADS * KV_UNITS, "threads for the largest page");
   a.q_rows = threads / upr < n ? threads / upr : n;
   a.q_chunks = (n + a.q_rows - 1) / a.q_rows;
   a.q_groups = (Hq + Q_HEADS - 1) / Q_HEADS;
