@@ -63,7 +63,7 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int STAGE_TOK = 128;  // tokens of a stage (stream kernel)
+constexpr int STAGE_LOG = 7, STAGE_TOK = 1 << STAGE_LOG;  // tokens of a stage (stream kernel)
 constexpr int ROWS = 16;    // heads of a group, padded
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
 constexpr float LSE_EMPTY = -1.0e9f;
@@ -167,12 +167,16 @@ struct Chunk {
 // Floats of one partial: (m, l) of each row, then the accumulator rows.
 __host__ __device__ constexpr int part_floats(int D) { return ROWS * (D + 2); }
 
-// Tokens that sequence b holds, and the stages of 128 that they make.
+// Tokens that sequence b holds (at most max_pages * page <= 2^31 - 16: what lies behind the last of them is counted in
+// unsigned numbers), and the pages and stages of 128 that they make.
 __device__ __forceinline__ int tokens_of(const DecodeArgs& a, int b) {
   return max(0, min(a.lens[b], a.max_pages * a.page));
 }
+__device__ __forceinline__ int pieces_of(int tokens, int size_log) {
+  return static_cast<int>((static_cast<uint32_t>(tokens) + (1u << size_log) - 1u) >> size_log);
+}
 __device__ __forceinline__ int stages_of(const DecodeArgs& a, int b) {
-  return (tokens_of(a, b) + STAGE_TOK - 1) / STAGE_TOK;
+  return pieces_of(tokens_of(a, b), STAGE_LOG);
 }
 
 // The units (a stage of one kv head) before sequence `upto`; a block-wide call,
@@ -240,7 +244,7 @@ __device__ __forceinline__ void decode_range(const DecodeArgs& a, int b, int h, 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * RING * L::SLOT;
-  const int len = min(a.lens[b], a.max_pages * a.page);
+  const int len = tokens_of(a, b);
   const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
 
   // The slots' pages, one a lane: first token (or -1), pool page, scales.
@@ -249,7 +253,7 @@ __device__ __forceinline__ void decode_range(const DecodeArgs& a, int b, int h, 
   float my_ks = 0.0f, my_vs = 0.0f;
   {
     const SlotRow sel = nsa_live_slots(a.block_idx + (static_cast<size_t>(b) * a.Hkv + h) * a.S, a.S, len - 1,
-                                       (len + a.page - 1) / a.page, a.page);
+                                       pieces_of(len, 31 - __clz(a.page)), a.page);
     if (lane >= p0 && lane < p1 && ((sel.live >> lane) & 1u)) {
       my_id = a.table[static_cast<size_t>(b) * a.max_pages + sel.blk_lane];
       if (my_id >= 0 && my_id < a.num_pages) {
@@ -702,7 +706,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
       QRows q = load_q(b, h);
       for (long long u = u0; u < u1 && ok;) {
         const int s1 = static_cast<int>(min(static_cast<long long>(n_st), s0 + (u1 - u)));
-        const int len = tokens_of(a, b), n_pages = (len + a.page - 1) >> page_log;
+        const int len = tokens_of(a, b), n_pages = pieces_of(len, page_log);
         const int whole = s0 == 0 && s1 == n_st ? SEG_WHOLE : 0;
         const SegmentHead sg{b, h, len, 2 * static_cast<int>(blockIdx.x) + (u != u0 ? 1 : 0)};
         // The window in use, the next one with its scales, and the pool pages of the one behind that: no stage
@@ -714,10 +718,11 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
         int behind = pool_page(w0 + 32);
         open_segment(sg, q);
         for (int s = s0; s < s1 && ok;) {
-          open_window(next.id, (w0 + lane) << page_log, next.ks, next.vs);
+          open_window(next.id, static_cast<int>(static_cast<uint32_t>(w0 + lane) << page_log), next.ks, next.vs);
           next = scales_of(behind, h);
           behind = pool_page(w0 + 64);
-          const int end = min(s1, ((w0 + 32) << page_log) / STAGE_TOK);  // stages of this window
+          // stages of this window (its end may be past 2^31 tokens)
+          const int end = min(s1, static_cast<int>((static_cast<uint32_t>(w0 + 32) << page_log) >> STAGE_LOG));
           put_all(sg, whole, s0, s1, s, end, w0 << page_log, 32);
           s = end;
           w0 += 32;
