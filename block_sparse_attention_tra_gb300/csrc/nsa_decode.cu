@@ -19,8 +19,14 @@
 // The query rows (heads of the group, 16 with zero rows behind the last) go to
 // f16 under a power-of-two factor of their own that brings their largest
 // element near 2^14: exact for what is not 2^-28 of it.  Probabilities are
-// rounded to f16 (2^-11): their products with the codes then are exact in the
-// tensor cores, and the error is an eighth of the final bf16 rounding.
+// rounded to f16: their products with the codes then are exact in the tensor
+// cores.  They are taken over 2^-11 to 2^-15 of the largest score's
+// exponential so far, which puts the largest at the top of the f16 range: a
+// token whose probability is 2^-25 of it still has 2^-11 of precision, an
+// eighth of the final bf16 rounding, and what is smaller is off by at most
+// 2^-36 of it.  (With the largest at 1 that border lay at 2^-14: a first token
+// of nearly all the weight and hardly a value, and tens of thousands of others
+// that make up the result, lost whole bits of it.)
 //
 // Two kernels.
 //
@@ -67,6 +73,10 @@ constexpr int STAGE_LOG = 7, STAGE_TOK = 1 << STAGE_LOG;  // tokens of a stage (
 constexpr int ROWS = 16;    // heads of a group, padded
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
 constexpr float LSE_EMPTY = -1.0e9f;
+// Exponents (log2 domain) are taken against a reference that is set P_SET below the largest score so far when one
+// exceeds it by P_MAX: probabilities stay below 2^15 (an f16 ends at 65504).  Sums and accumulators leave a warp in
+// units of 2^P_SET.
+constexpr float P_SET = 11.0f, P_MAX = 15.0f, P_UNIT = 1.0f / 2048.0f;
 
 struct DecodeArgs {
   const __nv_bfloat16* q;
@@ -99,6 +109,9 @@ struct Dec {
   static constexpr int MERGE = WARPS * ROWS * CST * 4;
   static constexpr int BYTES = WARPS * RING * SLOT > MERGE ? WARPS * RING * SLOT : MERGE;
 };
+
+// (scores past 2^24, from which 11 cannot be taken without a rounding, are their own reference)
+__device__ __forceinline__ float reference_of(float mx) { return fabsf(mx) < 16777216.0f ? mx - P_SET : mx; }
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -378,7 +391,8 @@ __device__ __forceinline__ void decode_range(const DecodeArgs& a, int b, int h, 
           mma_f16(sc[jj + j], qa[k], f16_lo(w), f16_hi(w));
         }
     }
-    const float ks = __shfl_sync(0xffffffffu, my_ks, cur.slot), vs = __shfl_sync(0xffffffffu, my_vs, cur.slot);
+    const float ks = __shfl_sync(0xffffffffu, my_ks, cur.slot);
+    const float vs = __shfl_sync(0xffffffffu, my_vs, cur.slot) * P_UNIT;
     const float e0 = f0 * ks, e1 = f1 * ks;
     const bool tail = cur.tok0 + C > len;
     float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -396,9 +410,9 @@ __device__ __forceinline__ void decode_range(const DecodeArgs& a, int b, int h, 
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-    // lazy rescale: the running maximum moves only when a score exceeds it by 8 (a probability by 2^8)
-    if (__any_sync(0xffffffffu, mx0 > m0 + 8.0f || mx1 > m1 + 8.0f)) {
-      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+    // lazy rescale: the reference moves only when a probability would exceed 2^15
+    if (__any_sync(0xffffffffu, mx0 - m0 > P_MAX || mx1 - m1 > P_MAX)) {
+      const float n0 = fmaxf(m0, reference_of(mx0)), n1 = fmaxf(m1, reference_of(mx1));
       // (a row of -inf scores so far keeps zero sums: exp2(-inf - -inf) is not taken)
       const float s0 = n0 == -INFINITY ? 1.0f : ex2f(m0 - n0), s1 = n1 == -INFINITY ? 1.0f : ex2f(m1 - n1);
       m0 = n0;
@@ -473,9 +487,9 @@ __device__ __forceinline__ void decode_range(const DecodeArgs& a, int b, int h, 
   }
   if (t == 0) {
     ml[warp][g][0] = m0;
-    ml[warp][g][1] = l0;
+    ml[warp][g][1] = l0 * P_UNIT;
     ml[warp][g + 8][0] = m1;
-    ml[warp][g + 8][1] = l1;
+    ml[warp][g + 8][1] = l1 * P_UNIT;
   }
   __syncthreads();
   const int row = threadIdx.x >> 3;
@@ -501,7 +515,7 @@ __device__ __forceinline__ void decode_range(const DecodeArgs& a, int b, int h, 
 // 1 / sum for a row with tokens, 0 for one without (NaN stays).
 __device__ __forceinline__ float inverse_sum(float sum) { return sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum; }
 __device__ __forceinline__ float lse_of(float M, float sum) {
-  return sum == 0.0f ? LSE_EMPTY : (M + __log2f(sum)) * LN2;
+  return sum == 0.0f ? LSE_EMPTY : (M + (P_SET + __log2f(sum))) * LN2;
 }
 
 // ------------------------------------------------------------ stream kernel
@@ -837,9 +851,9 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-      // lazy rescale: the running maximum moves only when a score exceeds it by 8 (a probability by 2^8)
-      if (__any_sync(0xffffffffu, mx0 > m0 + 8.0f || mx1 > m1 + 8.0f)) {
-        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+      // lazy rescale: the reference moves only when a probability would exceed 2^15
+      if (__any_sync(0xffffffffu, mx0 - m0 > P_MAX || mx1 - m1 > P_MAX)) {
+        const float n0 = fmaxf(m0, reference_of(mx0)), n1 = fmaxf(m1, reference_of(mx1));
         // (a row of -inf scores so far keeps zero sums: exp2(-inf - -inf) is not taken)
         const float s0 = n0 == -INFINITY ? 1.0f : ex2f(m0 - n0), s1 = n1 == -INFINITY ? 1.0f : ex2f(m1 - n1);
         m0 = n0;
@@ -855,12 +869,13 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
         }
       }
       const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
-      // The accumulator is held in units of vref.  A page whose scale is within 2^3 of it (nearly all are) has the
-      // ratio folded into its probabilities, and its product goes straight into the accumulator; another's is taken
-      // on its own and added under its scale, as an f16 would lose what such a ratio leaves of a probability.
+      // The accumulator is held in units of vref, the largest scale so far.  A page whose scale is at least 2^-3 of it
+      // (nearly all are) has the ratio folded into its probabilities, and its product goes straight into the
+      // accumulator; another's is taken on its own and added under its scale: an f16 would lose what a smaller ratio
+      // leaves of a probability, and what a larger one makes of it.
       if (vref == 0.0f) vref = vs;
       const float ratio = vref != 0.0f ? vs / vref : 0.0f;
-      const bool fold = ratio >= 0.125f && ratio <= 8.0f;
+      const bool fold = ratio >= 0.125f && ratio <= 1.0f;
       const float fr = fold ? ratio : 1.0f;
       uint32_t pa[4];
 #pragma unroll
@@ -884,9 +899,8 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
           mma_f16(acc[i + 1], pa, f16_hi(x01), f16_hi(x23));
         }
       } else {
-        // (the first page of a segment may be all zeros under the least scale: a far larger one becomes the unit)
-        const float grow = ratio > 8.0f ? vref / vs : 1.0f, add = ratio > 8.0f ? 1.0f : ratio;
-        if (ratio > 8.0f) vref = vs;
+        const float grow = ratio > 1.0f ? vref / vs : 1.0f, add = ratio > 1.0f ? 1.0f : ratio;
+        if (ratio > 1.0f) vref = vs;
 #pragma unroll
         for (int i = 0; i < NT; i += 2) {
           const int w = i / 4;
@@ -916,14 +930,15 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
     // every warp has read the last merge (bounded waits, so that a warp that gave up leaves no other behind)
     if (merges > 0 && !mbar_wait(&merge_bar[1], (merges - 1) & 1)) break;
     // column n = 2t, 2t + 1 of tile j, which is dim n D/8 + j, at place 8 j + n: no bank conflicts here or below
+    const float unit = vref * P_UNIT;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      *reinterpret_cast<float2*>(&merge[warp][g][8 * j + 2 * t]) = make_float2(acc[j][0] * vref, acc[j][1] * vref);
-      *reinterpret_cast<float2*>(&merge[warp][g + 8][8 * j + 2 * t]) = make_float2(acc[j][2] * vref, acc[j][3] * vref);
+      *reinterpret_cast<float2*>(&merge[warp][g][8 * j + 2 * t]) = make_float2(acc[j][0] * unit, acc[j][1] * unit);
+      *reinterpret_cast<float2*>(&merge[warp][g + 8][8 * j + 2 * t]) = make_float2(acc[j][2] * unit, acc[j][3] * unit);
     }
     if (t == 0) {
-      ml[warp][g] = make_float2(m0, l0);
-      ml[warp][g + 8] = make_float2(m1, l1);
+      ml[warp][g] = make_float2(m0, l0 * P_UNIT);
+      ml[warp][g + 8] = make_float2(m1, l1 * P_UNIT);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&merge_bar[0]);

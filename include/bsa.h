@@ -597,7 +597,9 @@ BSA_API int nsa_cache_append(const void* k, const void* v, const void* q,
  *   lse = ln sum_{t in J} exp((q . k_t) D^-0.5)            (-1e9 if J is empty)
  *
  * with k_t, v_t the values the codes stand for, which enter the products
- * unrounded (the probabilities are rounded to f16; sums are fp32).
+ * unrounded.  Probabilities are rounded to f16, to 2^-11 of themselves down to
+ * 2^-25 of the largest and to 2^-36 of the largest below that (over every page,
+ * where pages' scales differ, to 2^-33); sums are fp32.
  *
  *   q, out     : [B, Hq, 1, D] bf16 (q rotated already).
  *   block_idx  : [B, Hkv, 1, S] int32 logical pages, read as a set, -1 =

@@ -2,11 +2,13 @@
 their documented ranges, against the float64 oracle (tolerances as in
 ``test_gpu_nsa_cache.py``)."""
 
+import numpy as np
 import pytest
 import torch
 
 from block_sparse_attention_tra_gb300 import bsa
-from test_gpu_nsa_cache import Pool, check_append, check_decode
+from oracle import cache as ocache
+from test_gpu_nsa_cache import BF, U, Pool, check_append, check_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +74,55 @@ def test_decode_of_the_least_lengths():
     for pick in (None, torch.zeros((2, 1, 1, 2), dtype=torch.int32, device="cuda")):
         out, lse = bsa.nsa_select_decode(q, *pool.args(), lt, block_idx=pick, return_lse=True)
         assert not out.any() and (lse == -1.0e9).all()
+
+
+@pytest.mark.parametrize("below", [14, 20, 25, 28])
+@pytest.mark.parametrize("D,page,S", [(64, 64, 0), (64, 64, 32), (128, 32, 0), (32, 16, 32)])
+def test_decode_with_most_of_the_weight_on_a_token_of_no_value(D, page, S, below):
+    """A first token of probability next to 1 and values next to 0; the result is the sum of the many others, each of
+    probability near 2^-below, on pages whose scales differ by up to 2^3.
+
+    A probability p of the largest P is off by 2^-11 p, or by 2^-36 P where that is more, which a page's scale of 2^-3
+    of the accumulator's may make 2^-33 P; scores and sums are in fp32 (U an operation, one a product of 16 tokens and 16
+    to join the parts), the result is rounded to bf16.
+    """
+    pages, G = 32, 4
+    r = np.random.default_rng(below + D)
+    pool = Pool(1, 1, D, page, pages, seed=below)
+    k = ocache.VALUES[r.integers(0, 0x38, (pool.pages, 1, page, D))]  # 0 .. 0.9375
+    k *= np.where(r.random(k.shape) < 0.5, 1.0, -1.0)
+    at = pool.table[0].cpu().numpy()
+    k[at[0], 0, 0, :] = 0.0
+    k[..., 0], k[at[0], 0, 0, 0] = 0.0, 32.0
+    v = r.integers(0, 0x7F, (pool.pages, 1, page, D)).astype(np.uint8)
+    v[at[0], 0, 0] = 0x01  # 2^-9
+    pool.k.copy_(torch.from_numpy(ocache.e4m3_encode(k)))
+    pool.v.copy_(torch.from_numpy(v))
+    pool.ks.fill_(0.25)
+    q = 0.02 * torch.randn((1, G, 1, D), generator=torch.Generator().manual_seed(below))
+    q[..., 0] = below * np.log(2.0) * D ** 0.5 / 8.0
+    q = q.to(torch.bfloat16).cuda()
+    n = pages * page - 3
+    idx = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, 1, 1, -1)[..., :S] if S else None
+    out, lse = bsa.nsa_select_decode(q, *pool.args(), torch.tensor([n], device="cuda"), block_idx=idx, return_lse=True)
+    torch.cuda.synchronize()
+    p = pool.copy()
+    want, wl, sums = ocache.decode(q.double().cpu().numpy(), *p, [n], None if idx is None else idx.cpu().numpy())
+    small = 2.0 ** -33 * sums["v"] if S == 0 else 2.0 ** -36 * sums["v"]
+    bound = (1 + BF) * (2.0 ** -11 * sums["p"] + U * (sums["e"] + 2 * (n / 16 + 16) * sums["p"]) + small)
+    worst = (np.abs(out.double().cpu().numpy() - want) / (bound + BF * np.abs(want))).max()
+    assert worst <= 1, f"{worst:.2f} times its bound"
+    assert (np.abs(lse.double().cpu().numpy() - wl) <= U * (sums["lse"] + n + 8) + 2.0 ** -23 * np.abs(wl)).all()
+
+
+@pytest.mark.parametrize("S", [0, 3])
+@pytest.mark.parametrize("e", [14, 18, 20, 22, 24, 40, 100])
+def test_decode_scores_of_any_magnitude_are_finite(S, e):
+    """Scores up to and past the numbers between which an fp32 has no room for one: the largest has all the weight."""
+    B, D, page = 1, 64, 16
+    pool = Pool(B, 1, D, page, 40, seed=e).clean()
+    q = (torch.randn((B, 3, 1, D), generator=torch.Generator().manual_seed(e)) * 2.0 ** e).to(torch.bfloat16).cuda()
+    idx = torch.tensor([3, 0, 39], dtype=torch.int32, device="cuda").view(1, 1, 1, 3) if S else None
+    lt = torch.tensor([630], device="cuda")
+    out, lse = bsa.nsa_select_decode(q, *pool.args(), lt, block_idx=idx, return_lse=True)
+    check_decode(out, lse, q, pool, [630], idx)
