@@ -644,6 +644,12 @@ def nsa_select_backward(q, k, v, block_idx, out, lse, dout, block_size: int = 64
     return dq, dk, dv
 
 
+def _nsa_backward_counts(B, Hq, Hkv, T, S) -> bool:
+    """Whether nsa_select_backward can count these sizes (the forward takes larger ones): rows and list entries are
+    32-bit numbers, a query and its slot one of them, and (batch, kv head) pairs run along a grid's second axis."""
+    return B * Hkv * T * S < 2 ** 31 and B * Hq * T < 2 ** 31 and T < 2 ** 26 and B * Hkv <= 65535
+
+
 _NSA_FUNCTION = None
 
 
@@ -678,12 +684,20 @@ def nsa_select_attention(q, k, v, block_idx, block_size: int = 64):
     """NSA selection-branch attention with autograd: ``nsa_select_forward``
     whose gradients with respect to q, k and v come from
     ``nsa_select_backward`` (arguments as for ``nsa_select_forward``).  Runs on
-    the current stream of the tensors' device, whichever device is current.  To
-    capture a training step into a CUDA graph, capture forward and backward
-    together, with no graph of the same leaves left from outside the capture.
+    the current stream of the tensors' device, whichever device is current.
+    Where a gradient is asked for, sizes that only the forward takes are refused
+    here and not in the backward pass.  To capture a training step into a CUDA
+    graph, capture forward and backward together, with no graph of the same
+    leaves left from outside the capture.
     """
     import torch
 
+    if (torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad)
+            and q.dim() == k.dim() == block_idx.dim() == 4):
+        sizes = (*q.shape[:2], k.shape[1], q.shape[2], block_idx.shape[3])
+        if not _nsa_backward_counts(*sizes):
+            raise BsaError(f"nsa_select_attention: no gradients for B, Hq, Hkv, T, S = {sizes} "
+                           "(the limits of nsa_select_backward)", 2)
     with torch.cuda.device(_one_device("nsa_select_attention", q, k, v, block_idx)):
         return _nsa_function().apply(q, k, v, block_idx, block_size)
 

@@ -111,3 +111,16 @@ def test_binding_has_no_cpu_path():
         bsa.nsa_cache_append(x, x, c, c, s, s, t, n)
     with pytest.raises(BsaError, match="no CPU path"):
         bsa.nsa_select_decode(x[:, :, :1], c, c, s, s, t, n)
+
+
+def test_attention_refuses_what_its_backward_cannot_count():
+    """The binding's rule is the library's, on both sides of each limit; the refusal comes before the forward runs."""
+    size = bsa.nsa_select_backward_workspace_size
+    for B, Hq, Hkv, T, S in ((65535, 1, 1, 16, 1), (65536, 1, 1, 16, 1), (5, 13107, 13107, 16, 1),
+                             (16, 8192, 4096, 16, 1), (1, 1, 1, (1 << 26) - 16, 1), (1, 1, 1, 1 << 26, 1),
+                             (1, 1, 1, (1 << 26) - 16, 32), (1, 32, 2, (1 << 26) - 16, 1),
+                             (1, 31, 31, (1 << 26) - 16, 1), (64, 64, 16, 131072, 16), (64, 64, 16, 131072, 15), (2048, 16, 16, 65536, 1)):
+        assert bsa._nsa_backward_counts(B, Hq, Hkv, T, S) == (size(B, Hq, Hkv, T, 16, 16, S) > 0), (B, Hq, Hkv, T, S)
+    q, i = (torch.empty(65536, 1, 16, n, dtype=torch.bfloat16, device="meta") for n in (16, 1))
+    with pytest.raises(BsaError, match="no gradients for"):
+        bsa.nsa_select_attention(q.requires_grad_(), q, q, i, 16)

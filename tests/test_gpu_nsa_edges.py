@@ -126,3 +126,22 @@ def test_decode_scores_of_any_magnitude_are_finite(S, e):
     lt = torch.tensor([630], device="cuda")
     out, lse = bsa.nsa_select_decode(q, *pool.args(), lt, block_idx=idx, return_lse=True)
     check_decode(out, lse, q, pool, [630], idx)
+
+
+# ----------------------------------------------------------------- autograd
+
+
+def test_attention_beyond_the_backwards_limits():
+    """More (batch, kv head) pairs than the backward takes: the forward alone runs, a graph is not begun."""
+    B, T, D = 65536, 16, 16
+    q, k, v = (torch.randn((B, 1, T, D), device="cuda").to(torch.bfloat16) for _ in range(3))
+    idx = torch.zeros((B, 1, T, 1), dtype=torch.int32, device="cuda")
+    want = bsa.nsa_select_forward(q, k, v, idx, 16)
+    assert torch.equal(bsa.nsa_select_attention(q, k, v, idx, 16), want)
+    for leaf in (q, k, v):
+        leaf.requires_grad_()
+        with pytest.raises(bsa.BsaError, match="no gradients for"):
+            bsa.nsa_select_attention(q, k, v, idx, 16)
+        with torch.no_grad():
+            assert torch.equal(bsa.nsa_select_attention(q, k, v, idx, 16), want)
+        leaf.requires_grad_(False)
