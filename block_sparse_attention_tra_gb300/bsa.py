@@ -290,6 +290,14 @@ def _in_place(what, name, t, shape, *dtypes):
         raise BsaError(f"{what}: {name} must be contiguous", 2)
 
 
+def _no_gradient(what, *tensors):
+    """Refuses tensors that a gradient is asked of (called where autograd records): nothing would flow through the
+    cache's codes, and what is written in place would change under a graph that holds it."""
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise BsaError(f"{what} has no gradient: call it under torch.no_grad() or on detached tensors")
+
+
 def _int32(torch, t):
     return (t if t.dtype is torch.int32 else t.to(torch.int32)).contiguous()
 
@@ -733,12 +741,15 @@ def nsa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache
     neighbours if ``interleaved`` (None: no rotation).  With ``q [B, Hq, n,
     D]`` the rotated queries are returned, in ``q_out`` if given (q itself is
     allowed; rows past ``new_lens`` are left as they were, or zero in a new
-    tensor).  Runs on ``stream`` (default: torch's current stream) without
+    tensor).  Has no gradient: where autograd records, tensors that require one
+    are refused.  Runs on ``stream`` (default: torch's current stream) without
     synchronising.
     """
     import torch
 
     what = "nsa_cache_append"
+    if torch.is_grad_enabled():
+        _no_gradient(what, k, v, q, q_out, k_cache, v_cache, k_scale, v_scale)
     dev = _one_device(what, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens, inv_freq, q,
                       q_out)
     if stream is not None or dev != torch.cuda.current_device():
@@ -796,12 +807,15 @@ def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
     ``return_lse``); an empty sequence or selection gives 0 and -1e9.
     ``workspace`` is a uint8 CUDA tensor of at least
     ``nsa_select_decode_workspace_size(...)`` bytes (allocated when None).
-    Runs on ``stream`` (default: torch's current stream) without
+    Has no gradient: where autograd records, tensors that require one are
+    refused.  Runs on ``stream`` (default: torch's current stream) without
     synchronising.
     """
     import torch
 
     what = "nsa_select_decode"
+    if torch.is_grad_enabled():
+        _no_gradient(what, q, k_cache, v_cache, k_scale, v_scale, out, lse)
     dev = _one_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx, out, lse,
                       workspace)
     if stream is not None or dev != torch.cuda.current_device():

@@ -119,8 +119,29 @@ def test_attention_refuses_what_its_backward_cannot_count():
     for B, Hq, Hkv, T, S in ((65535, 1, 1, 16, 1), (65536, 1, 1, 16, 1), (5, 13107, 13107, 16, 1),
                              (16, 8192, 4096, 16, 1), (1, 1, 1, (1 << 26) - 16, 1), (1, 1, 1, 1 << 26, 1),
                              (1, 1, 1, (1 << 26) - 16, 32), (1, 32, 2, (1 << 26) - 16, 1),
-                             (1, 31, 31, (1 << 26) - 16, 1), (64, 64, 16, 131072, 16), (64, 64, 16, 131072, 15), (2048, 16, 16, 65536, 1)):
+                             (1, 31, 31, (1 << 26) - 16, 1), (64, 64, 16, 131072, 16), (64, 64, 16, 131072, 15),
+                             (2048, 16, 16, 65536, 1)):
         assert bsa._nsa_backward_counts(B, Hq, Hkv, T, S) == (size(B, Hq, Hkv, T, 16, 16, S) > 0), (B, Hq, Hkv, T, S)
     q, i = (torch.empty(65536, 1, 16, n, dtype=torch.bfloat16, device="meta") for n in (16, 1))
     with pytest.raises(BsaError, match="no gradients for"):
         bsa.nsa_select_attention(q.requires_grad_(), q, q, i, 16)
+
+
+def test_cache_calls_refuse_tensors_that_a_gradient_is_asked_of():
+    def of(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype)
+
+    x, c = of(1, 1, 1, 64, dtype=torch.bfloat16), of(1, 1, 64, 64, dtype=torch.uint8)
+    t, n = of(1, 1, dtype=torch.int32), of(1, dtype=torch.int32)
+    append = {"k": x, "v": x, "k_cache": c, "v_cache": c, "k_scale": of(1, 1), "v_scale": of(1, 1), "q": x, "q_out": x}
+    decode = {"q": x, "k_cache": c, "v_cache": c, "k_scale": of(1, 1), "v_scale": of(1, 1), "out": x,
+              "lse": of(1, 1, 1)}
+    for call, args in ((bsa.nsa_cache_append, append), (bsa.nsa_select_decode, decode)):
+        for name, tensor in args.items():
+            if not tensor.is_floating_point():
+                continue
+            given = args | {name: tensor.clone().requires_grad_()}
+            with pytest.raises(BsaError, match="has no gradient"):
+                call(**given, page_table=t, cache_lens=n)
+            with torch.no_grad(), pytest.raises(BsaError, match="no CPU path"):  # the next refusal
+                call(**given, page_table=t, cache_lens=n)

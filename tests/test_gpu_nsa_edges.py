@@ -83,8 +83,8 @@ def test_decode_with_most_of_the_weight_on_a_token_of_no_value(D, page, S, below
     probability near 2^-below, on pages whose scales differ by up to 2^3.
 
     A probability p of the largest P is off by 2^-11 p, or by 2^-36 P where that is more, which a page's scale of 2^-3
-    of the accumulator's may make 2^-33 P; scores and sums are in fp32 (U an operation, one a product of 16 tokens and 16
-    to join the parts), the result is rounded to bf16.
+    of the accumulator's may make 2^-33 P; scores and sums are in fp32 (U an operation, one a product of 16 tokens and
+    16 to join the parts), the result is rounded to bf16.
     """
     pages, G = 32, 4
     r = np.random.default_rng(below + D)
@@ -145,3 +145,16 @@ def test_attention_beyond_the_backwards_limits():
         with torch.no_grad():
             assert torch.equal(bsa.nsa_select_attention(q, k, v, idx, 16), want)
         leaf.requires_grad_(False)
+
+
+def test_cache_calls_on_parameters_without_autograd():
+    """Weights require gradients in a serving program too: under no_grad the calls are those on detached tensors."""
+    pool = Pool(1, 1, 64, 16, 2, seed=3).clean()
+    x = torch.randn((1, 1, 5, 64), device="cuda").to(torch.bfloat16).requires_grad_()
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with torch.no_grad():
+        q = bsa.nsa_cache_append(x, x, *pool.args(), n, q=x)
+        a = bsa.nsa_select_decode(x[:, :, :1], *pool.args(), n + 5)
+    d = x.detach()
+    assert torch.equal(q, d) and not q.requires_grad
+    assert torch.equal(a, bsa.nsa_select_decode(d[:, :, :1], *pool.args(), n + 5))
