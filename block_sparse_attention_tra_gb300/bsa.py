@@ -780,8 +780,11 @@ def nsa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache
     news = None if new_lens is None else _int32(torch, new_lens)
     freq = None if inv_freq is None else inv_freq.to(torch.float32).contiguous()
     q_ptr = out_ptr = None
+    written = [k_cache, v_cache, k_scale, v_scale]
     if q is not None:
-        if q_out is None:
+        if q_out is not None:
+            written.append(q_out)
+        else:
             make = torch.empty if news is None else torch.zeros
             q_out = make(q.shape, dtype=q.dtype, device=q.device)
         q = q.contiguous()
@@ -792,6 +795,7 @@ def nsa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache
                               Hq, Hkv, n, D, page_size, max_pages, pages, rotary, interleaved, _dtype_code(k),
                               torch.cuda.current_stream(dev).cuda_stream)
     _check(st, what)
+    torch.autograd.graph.increment_version(written)  # a graph that saved one of them must not use it any more
     return q_out
 
 
@@ -835,10 +839,13 @@ def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
         S = block_idx.shape[-1]
         if block_idx.shape != (B, Hkv, 1, S):
             raise BsaError("block_idx must be [B,Hkv,1,S]", 2)
+    written = []
     if out is not None:
         _in_place(what, "out", out, q.shape, torch.bfloat16)
+        written.append(out)
     if lse is not None:
         _in_place(what, "lse", lse, (B, Hq, 1), torch.float32)
+        written.append(lse)
     q = q.contiguous()
     table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
     idx = None if block_idx is None else _int32(torch, block_idx)
@@ -856,6 +863,8 @@ def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                torch.cuda.current_stream(dev).cuda_stream)
     _check(st, what)
+    if written:
+        torch.autograd.graph.increment_version(written)
     return (out, lse) if return_lse else out
 
 

@@ -158,3 +158,29 @@ def test_cache_calls_on_parameters_without_autograd():
     d = x.detach()
     assert torch.equal(q, d) and not q.requires_grad
     assert torch.equal(a, bsa.nsa_select_decode(d[:, :, :1], *pool.args(), n + 5))
+
+
+def test_what_a_call_writes_in_place_is_known_to_autograd():
+    """A graph that saved a tensor which a call then overwrites refuses its backward, as after torch's own in-place
+    operations; what a call only reads stays usable."""
+    pool = Pool(1, 1, 64, 16, 2, seed=4).clean()
+    x = torch.randn((1, 1, 1, 64), device="cuda").to(torch.bfloat16)
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = torch.empty_like(x), torch.empty((1, 1, 1), device="cuda")
+    w = torch.ones((), device="cuda", requires_grad=True)
+
+    def backward_after(saved, call):
+        y = (w * saved).sum()
+        call()
+        y.backward()
+
+    append = lambda: bsa.nsa_cache_append(x, x, *pool.args(), n, q=x, q_out=x)  # noqa: E731
+    decode = lambda: bsa.nsa_select_decode(x, *pool.args(), n + 1, out=out, lse=lse)  # noqa: E731
+    for saved, call in ((x, append), (pool.ks, append), (pool.vs, append), (out, decode), (lse, decode)):
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            backward_after(saved, call)
+    backward_after(x, decode)
+    backward_after(pool.ks, decode)
+    with torch.inference_mode():
+        y = torch.randn((1, 1, 1, 64), device="cuda").to(torch.bfloat16)
+        assert bsa.nsa_cache_append(y, y, *pool.args(), n, q=y, q_out=y) is y
