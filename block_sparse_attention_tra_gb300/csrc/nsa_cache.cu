@@ -6,8 +6,8 @@
 // selection -- and per kv head one scale: code = e4m3(x / s), x ~ s * code.
 // The scale of a page that begins is the least power of two s = 2^e, e >= -96,
 // with max |x| <= 448 s over the tokens written; a page that was begun keeps
-// its scale while the new tokens fit under 448 s, and otherwise takes the
-// larger one, the codes it holds being multiplied by the (power-of-two) ratio
+// its scale while that is 2^-96 or more and the new tokens fit under 448 s, and
+// otherwise takes the larger one, the codes it holds being multiplied by the (power-of-two) ratio
 // and rounded to e4m3 again.  NaN and infinities do not count towards the
 // maximum; NaN is stored as NaN, an infinity as +-448 s.
 //
@@ -227,7 +227,8 @@ __device__ void append_kv(const AppendArgs& a, const uint64_t* turns, float* red
 
   uint8_t* dst = (kv ? a.v_cache : a.k_cache) + (static_cast<size_t>(id) * a.Hkv + h) * a.page * a.D;
   float s = old;
-  if (r0 == 0 || !(amax <= 448.0f * old)) {
+  // (a page begun elsewhere may have a scale of zero, which no value can be divided by)
+  if (r0 == 0 || !(amax <= 448.0f * old && old >= exp2i(E_MIN))) {
     s = exp2i(scale_exponent(amax));
     if (threadIdx.x == 0) *scale = s;
     const float f = old / s;  // the codes already held move to the larger scale

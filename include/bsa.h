@@ -547,8 +547,8 @@ BSA_API int nsa_select_backward(const void* q, const void* k, const void* v,
  *
  * Scale of a page and head: for a page whose first slot this call writes, the
  * least 2^e, e >= -96, with max |x| <= 448 * 2^e over the (rotated) values
- * written; for a page begun before, its scale if max |x| <= 448 * scale, else
- * that least power of two, and the codes held are multiplied by the ratio of
+ * written; for a page begun before, its scale if max |x| <= 448 * scale and
+ * scale >= 2^-96, else that least power of two, and the codes held are multiplied by the ratio of
  * the scales and rounded to e4m3 again.  Values are rounded to the nearest
  * code, ties to even; infinities become +-448 and, like NaN (stored as NaN),
  * do not count towards the maximum.  Slots that get no token, and pages that

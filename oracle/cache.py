@@ -89,7 +89,7 @@ def append(x, cache, scale, table, lens, new_lens):
                 fin = np.abs(new[np.isfinite(new)])
                 amax = fin.max() if fin.size else 0.0
                 s = scale[pid, h] if r0 else 0.0
-                if not r0 or amax > 448 * s:
+                if not r0 or amax > 448 * s or s < 2.0 ** E_MIN:
                     grown = least_scale(amax)
                     codes[pid, h, :r0] = e4m3_encode(VALUES[codes[pid, h, :r0]] * (s / grown))
                     s = grown

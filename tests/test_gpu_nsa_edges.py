@@ -38,6 +38,18 @@ def test_append_around_every_warp_of_threads(D, page):
         check_append(2, 2, 1, n, D, page, [0, 3 * page - 2], seed=n + D + page)
 
 
+@pytest.mark.parametrize("old", [0.0, 2.0 ** -140, 2.0 ** -97, 2.0 ** -96])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -110, 2.0 ** -104, 1.0])
+def test_append_behind_tokens_of_a_scale_of_zero(old, scale):
+    """A page begun elsewhere, all of whose values are zero or next to it: what is appended keeps its value."""
+    pool = Pool(2, 1, 64, 32, 2, seed=2).clean()
+    pool.ks.fill_(old)
+    pool.vs.fill_(old)
+    check_append(2, 2, 1, 7, 64, 32, [3, 30], rotary=0, scale=scale, dtype=torch.float32, pool=pool)
+    for c in (pool.k, pool.v):
+        assert ((c & 127) != 127).all()
+
+
 # ------------------------------------------------------------------- decode
 
 
