@@ -643,6 +643,8 @@ def nsa_select_backward(q, k, v, block_idx, out, lse, dout, block_size: int = 64
     if workspace is None:
         need = nsa_select_backward_workspace_size(B, Hq, Hkv, T, D, block_size, S)
         workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    elif not workspace.is_contiguous():  # (its elements are counted as its memory)
+        raise BsaError("nsa_select_backward: workspace must be contiguous", 2)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     st = nsa_select_backward_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(), out.data_ptr(),
                                  lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq,
@@ -852,6 +854,8 @@ def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
     if workspace is None:
         need = nsa_select_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S)
         workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    elif not workspace.is_contiguous():
+        raise BsaError(f"{what}: workspace must be contiguous", 2)
     if out is None:
         out = torch.empty_like(q)
     if lse is None and return_lse:

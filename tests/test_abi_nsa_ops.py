@@ -145,3 +145,21 @@ def test_cache_calls_refuse_tensors_that_a_gradient_is_asked_of():
                 call(**given, page_table=t, cache_lens=n)
             with torch.no_grad(), pytest.raises(BsaError, match="no CPU path"):  # the next refusal
                 call(**given, page_table=t, cache_lens=n)
+
+
+def test_workspaces_are_contiguous(monkeypatch):
+    """The elements of an expanded or strided tensor say nothing about the memory behind it.  (Tensors that pass for a
+    device's: the refusal comes before anything is called.)"""
+    monkeypatch.setattr(bsa, "_one_device", lambda *a: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(bsa, "nsa_select_backward_raw", None)
+    monkeypatch.setattr(bsa, "nsa_select_decode_raw", None)
+    x = torch.zeros(1, 1, 64, 64, dtype=torch.bfloat16)
+    i = torch.zeros(1, 1, 64, 1, dtype=torch.int32)
+    c = torch.zeros(1, 1, 64, 64, dtype=torch.uint8)
+    s, t, n = torch.ones(1, 1), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for w in (torch.zeros(1, dtype=torch.uint8).expand(1 << 30), torch.zeros(1 << 10, dtype=torch.uint8)[::2]):
+        with pytest.raises(BsaError, match="workspace must be contiguous"):
+            bsa.nsa_select_backward(x, x, x, i, x, torch.zeros(1, 1, 64), x, workspace=w)
+        with pytest.raises(BsaError, match="workspace must be contiguous"):
+            bsa.nsa_select_decode(x[:, :, :1], c, c, s, s, t, n, workspace=w)
