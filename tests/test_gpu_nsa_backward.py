@@ -261,3 +261,33 @@ def test_a_captured_training_step_and_an_eager_one_on_another_stream(D, bs):
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(grads, w))
         assert all(torch.equal(x, y) for x, y in zip(again, beside))
+
+
+@pytest.mark.parametrize("Hq,Hkv,T,D,bs,S", [(4, 2, 96, 32, 32, 2), (4, 1, 128, 64, 64, 2), (2, 1, 64, 128, 16, 3),
+                                             (4, 2, 64, 16, 16, 2), (5, 1, 256, 64, 128, 2)])
+def test_slope_along_the_gradient_is_its_length(Hq, Hkv, T, D, bs, S):
+    """Along the unit vector w of a gradient the float64 forward, by central differences, rises as fast as the gradient
+    is long; the kernels' gradient may differ from that slope by its elements' bounds times |w| and by what the rounding
+    of out to bf16 moves the formula.  That is under 5% of the slope, and a gradient of another length or sign is refused.
+    """
+    q, k, v, idx, dout = inputs(1, Hq, Hkv, T, D, bs, S, 11)
+    out, lse = forward(q, k, v, idx, bs)
+    grads = bsa.nsa_select_backward(q, k, v, idx, out, lse, dout, bs)
+    h, n, d = [t.double().cpu().numpy() for t in (q, k, v)], idx.cpu().numpy(), dout.double().cpu().numpy()
+    o, m = onsa.nsa_select_forward(*h, n, bs)
+    true = onsa.nsa_select_backward(*h, n, o, m, d, bs)
+    *rounded, sums = onsa.nsa_select_backward(*h, n, out.double().cpu().numpy(), lse.double().cpu().numpy(), d, bs)
+    for which, (name, terms) in enumerate((("dq", S * bs), ("dk", T * Hq // Hkv), ("dv", T * Hq // Hkv))):
+        w, r = true[which] / np.linalg.norm(true[which]), rounded[which]
+        side = []
+        for e in (1e-3, -1e-3):
+            x = [y + e * w if j == which else y for j, y in enumerate(h)]
+            side.append((onsa.nsa_select_forward(*x, n, bs)[0] * d).sum())
+        slope = (side[0] - side[1]) / 2e-3
+        bound = (1 + BF) * (BF * sums[name] + U * (sums[name + "_e"] + terms * sums[name])) + BF * np.abs(r)
+        # (differences: 1e-6 of the third derivative, at most 1e-4 of the slope here)
+        slack = (bound * np.abs(w)).sum() + abs(((r - true[which]) * w).sum()) + 1e-4 * slope
+        assert slack <= 0.05 * slope
+        assert abs((grads[which].double().cpu().numpy() * w).sum() - slope) <= slack, name
+        for factor in (-1.0, 0.5, 0.9, 1.1, 2.0):  # planted in the oracle's
+            assert abs(factor * (r * w).sum() - slope) > slack
