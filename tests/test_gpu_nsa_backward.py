@@ -268,7 +268,7 @@ def test_a_captured_training_step_and_an_eager_one_on_another_stream(D, bs):
 def test_slope_along_the_gradient_is_its_length(Hq, Hkv, T, D, bs, S):
     """Along the unit vector w of a gradient the float64 forward, by central differences, rises as fast as the gradient
     is long; the kernels' gradient may differ from that slope by its elements' bounds times |w| and by what the rounding
-    of out to bf16 moves the formula.  That is under 5% of the slope, and a gradient of another length or sign is refused.
+    of out to bf16 moves the formula.  That is under 5% of the slope: another length or sign is refused.
     """
     q, k, v, idx, dout = inputs(1, Hq, Hkv, T, D, bs, S, 11)
     out, lse = forward(q, k, v, idx, bs)
@@ -291,3 +291,25 @@ def test_slope_along_the_gradient_is_its_length(Hq, Hkv, T, D, bs, S):
         assert abs((grads[which].double().cpu().numpy() * w).sum() - slope) <= slack, name
         for factor in (-1.0, 0.5, 0.9, 1.1, 2.0):  # planted in the oracle's
             assert abs(factor * (r * w).sum() - slope) > slack
+
+
+@pytest.mark.parametrize("D,bs,Hq,Hkv", [(64, 64, 8, 1), (128, 64, 16, 1), (128, 128, 3, 1), (64, 32, 4, 2),
+                                         (128, 16, 8, 2), (32, 32, 4, 1), (64, 128, 5, 1)])
+@pytest.mark.parametrize("cut", [1, 9])
+def test_a_padded_tail_of_any_finite_size_stays_out(D, bs, Hq, Hkv, cut):
+    """Tokens behind a sequence's end, inside a block that its last rows select, hold numbers up to bf16's largest and
+    their rows select nothing: every other row's and key's gradient is the one beside a tail of zeros."""
+    T, S = 512, 3
+    q, k, v, idx, dout = inputs(1, Hq, Hkv, T, D, bs, S, D + bs + cut)
+    idx[:, :, T - cut:] = -1
+    for t in (q, k, v, dout):
+        t[:, :, T - cut:] = 0
+    out, lse = forward(q, k, v, idx, bs)
+    clean = bsa.nsa_select_backward(q, k, v, idx, out, lse, dout, bs)
+    for t, x in ((k, 3e38), (v, -1e38), (q, 1e38), (dout, 3e38)):
+        t[:, :, T - cut:] = x
+    k[:, :, T - cut:, ::3] = -1e30
+    got = bsa.nsa_select_backward(q, k, v, idx, out, lse, dout, bs)
+    torch.cuda.synchronize()
+    for x, y in zip(got, clean):
+        assert torch.equal(x, y)
