@@ -556,8 +556,9 @@ int bsa_read_probe(const void* buf, size_t bytes, int reps, unsigned int* sink, 
 
 int bsa_device_error(void) {
   const unsigned codes[10] = {tra_bf16_device_error(), tra_f32_device_error(), nsa_device_error(),
-                             tra_bwd_device_error(), tra_diff_device_error(), nsa_fsa_device_error(),
-                             nsa_bwd_device_error(), nsa_bwd_tc_device_error(), nsa_decode_device_error(), selftest_device_error()};
+                              tra_bwd_device_error(), tra_diff_device_error(), nsa_fsa_device_error(),
+                              nsa_bwd_device_error(), nsa_bwd_tc_device_error(), nsa_decode_device_error(),
+                              selftest_device_error()};
   unsigned worst = 0;
   for (unsigned c : codes) {
     if (c == 0xffffffffu) return -1;

@@ -147,9 +147,10 @@ int launch_nsa_cache_append(const void* k, const void* v, const void* q, void* q
                             cudaStream_t stream);
 
 // Attention of one query token per sequence over that cache (nsa_decode.cu);
-// block_idx null: every page.  `workspace` holds nsa_decode_workspace_bytes(D)
-// bytes, 16-byte aligned: the partial results of at most DECODE_MAX_RANGES
-// ranges of the work list.
+// block_idx null: every page.  `workspace` holds nsa_decode_workspace_bytes(D,
+// S) bytes, 16-byte aligned: for S = 0 (every page) the partial results of at
+// most DECODE_MAX_RANGES ranges of the work list; selected pages (S > 0) leave
+// none, and use nothing of their 256 bytes.
 constexpr int DECODE_MAX_RANGES = 512;
 size_t nsa_decode_workspace_bytes(int D, int S);
 int launch_nsa_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

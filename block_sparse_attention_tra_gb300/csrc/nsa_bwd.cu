@@ -35,8 +35,11 @@
 // once and writes a row of dq per slot.  The whole call on 4096 tokens, 32
 // heads of 128 in groups of 16, with 1024 tokens selected in blocks of 128, 64
 // and 32 (512 in blocks of 16): 865, 1040, 1167 and 1260 us by kernels of the
-// second kind, 394, 367, 675 and 668 by the first.  At D = 32 (64-token
-// blocks, 340 us) a tcgen05 tile would be half empty.
+// mma.sync kind, 399, 374, 681 and 668 by the tcgen05 pass.  The pass is built
+// for 64 and 128 dims.  The mma.sync kernels, which serve 16 and 32, take 271
+// and 324 us there (64-token blocks) where the pass takes 243 for 64 dims:
+// rows filled up to 64 columns with zeros would be the faster form of 32 at
+// these sizes, and are not built.
 //
 // Where the sizes are small every step is a few microseconds of latency (256
 // tokens of 8 heads of 32: 23 us of kernels in the 45 us that seven launches

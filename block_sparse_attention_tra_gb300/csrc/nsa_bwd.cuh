@@ -23,8 +23,9 @@ struct NsaBwdArgs {
 // Pieces of the workspace.  list: the queries of every block, ascending, as
 // i * 32 + slot; items: {block, first list entry, queries, items of its
 // block}; part: fp32 dk, dv of each item of a block with several; dq_part,
-// dq_scale (tcgen05 pass): f16 dQ rows [slot of the index tensor][64 tokens of
-// its block][head][D] and their factors.
+// dq_scale (tcgen05 pass): f16 dQ rows [slot of the index tensor][head][D] and
+// their factors, one row a slot; for blocks of 128 tokens two a slot, one for
+// each half of its block: [slot][half][head][D].
 struct NsaBwdScratch {
   float2* stats;
   int* list;

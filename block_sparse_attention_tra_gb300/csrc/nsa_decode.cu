@@ -52,8 +52,8 @@
 // writes the pairs that it covers whole, and of the ones it starts or ends in
 // the middle of leaves (max, sum, accumulator) in the workspace, which a
 // second kernel joins in order.  Bound by the cache's bytes on paper: four
-// sequences of up to 131072 tokens are 155 MB, 42.4 us (3.7 TB/s; the first
-// kernel alone 39.5).  What holds it there is the consumers' latency: a slice
+// sequences of up to 131072 tokens are 155 MB, 42.5 us (3.6 TB/s; the first
+// kernel alone 39).  What holds it there is the consumers' latency: a slice
 // of 16 tokens is 1450 cycles of load, product, maximum, exponential, product,
 // and the registers of eight warps (168 each) leave two a scheduler to hide it
 // (issue slots 31% busy).  Slices of 32 tokens on two teams of warps, and score
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
         tma_load_3d(dst + L::KV + 16 * k * D, &tmV, &full[st], 0, 0, head);
       }
     };
-    // stages [s, end) of a segment that has [s0, s1); stage x begins with token x * 64 - origin of the window
+    // stages [s, end) of a segment that has [s0, s1); stage x begins with token x * STAGE_TOK - origin of the window
     auto put_all = [&](const SegmentHead& sg, int whole, int s0, int s1, int s, int end, int origin, int n) {
       for (; s < end && ok; s += BATCH) {
         const int x = s + lane;
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1)
     };
     // the whole warp: lane l's page into the window
     auto open_window = [&](int id, int tok, float ks, float vs) {
-      __syncwarp();  // lane 0 is done with the last one
+      __syncwarp();  // the lanes that put stages up are done with the last one
       win[lane] = make_int4(id, tok, __float_as_int(ks), __float_as_int(vs));
       __syncwarp();
     };
@@ -1167,9 +1167,9 @@ template <int D, int C>
 int launch_cluster(const DecodeArgs& a, cudaStream_t stream) {
   using L = Dec<D, C>;
   const long long items = static_cast<long long>(a.B) * a.Hkv;
-  // Blocks of a cluster: as many, of whole slots, as leave each a SM.  More share the SMs without a gain (24 sequences
-  // of 4 kv heads and 16 pages of 64 tokens, with cold caches: one block a pair 18.8 us, two 22.5, four 27.9); fewer
-  // leave some idle (one sequence of 2 kv heads: eight blocks 12.3 us, one 18.4; of each, 5 us are the timing's).
+  // Blocks of a cluster: as many, of whole slots, as leave each a SM.  More share the SMs (24 sequences of 4 kv heads
+  // and 16 pages of 64 tokens of 128, with cold caches: one block a pair 15.0 us, two 17.7, four 23.7, eight 27.4; of
+  // 64 dims 10.6, 11.0, 10.1, 15.7); fewer leave some idle (one sequence of 2 kv heads: 14.1, 13.3, 9.5, 8.1).
   int cs = 1;
   while (cs < 8 && 2 * cs <= a.S && 2 * items * cs <= sm_count()) cs *= 2;
   auto kern = nsa_decode_select_kernel<D, C>;

@@ -475,14 +475,22 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
  * A row that selects nothing has dq = 0 and adds nothing to dk and dv; a key
  * that no row reads has dk = dv = 0.  p and dS are rounded to bf16 before the
  * products with dout, q and k; every sum is fp32, in an order that does not
- * vary: results repeat bit for bit.  (The tcgen05 pass keeps each block's row
- * of dq as f16 under a power-of-two factor of its own, 2^-11 of an element,
- * until the blocks are summed: workspace of B * Hq * T * S * (2 D + 4) bytes,
- * twice that for blocks of 128 tokens, and B * Hq * T * 4 D for q and dout
- * packed by query.)  Blocks that no row selects and rows that select nothing
- * may hold anything; a NaN or an infinity elsewhere may reach
- * every result of the blocks and rows it is paired with, tokens that the
- * causal mask hides inside a selected block included (as in the forward).
+ * vary: results repeat bit for bit.  The tcgen05 pass keeps each block's row
+ * of dq as f16 under a power-of-two factor of its own until the blocks are
+ * summed: 2^-11 of an element, or 2^-39 of sum_j |dS_ij| times the largest
+ * element of the block's keys that are read, where that is more.
+ *
+ * Blocks that no row selects and rows that select nothing may hold anything,
+ * and the tokens of a selected block that no row reads (behind a sequence's
+ * end) anything finite.  A NaN or an infinity elsewhere may reach every result
+ * of the blocks and rows it is paired with, tokens that the causal mask hides
+ * inside a selected block included (as in the forward).
+ *
+ * Workspace: for D of 64 and 128, B * Hq * T * S * (2 D + 4) bytes (twice that
+ * for blocks of 128 tokens) and B * Hq * T * 4 D for q and dout packed by
+ * query; the lists take B * Hkv * T * S * 4 bytes and a count of each block for
+ * every 128 rows, B * Hkv * T^2 / (32 * block_size) bytes.  Calls on some of
+ * the batches or kv heads at a time need less.
  *
  *   q, out, dout, dq   : [B, Hq, T, D] bf16 (out as the forward wrote it).
  *   k, v, dk, dv       : [B, Hkv, T, D] bf16.
@@ -555,8 +563,9 @@ BSA_API int nsa_select_backward(const void* q, const void* k, const void* v,
  * get none, are left as they were.
  *
  *   k, v       : [B, Hkv, n, D] of `dtype`.
- *   q, q_out   : [B, Hq, n, D] of `dtype`, or both NULL; q_out may be q.  Rows
- *                past new_lens[b] are not written.
+ *   q, q_out   : [B, Hq, n, D] of `dtype`, or both NULL; q_out may be q, and
+ *                overlaps no input otherwise.  Rows past new_lens[b] are not
+ *                written.
  *   cache_lens : [B] int32 (a negative one: nothing is cached for b).
  *   new_lens   : [B] int32, clamped to n, or NULL (n for every sequence).
  *   inv_freq   : [rotary_dim / 2] fp32, finite; may be NULL if rotary_dim is 0.
