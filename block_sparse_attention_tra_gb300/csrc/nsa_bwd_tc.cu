@@ -9,7 +9,8 @@
 // cp.async from rows that a first kernel has packed by query.  Per tile, all
 // accumulators fp32 in TMEM:
 //     S  = Q K^T, dP = dO V^T                [96 rows x 64 keys]
-//     P  = exp2(S c log2e - lse2), dS = c P (dP - delta)     (epilogue, bf16)
+//     P  = exp2(S c log2e - lse2), dS = c P (dP - delta)     (epilogue; to bf16,
+//                                   as both operands of an MMA have one type)
 //     dV^T += dO^T P, dK^T += Q^T dS         [D x 64 keys]
 //     dQ = dS K                              [96 rows x D]
 // Every product has 128 rows of A this way (64 keys as M would run the tensor
