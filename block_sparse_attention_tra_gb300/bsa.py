@@ -751,7 +751,7 @@ def nsa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache
 
     what = "nsa_cache_append"
     if torch.is_grad_enabled():
-        _no_gradient(what, k, v, q, q_out, k_cache, v_cache, k_scale, v_scale)
+        _no_gradient(what, k, v, q, q_out, k_cache, v_cache, k_scale, v_scale, inv_freq)
     dev = _one_device(what, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens, inv_freq, q,
                       q_out)
     if stream is not None or dev != torch.cuda.current_device():

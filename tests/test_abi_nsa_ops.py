@@ -133,7 +133,8 @@ def test_cache_calls_refuse_tensors_that_a_gradient_is_asked_of():
 
     x, c = of(1, 1, 1, 64, dtype=torch.bfloat16), of(1, 1, 64, 64, dtype=torch.uint8)
     t, n = of(1, 1, dtype=torch.int32), of(1, dtype=torch.int32)
-    append = {"k": x, "v": x, "k_cache": c, "v_cache": c, "k_scale": of(1, 1), "v_scale": of(1, 1), "q": x, "q_out": x}
+    append = {"k": x, "v": x, "k_cache": c, "v_cache": c, "k_scale": of(1, 1), "v_scale": of(1, 1), "q": x, "q_out": x,
+              "inv_freq": of(8)}
     decode = {"q": x, "k_cache": c, "v_cache": c, "k_scale": of(1, 1), "v_scale": of(1, 1), "out": x,
               "lse": of(1, 1, 1)}
     for call, args in ((bsa.nsa_cache_append, append), (bsa.nsa_select_decode, decode)):
