@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(DQ_THREADS, DQ_CTAS)
       for (int e = lane; e < 16 * CPR; e += 32) {
         const int r = e / CPR, c = e % CPR;
         const size_t off = static_cast<size_t>(debug_index(tok0 + r, 0, T)) * D + c * 8;
-        cp_async16(dk + r * L::RB + c * 16, kb + off);
+        // (dS of the keys that the mask hides is 0; what they hold may not be a number)
+        cp_async16(dk + r * L::RB + c * 16, kb + off, tok0 + r <= i ? 16u : 0u);
         cp_async16(dv + r * L::RB + c * 16, vb + off);
       }
     };

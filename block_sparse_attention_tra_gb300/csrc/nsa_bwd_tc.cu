@@ -25,9 +25,9 @@
 // that nothing overflows (an f16 keeps 2^-11 of each element down to 2^-29 of
 // the bound): half the bytes of fp32 at an eighth of the final bf16 rounding.
 // max|K| is over the keys that a query of the item reads: what lies behind them
-// in the block (a padded tail) may be of any finite size.  (A bound of every
-// row's own, sum_j |dS_j| max|K_j|, took 3 to 10% longer at D = 64 and for
-// blocks of 32 tokens.)
+// in the block (a padded tail) does not count.  (A bound of every row's own,
+// sum_j |dS_j| max|K_j|, took 3 to 10% longer at D = 64 and for blocks of 32
+// tokens.)
 // A last kernel sums them per query in slot order, so nothing depends on the
 // order in which CTAs run.  Adding fp32 rows to dq in L2 instead would move
 // twice the bytes through the L2's atomic units and not repeat bit for bit.
@@ -490,14 +490,16 @@ __global__ void __launch_bounds__(tc_threads<D, TMA_IN>(), 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 32 * w;
     const float sl2 = scale * NSA_LOG2E;
     bool ok = mbar_wait(kv_full, 0);
-    // max |K| over the keys up to the item's last query, for the drain's bound on a dQ row
+    // max |K| over the keys up to the item's last query, for the drain's bound on a dQ row.  The keys behind it become
+    // zeros, as dS of them does: what they hold may not be a number.  (The first scores may be read before that or
+    // after: the mask hides them.  dQ's products come behind this warp's first proxy fence and arrival below.)
     {
       const int live = (list[first + npairs - 1] >> 5) - key0;
-      const uint4* kt = reinterpret_cast<const uint4*>(smem + L::K_OFF);
+      uint4* kt = reinterpret_cast<uint4*>(smem + L::K_OFF);
       uint32_t m = 0u;
       for (int e = r + w * ROWS; e < L::NP * KEYS * 8; e += 2 * ROWS) {
-        if (e % (KEYS * 8) / 8 > live) continue;
-        const uint4 u = kt[e / (KEYS * 8) * (KV_PANEL / 16) + e % (KEYS * 8)];
+        uint4& u = kt[e / (KEYS * 8) * (KV_PANEL / 16) + e % (KEYS * 8)];
+        if (e % (KEYS * 8) / 8 > live) u = make_uint4(0u, 0u, 0u, 0u);
         const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) m = max(m, max((x[j] & 0x7fffu) << 16, x[j] & 0x7fff0000u));

@@ -480,11 +480,12 @@ BSA_API int nsa_select_forward_fsa(const void* q, const void* k,
  * summed: 2^-11 of an element, or 2^-39 of sum_j |dS_ij| times the largest
  * element of the block's keys that are read, where that is more.
  *
- * Blocks that no row selects and rows that select nothing may hold anything,
- * and the tokens of a selected block that no row reads (behind a sequence's
- * end) anything finite.  A NaN or an infinity elsewhere may reach every result
- * of the blocks and rows it is paired with, tokens that the causal mask hides
- * inside a selected block included (as in the forward).
+ * Blocks that no row selects, rows that select nothing, and the tokens of a
+ * block that lie behind every row that selects it (a padded tail) may hold
+ * anything.  A NaN or an infinity elsewhere may reach every result of the
+ * blocks and rows it is paired with, tokens that the causal mask hides inside a
+ * selected block included.  (In the forward an infinity or a NaN in v reaches
+ * the rows of its block from a padded tail too.)
  *
  * Workspace: for D of 64 and 128, B * Hq * T * S * (2 D + 4) bytes (twice that
  * for blocks of 128 tokens) and B * Hq * T * 4 D for q and dout packed by

@@ -296,9 +296,10 @@ def test_slope_along_the_gradient_is_its_length(Hq, Hkv, T, D, bs, S):
 @pytest.mark.parametrize("D,bs,Hq,Hkv", [(64, 64, 8, 1), (128, 64, 16, 1), (128, 128, 3, 1), (64, 32, 4, 2),
                                          (128, 16, 8, 2), (32, 32, 4, 1), (64, 128, 5, 1)])
 @pytest.mark.parametrize("cut", [1, 9])
-def test_a_padded_tail_of_any_finite_size_stays_out(D, bs, Hq, Hkv, cut):
-    """Tokens behind a sequence's end, inside a block that its last rows select, hold numbers up to bf16's largest and
-    their rows select nothing: every other row's and key's gradient is the one beside a tail of zeros."""
+@pytest.mark.parametrize("what", ["large", "inf", "nan"])
+def test_a_padded_tail_of_anything_stays_out(D, bs, Hq, Hkv, cut, what):
+    """Tokens behind a sequence's end, inside a block that its last rows select, hold numbers up to bf16's largest or
+    none, and their rows select nothing: every other row's and key's gradient is the one beside a tail of zeros."""
     T, S = 512, 3
     q, k, v, idx, dout = inputs(1, Hq, Hkv, T, D, bs, S, D + bs + cut)
     idx[:, :, T - cut:] = -1
@@ -306,7 +307,8 @@ def test_a_padded_tail_of_any_finite_size_stays_out(D, bs, Hq, Hkv, cut):
         t[:, :, T - cut:] = 0
     out, lse = forward(q, k, v, idx, bs)
     clean = bsa.nsa_select_backward(q, k, v, idx, out, lse, dout, bs)
-    for t, x in ((k, 3e38), (v, -1e38), (q, 1e38), (dout, 3e38)):
+    top = {"large": 3e38, "inf": float("inf"), "nan": float("nan")}[what]
+    for t, x in ((k, top), (v, -top), (q, top / 2), (dout, top), (out, top), (lse, top)):
         t[:, :, T - cut:] = x
     k[:, :, T - cut:, ::3] = -1e30
     got = bsa.nsa_select_backward(q, k, v, idx, out, lse, dout, bs)
