@@ -18,6 +18,13 @@ kernel for sm_103a behind a C ABI (``include/bsa.h``, ``libbsa.so``):
   serving: new tokens' keys (rotated by position) and values into a paged
   cache of e4m3 codes with a scale for each page and head, and one query token
   per sequence over that cache, its selected blocks or all of them.
+* ``qk_norm_rope`` -- what stands before the attention: the RMS norm of every
+  query and key head and its rotation by position, in one pass, with its
+  gradients (``qk_norm_rope_forward``, ``qk_norm_rope_backward``;
+  ``rope_frequencies`` makes the frequencies).
+* ``nsa_cache4_append``, ``nsa_cache4_read`` and ``nsa_cache4_decode`` -- a
+  paged cache of 4-bit codes with a scale for every 16 elements: filled (keys
+  normalised and rotated on the way), read back, attended to.
 * ``tra_forward_host`` -- ``tra_forward`` on host tensors, streamed through
   the GPU in chunks of heads with overlapped copies.
 * ``tra_backward`` and ``tra_attention`` -- the gradients of ``tra_forward``,
@@ -35,6 +42,13 @@ from .bsa import (  # noqa: F401
     device_error,
     library_path,
     load_library,
+    nsa_cache4_append,
+    nsa_cache4_append_raw,
+    nsa_cache4_decode,
+    nsa_cache4_decode_raw,
+    nsa_cache4_decode_workspace_size,
+    nsa_cache4_read,
+    nsa_cache4_read_raw,
     nsa_cache_append,
     nsa_cache_append_raw,
     nsa_select_attention,
@@ -49,6 +63,13 @@ from .bsa import (  # noqa: F401
     nsa_select_forward_fsa_raw,
     nsa_select_forward_raw,
     nsa_select_fsa_workspace_size,
+    qk_norm_rope,
+    qk_norm_rope_backward,
+    qk_norm_rope_backward_raw,
+    qk_norm_rope_backward_workspace_size,
+    qk_norm_rope_forward,
+    qk_norm_rope_forward_raw,
+    rope_frequencies,
     status_string,
     tra_attention,
     tra_backward,
@@ -99,5 +120,19 @@ __all__ = [
     "nsa_select_decode",
     "nsa_select_decode_raw",
     "nsa_select_decode_workspace_size",
+    "nsa_cache4_append",
+    "nsa_cache4_append_raw",
+    "nsa_cache4_decode",
+    "nsa_cache4_decode_raw",
+    "nsa_cache4_decode_workspace_size",
+    "nsa_cache4_read",
+    "nsa_cache4_read_raw",
+    "qk_norm_rope",
+    "qk_norm_rope_backward",
+    "qk_norm_rope_backward_raw",
+    "qk_norm_rope_backward_workspace_size",
+    "qk_norm_rope_forward",
+    "qk_norm_rope_forward_raw",
+    "rope_frequencies",
     "status_string",
 ]

@@ -111,6 +111,20 @@ def open_library(path):
     lib.nsa_select_decode_workspace_size.restype = sz
     lib.nsa_select_decode.argtypes = [vp] * 10 + [i32] * 8 + [vp, sz, vp]
     lib.nsa_select_decode.restype = i32
+    lib.qk_norm_rope_forward.argtypes = [vp] * 9 + [i32] * 7 + [f32, f32, i32, i32, vp]
+    lib.qk_norm_rope_forward.restype = i32
+    lib.qk_norm_rope_backward_workspace_size.argtypes = [i32] * 5
+    lib.qk_norm_rope_backward_workspace_size.restype = sz
+    lib.qk_norm_rope_backward.argtypes = [vp] * 13 + [i32] * 7 + [f32, f32, i32, i32, vp, sz, vp]
+    lib.qk_norm_rope_backward.restype = i32
+    lib.nsa_cache4_append.argtypes = [vp] * 17 + [i32] * 10 + [f32, f32, i32, i32, vp]
+    lib.nsa_cache4_append.restype = i32
+    lib.nsa_cache4_read.argtypes = [vp] * 11 + [i32] * 8 + [vp]
+    lib.nsa_cache4_read.restype = i32
+    lib.nsa_cache4_decode_workspace_size.argtypes = [i32] * 7
+    lib.nsa_cache4_decode_workspace_size.restype = sz
+    lib.nsa_cache4_decode.argtypes = [vp] * 12 + [i32] * 8 + [vp, sz, vp]
+    lib.nsa_cache4_decode.restype = i32
     lib.bsa_status_string.argtypes = [i32]
     lib.bsa_status_string.restype = ctypes.c_char_p
     lib.bsa_version.argtypes = []
@@ -254,6 +268,73 @@ def nsa_select_decode_raw(q, k_cache, v_cache, k_scale, v_scale, page_table, cac
     return load_library().nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx,
                                             out, lse, B, Hq, Hkv, D, page_size, max_pages, num_pages, S, workspace,
                                             int(workspace_bytes), stream)
+
+
+def _strides(numbers):
+    """Strides in elements as the C entry points take them (None: all contiguous)."""
+    return None if numbers is None else (ctypes.c_int64 * len(numbers))(*numbers)
+
+
+def qk_norm_rope_forward_raw(q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq, strides, B, Hq, Hkv, T, D,
+                             rotary_dim, interleaved, rotary_scale, eps, dtype, weight_dtype, stream=0) -> int:
+    """Direct C call with integer device pointers (q_weight, k_weight,
+    positions and inv_freq may be None); ``strides``: 12 numbers or None."""
+    return load_library().qk_norm_rope_forward(q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq,
+                                               _strides(strides), B, Hq, Hkv, T, D, rotary_dim, int(bool(interleaved)),
+                                               float(rotary_scale), float(eps), int(dtype), int(weight_dtype), stream)
+
+
+def qk_norm_rope_backward_workspace_size(B, Hq, Hkv, T, D) -> int:
+    """Bytes of workspace ``qk_norm_rope_backward`` needs (0 = sizes not accepted)."""
+    return int(load_library().qk_norm_rope_backward_workspace_size(B, Hq, Hkv, T, D))
+
+
+def qk_norm_rope_backward_raw(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, q_weight, k_weight, positions,
+                              inv_freq, strides, B, Hq, Hkv, T, D, rotary_dim, interleaved, rotary_scale, eps, dtype,
+                              weight_dtype, workspace, workspace_bytes, stream=0) -> int:
+    """Direct C call with integer device pointers; ``strides``: 18 numbers or None."""
+    return load_library().qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, q_weight, k_weight,
+                                                positions, inv_freq, _strides(strides), B, Hq, Hkv, T, D, rotary_dim,
+                                                int(bool(interleaved)), float(rotary_scale), float(eps), int(dtype),
+                                                int(weight_dtype), workspace, int(workspace_bytes), stream)
+
+
+def nsa_cache4_append_raw(k, v, q, q_out, k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table,
+                          cache_lens, new_lens, q_weight, k_weight, inv_freq, strides, B, Hq, Hkv, n, D, page_size,
+                          max_pages, num_pages, rotary_dim, interleaved, rotary_scale, eps, dtype, weight_dtype,
+                          stream=0) -> int:
+    """Direct C call with integer device pointers (q, q_out, the factors,
+    new_lens, the weights and inv_freq may be None); ``strides``: 9 numbers or
+    None."""
+    return load_library().nsa_cache4_append(k, v, q, q_out, k_cache, v_cache, k_scale, v_scale, k_factor, v_factor,
+                                            page_table, cache_lens, new_lens, q_weight, k_weight, inv_freq,
+                                            _strides(strides), B, Hq, Hkv, n, D, page_size, max_pages, num_pages,
+                                            rotary_dim, int(bool(interleaved)), float(rotary_scale), float(eps),
+                                            int(dtype), int(weight_dtype), stream)
+
+
+def nsa_cache4_read_raw(k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table, starts, cache_lens, k_out,
+                        v_out, B, Hkv, n, D, page_size, max_pages, num_pages, dtype, stream=0) -> int:
+    """Direct C call with integer device pointers (the factors and starts may
+    be None); returns the bsa_status."""
+    return load_library().nsa_cache4_read(k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table, starts,
+                                          cache_lens, k_out, v_out, B, Hkv, n, D, page_size, max_pages, num_pages,
+                                          int(dtype), stream)
+
+
+def nsa_cache4_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S) -> int:
+    """Bytes of workspace ``nsa_cache4_decode`` needs (0 = sizes not accepted)."""
+    return int(load_library().nsa_cache4_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S))
+
+
+def nsa_cache4_decode_raw(q, k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table, cache_lens, block_idx,
+                          out, lse, B, Hq, Hkv, D, page_size, max_pages, num_pages, S, workspace, workspace_bytes,
+                          stream=0) -> int:
+    """Direct C call with integer device pointers (the factors, block_idx and
+    lse may be None); returns the bsa_status."""
+    return load_library().nsa_cache4_decode(q, k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table,
+                                            cache_lens, block_idx, out, lse, B, Hq, Hkv, D, page_size, max_pages,
+                                            num_pages, S, workspace, int(workspace_bytes), stream)
 
 
 @contextlib.contextmanager
@@ -864,6 +945,459 @@ def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
                                v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(),
                                None if idx is None else idx.data_ptr(), out.data_ptr(),
                                None if lse is None else lse.data_ptr(), B, Hq, Hkv, D, page_size, max_pages, pages, S,
+                               workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, what)
+    if written:
+        torch.autograd.graph.increment_version(written)
+    return (out, lse) if return_lse else out
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: int = 0, fast: float = 32.0, slow: float = 1.0, device=None):
+    """``(inv_freq, rotary_scale)`` of a rotation over ``rotary_dim`` elements, for ``qk_norm_rope`` and the cache
+    appends: ``base ** (-2 j / rotary_dim)``, for contexts ``factor`` times as long as the ``original_length`` of
+    training scaled by
+
+    * ``"linear"``: every frequency over ``factor``;
+    * ``"base"``: the base times ``factor ** (r / (r - 2))``, which leaves the fastest pair and divides the slowest;
+    * ``"bands"``: pairs that make more than ``fast`` turns over ``original_length`` as they are, those under ``slow``
+      turns over ``factor``, those between in proportion, and ``rotary_scale = 0.1 ln(factor) + 1``.
+
+    ``inv_freq`` is float32, ``rotary_scale`` a number (1 but for ``"bands"``).
+    """
+    import math
+
+    import torch
+
+    if rotary_dim < 2 or rotary_dim % 2 or not base > 1.0 or not factor >= 1.0:
+        raise BsaError("rope_frequencies: an even rotary_dim, base > 1 and factor >= 1 expected", 2)
+    if scaling not in ("none", "linear", "base", "bands"):
+        raise BsaError(f"rope_frequencies: unknown scaling {scaling!r}", 4)
+    if scaling == "base" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        if original_length < 1 or not fast > slow:
+            raise BsaError("rope_frequencies: bands need original_length and fast > slow", 2)
+        keep = ((f * original_length / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        scale = 0.1 * math.log(factor) + 1.0
+    return f.to(device=device, dtype=torch.float32), scale
+
+
+def _row_strides(t):
+    """``t`` [B, H, T, D] as the kernels read rows in place, and its (batch, head, token) strides; a copy where a row's
+    elements do not follow each other or do not start on a 16-byte boundary."""
+    unit = 16 // t.element_size()
+    sizes, st = t.shape, t.stride()
+    s = [0 if n == 1 else x for n, x in zip(sizes, st)]
+    if st[3] != 1 or s[0] % unit or s[1] % unit or s[2] % unit or t.data_ptr() % 16:
+        t = t.contiguous()
+        if t.data_ptr() % 16:
+            t = t.clone()
+        s = t.stride()
+    return t, s[:3]
+
+
+def _rows_like(torch, t):
+    """An empty tensor of ``t``'s shape, heads inside tokens where t's are (so a projection's gradient is as it was)."""
+    if t.stride(1) < t.stride(2):
+        return torch.empty((t.shape[0], t.shape[2], t.shape[1], t.shape[3]), dtype=t.dtype,
+                           device=t.device).transpose(1, 2)
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _aligned(t):
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _row_parameters(torch, what, q_weight, k_weight, inv_freq, D):
+    """Weights of one dtype and frequencies as the kernels take them; (q_weight, k_weight, their dtype, inv_freq)."""
+    kind = BSA_F32
+    given = [w for w in (q_weight, k_weight) if w is not None]
+    if given:
+        if any(w.shape != (D,) for w in given):
+            raise BsaError(f"{what}: weights must be [{D}]", 2)
+        if all(w.dtype is torch.bfloat16 for w in given):
+            kind = BSA_BF16
+        elif any(w.dtype not in (torch.bfloat16, torch.float32) for w in given):
+            raise BsaError(f"{what}: weights must be float32 or bfloat16", 3)
+        if kind == BSA_F32:
+            q_weight, k_weight = (None if w is None else w.to(torch.float32) for w in (q_weight, k_weight))
+        q_weight, k_weight = (None if w is None else _aligned(w.contiguous()) for w in (q_weight, k_weight))
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise BsaError(f"{what}: inv_freq must be [rotary_dim / 2]", 2)
+        inv_freq = _aligned(inv_freq.to(torch.float32).contiguous()) if inv_freq.numel() else None
+    return q_weight, k_weight, kind, inv_freq
+
+
+def _row_inputs(torch, what, q, k, q_weight, k_weight, inv_freq, positions):
+    """Checks of ``qk_norm_rope``'s inputs; (q_weight, k_weight, their dtype, inv_freq, positions)."""
+    if q.dim() != 4 or k.dim() != 4 or q.shape[0] != k.shape[0] or q.shape[2:] != k.shape[2:]:
+        raise BsaError(f"{what}: q [B,Hq,T,D] and k [B,Hkv,T,D] expected", 2)
+    if q.dtype != k.dtype:
+        raise BsaError(f"{what}: q and k must share one dtype", 3)
+    B, T = q.shape[0], q.shape[2]
+    if positions is not None:
+        if positions.shape not in ((B, T), (T,)):
+            raise BsaError(f"{what}: positions must be [B,T] or [T]", 2)
+        positions = _int32(torch, positions.expand(B, T))
+    return (*_row_parameters(torch, what, q_weight, k_weight, inv_freq, q.shape[3]), positions)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, interleaved: bool = False,
+                         rotary_scale: float = 1.0, eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head and its rotation by position, in
+    one pass: ``(q_out [B, Hq, T, D], k_out [B, Hkv, T, D])``, contiguous, for
+    the attention calls.
+
+    q, k bf16 or fp32, read in place by their strides (views of a fused
+    projection ``[B, T, heads, D]`` among them).  ``q_weight``/``k_weight [D]``
+    (None: that one is not normalised), ``inv_freq [rotary_dim / 2]`` (None: no
+    rotation; ``rope_frequencies`` makes them) with pairs halves apart or
+    neighbours if ``interleaved``, ``positions [B, T]`` or ``[T]`` (None: 0 ..
+    T - 1); the rotated elements are multiplied by ``rotary_scale``.  Arithmetic
+    is fp32, rounded once.  Where autograd records, tensors that require a
+    gradient are refused: ``qk_norm_rope`` has one.  Runs on ``stream`` (default:
+    torch's current stream) without synchronising.
+    """
+    import torch
+
+    what = "qk_norm_rope_forward"
+    if torch.is_grad_enabled():
+        _no_gradient(what, q, k, q_weight, k_weight, inv_freq, q_out, k_out)
+    dev = _one_device(what, q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on_stream(torch, q.device, stream):
+            return qk_norm_rope_forward(q, k, q_weight, k_weight, inv_freq, positions, interleaved, rotary_scale, eps,
+                                        q_out, k_out)
+    qw, kw, kind, freq, pos = _row_inputs(torch, what, q, k, q_weight, k_weight, inv_freq, positions)
+    B, Hq, T, D = q.shape
+    Hkv = k.shape[1]
+    written = []
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is not None:
+            _in_place(what, name, t, like.shape, like.dtype)
+            written.append(t)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    (q, qs), (k, ks) = _row_strides(q), _row_strides(k)
+    st = qk_norm_rope_forward_raw(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(qw), _ptr(kw),
+                                  _ptr(pos), _ptr(freq), (*qs, *ks, Hq * T * D, T * D, D, Hkv * T * D, T * D, D), B,
+                                  Hq, Hkv, T, D, 0 if freq is None else 2 * freq.numel(), interleaved, rotary_scale,
+                                  eps, _dtype_code(q), kind, torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, what)
+    if written:
+        torch.autograd.graph.increment_version(written)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_freq=None, positions=None,
+                          interleaved: bool = False, rotary_scale: float = 1.0, eps: float = 1e-6, workspace=None,
+                          stream=None):
+    """Gradients ``(dq, dk, dq_weight, dk_weight)`` of ``qk_norm_rope_forward``
+    for the upstream gradients ``dq_out``, ``dk_out`` of its results.
+
+    Arguments as for the forward; dq and dk lie in memory as q and k do (heads
+    inside tokens, or tokens inside heads), the weights' gradients are fp32
+    (None without weights).  Results repeat bit for bit.  ``workspace`` is a
+    uint8 CUDA tensor of at least ``qk_norm_rope_backward_workspace_size(...)``
+    bytes (allocated when None).  Runs on ``stream`` (default: torch's current
+    stream) without synchronising.
+    """
+    import torch
+
+    what = "qk_norm_rope_backward"
+    dev = _one_device(what, q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions, workspace)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on_stream(torch, q.device, stream):
+            return qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions, interleaved,
+                                         rotary_scale, eps, workspace)
+    qw, kw, kind, freq, pos = _row_inputs(torch, what, q, k, q_weight, k_weight, inv_freq, positions)
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise BsaError(f"{what}: dq_out and dk_out must have the shapes of q and k", 2)
+    if dq_out.dtype != q.dtype or dk_out.dtype != k.dtype:
+        raise BsaError(f"{what}: dq_out and dk_out must have the dtype of q and k", 3)
+    B, Hq, T, D = q.shape
+    Hkv = k.shape[1]
+    if workspace is None:
+        workspace = torch.empty(max(qk_norm_rope_backward_workspace_size(B, Hq, Hkv, T, D), 1), device=q.device,
+                                dtype=torch.uint8)
+    elif not workspace.is_contiguous():
+        raise BsaError(f"{what}: workspace must be contiguous", 2)
+    dq, dk = _rows_like(torch, q), _rows_like(torch, k)
+    dqw, dkw = (None if w is None else torch.empty(D, dtype=torch.float32, device=q.device) for w in (qw, kw))
+    rows = [_row_strides(t) for t in (q, k, dq_out, dk_out)]
+    strides = [x for _, s in rows for x in s] + [*dq.stride()[:3], *dk.stride()[:3]]
+    st = qk_norm_rope_backward_raw(*(t.data_ptr() for t, _ in rows), dq.data_ptr(), dk.data_ptr(), _ptr(dqw), _ptr(dkw),
+                                   _ptr(qw), _ptr(kw), _ptr(pos), _ptr(freq), strides, B, Hq, Hkv, T, D,
+                                   0 if freq is None else 2 * freq.numel(), interleaved, rotary_scale, eps,
+                                   _dtype_code(q), kind, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(),
+                                   torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, what)
+    return dq, dk, dqw, dkw
+
+
+_ROPE_FUNCTION = None
+
+
+def _rope_function():
+    """The autograd function of the norm and rotation of query and key heads."""
+    global _ROPE_FUNCTION
+    if _ROPE_FUNCTION is None:
+        import torch
+        from torch.autograd.function import once_differentiable
+
+        class QkNormRopeFunction(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, q_weight, k_weight, inv_freq, positions, interleaved, rotary_scale, eps):
+                ctx.save_for_backward(q, k, q_weight, k_weight, inv_freq, positions)
+                ctx.rest = bool(interleaved), float(rotary_scale), float(eps)
+                return qk_norm_rope_forward(q, k, q_weight, k_weight, inv_freq, positions, *ctx.rest)
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dq_out, dk_out):
+                q, k, q_weight, k_weight, inv_freq, positions = ctx.saved_tensors
+                dq, dk, dqw, dkw = qk_norm_rope_backward(q, k, dq_out.to(q.dtype), dk_out.to(k.dtype), q_weight,
+                                                         k_weight, inv_freq, positions, *ctx.rest)
+                dqw = None if dqw is None else dqw.to(q_weight.dtype)
+                dkw = None if dkw is None else dkw.to(k_weight.dtype)
+                return dq, dk, dqw, dkw, None, None, None, None, None
+
+        _ROPE_FUNCTION = QkNormRopeFunction
+    return _ROPE_FUNCTION
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, interleaved: bool = False,
+                 rotary_scale: float = 1.0, eps: float = 1e-6):
+    """``qk_norm_rope_forward`` with autograd: gradients with respect to q, k
+    and the weights come from ``qk_norm_rope_backward`` (frequencies have
+    none).  Runs on the current stream of the tensors' device, whichever
+    device is current.  To capture a training step into a CUDA graph, capture
+    forward and backward together, with no graph of the same leaves left from
+    outside the capture.
+    """
+    import torch
+
+    if torch.is_grad_enabled():
+        _no_gradient("qk_norm_rope with respect to inv_freq", inv_freq)
+    with torch.cuda.device(_one_device("qk_norm_rope", q, k, q_weight, k_weight, inv_freq, positions)):
+        return _rope_function().apply(q, k, q_weight, k_weight, inv_freq, positions, interleaved, rotary_scale, eps)
+
+
+def _check_cache4(torch, what, k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table, cache_lens, B, Hkv,
+                  D):
+    """Shapes and types of the paged 4-bit cache; returns (num_pages, page_size, max_pages)."""
+    if k_cache.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != B or cache_lens.shape != (B,):
+        raise BsaError(f"{what}: k_cache [pages,Hkv,page_size,D/2], page_table [B,max_pages], cache_lens [B] expected",
+                       2)
+    pages, _, page_size, _ = k_cache.shape
+    codes, scales = (pages, Hkv, page_size, D // 2), (pages, Hkv, page_size, D // 16)
+    if not (k_cache.shape == codes and v_cache.shape == codes and k_scale.shape == scales and v_scale.shape == scales
+            and k_cache.dtype is torch.uint8 and v_cache.dtype is torch.uint8
+            and k_scale.dtype in (torch.float8_e4m3fn, torch.uint8)
+            and v_scale.dtype in (torch.float8_e4m3fn, torch.uint8) and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            _in_place(what, name, t, codes, torch.uint8)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _in_place(what, name, t, scales, torch.float8_e4m3fn, torch.uint8)
+    for name, t in (("k_factor", k_factor), ("v_factor", v_factor)):
+        if t is not None:
+            _in_place(what, name, t, (Hkv,), torch.float32)
+    return pages, page_size, page_table.shape[1]
+
+
+def nsa_cache4_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens=None, inv_freq=None,
+                      interleaved: bool = False, q=None, q_out=None, q_weight=None, k_weight=None,
+                      rotary_scale: float = 1.0, eps: float = 1e-6, k_factor=None, v_factor=None, stream=None):
+    """Writes the keys and values of new tokens into a paged cache of 4-bit
+    codes, in place, keys normalised and rotated by position on the way.
+
+    As ``nsa_cache_append`` but for the cache: ``k_cache``/``v_cache [pages,
+    Hkv, page_size, D / 2]`` uint8 (two e2m1 codes a byte, the first in the low
+    half), ``k_scale``/``v_scale [pages, Hkv, page_size, D / 16]`` float8_e4m3fn
+    (or uint8 codes): a scale for every 16 elements of a token; and
+    ``k_factor``/``v_factor [Hkv]`` fp32, optional factors of the heads, the same
+    in every call on a cache.  k, v and q are read in place by their strides;
+    ``q_weight``/``k_weight [D]`` (None: not normalised), ``rotary_scale`` and
+    ``eps`` are those of ``qk_norm_rope_forward``.  Returns the queries,
+    normalised and rotated (None without q).  Has no gradient: where autograd
+    records, tensors that require one are refused.  Runs on ``stream`` (default:
+    torch's current stream) without synchronising.
+    """
+    import torch
+
+    what = "nsa_cache4_append"
+    if torch.is_grad_enabled():
+        _no_gradient(what, k, v, q, q_out, k_scale, v_scale, inv_freq, q_weight, k_weight, k_factor, v_factor)
+    dev = _one_device(what, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens, inv_freq, q,
+                      q_out, q_weight, k_weight, k_factor, v_factor)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on_stream(torch, k.device, stream):
+            return nsa_cache4_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens,
+                                     inv_freq, interleaved, q, q_out, q_weight, k_weight, rotary_scale, eps, k_factor,
+                                     v_factor)
+    if k.dim() != 4 or k.shape != v.shape or (q is not None and q.dim() != 4):
+        raise BsaError("k, v [B,Hkv,n,D] and q [B,Hq,n,D] expected", 2)
+    B, Hkv, n, D = k.shape
+    Hq = Hkv if q is None else q.shape[1]
+    pages, page_size, max_pages = _check_cache4(torch, what, k_cache, v_cache, k_scale, v_scale, k_factor, v_factor,
+                                                page_table, cache_lens, B, Hkv, D)
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise BsaError("k, v, q must share one dtype", 3)
+    if q is not None and q.shape != (B, Hq, n, D):
+        raise BsaError("q must be [B,Hq,n,D] with k's B, n and D", 2)
+    if q is None and (q_out is not None or q_weight is not None):
+        raise BsaError("q_out or q_weight given without q")
+    if q_out is not None:
+        _in_place(what, "q_out", q_out, q.shape, q.dtype)
+    if new_lens is not None and new_lens.shape != (B,):
+        raise BsaError("new_lens must be [B]", 2)
+    qw, kw, kind, freq = _row_parameters(torch, what, q_weight, k_weight, inv_freq, D)
+    (k, ks), (v, vs) = _row_strides(k), _row_strides(v)
+    strides = [*ks, *vs, 0, 0, 0]
+    table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
+    news = None if new_lens is None else _int32(torch, new_lens)
+    written = [k_cache, v_cache, k_scale, v_scale]
+    if q is not None:
+        if q_out is not None:
+            written.append(q_out)
+        else:
+            make = torch.empty if news is None else torch.zeros
+            q_out = make(q.shape, dtype=q.dtype, device=q.device)
+        q, strides[6:] = _row_strides(q)
+    st = nsa_cache4_append_raw(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+                               k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_factor), _ptr(v_factor), table.data_ptr(),
+                               lens.data_ptr(), _ptr(news), _ptr(qw), _ptr(kw), _ptr(freq), strides, B, Hq, Hkv, n, D,
+                               page_size, max_pages, pages, 0 if freq is None else 2 * freq.numel(), interleaved,
+                               rotary_scale, eps, _dtype_code(k), kind, torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, what)
+    torch.autograd.graph.increment_version(written)  # a graph that saved one of them must not use it any more
+    return q_out
+
+
+def nsa_cache4_read(k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, n: int, starts=None, k_factor=None,
+                    v_factor=None, dtype=None, k_out=None, v_out=None, stream=None):
+    """The values that the 4-bit cache holds of tokens ``starts[b] + i``, ``i <
+    n`` (``starts`` None: the first n): ``(k, v)``, each ``[B, Hkv, n, D]`` of
+    ``dtype`` (bf16 or fp32; default bf16, or that of ``k_out``).
+
+    The cache, its factors and ``cache_lens`` as ``nsa_cache4_append`` left
+    them, the new tokens counted.  Rows past a sequence's length are zero.  Runs on ``stream`` (default: torch's
+    current stream) without synchronising.
+    """
+    import torch
+
+    what = "nsa_cache4_read"
+    if torch.is_grad_enabled():
+        _no_gradient(what, k_scale, v_scale, k_factor, v_factor, k_out, v_out)
+    dev = _one_device(what, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, starts, k_factor, v_factor,
+                      k_out, v_out)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on_stream(torch, k_cache.device, stream):
+            return nsa_cache4_read(k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, n, starts, k_factor,
+                                   v_factor, dtype, k_out, v_out)
+    if k_cache.dim() != 4 or page_table.dim() != 2:
+        raise BsaError("k_cache [pages,Hkv,page_size,D/2] and page_table [B,max_pages] expected", 2)
+    B, Hkv, D = page_table.shape[0], k_cache.shape[1], 2 * k_cache.shape[3]
+    pages, page_size, max_pages = _check_cache4(torch, what, k_cache, v_cache, k_scale, v_scale, k_factor, v_factor,
+                                                page_table, cache_lens, B, Hkv, D)
+    if starts is not None and starts.shape != (B,):
+        raise BsaError("starts must be [B]", 2)
+    if (k_out is None) != (v_out is None):
+        raise BsaError(f"{what}: give k_out and v_out together")
+    if dtype is None:
+        dtype = torch.bfloat16 if k_out is None else k_out.dtype
+    shape, written = (B, Hkv, n, D), []
+    if k_out is not None:
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            _in_place(what, name, t, shape, dtype)
+            written.append(t)
+    else:
+        if n < 1:
+            raise BsaError(f"{what}: n must be at least 1", 2)
+        k_out, v_out = torch.empty((2, *shape), dtype=dtype, device=k_cache.device)
+    table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
+    begin = None if starts is None else _int32(torch, starts)
+    st = nsa_cache4_read_raw(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                             _ptr(k_factor), _ptr(v_factor), table.data_ptr(), _ptr(begin), lens.data_ptr(),
+                             k_out.data_ptr(), v_out.data_ptr(), B, Hkv, n, D, page_size, max_pages, pages,
+                             _dtype_code(k_out), torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, what)
+    if written:
+        torch.autograd.graph.increment_version(written)
+    return k_out, v_out
+
+
+def nsa_cache4_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx=None, k_factor=None,
+                      v_factor=None, out=None, lse=None, return_lse: bool = False, workspace=None, stream=None):
+    """``nsa_select_decode`` over the paged 4-bit cache that
+    ``nsa_cache4_append`` fills.
+
+    q ``[B, Hq, 1, D]`` bf16 (normalised and rotated), the cache and its factors
+    as for ``nsa_cache4_append``, everything else as for ``nsa_select_decode``
+    (``workspace``: ``nsa_cache4_decode_workspace_size(...)`` bytes).
+    """
+    import torch
+
+    what = "nsa_cache4_decode"
+    if torch.is_grad_enabled():
+        _no_gradient(what, q, k_scale, v_scale, k_factor, v_factor, out, lse)
+    dev = _one_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx, k_factor,
+                      v_factor, out, lse, workspace)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on_stream(torch, q.device, stream):
+            return nsa_cache4_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, block_idx,
+                                     k_factor, v_factor, out, lse, return_lse, workspace)
+    if q.dim() != 4 or q.shape[2] != 1 or k_cache.dim() != 4:
+        raise BsaError("q [B,Hq,1,D] and k_cache [pages,Hkv,page_size,D/2] expected", 2)
+    if q.dtype != torch.bfloat16:
+        raise BsaError("nsa_cache4_decode takes bfloat16 q", 3)
+    B, Hq, _, D = q.shape
+    Hkv = k_cache.shape[1]
+    pages, page_size, max_pages = _check_cache4(torch, what, k_cache, v_cache, k_scale, v_scale, k_factor, v_factor,
+                                                page_table, cache_lens, B, Hkv, D)
+    S = 0
+    if block_idx is not None:
+        S = block_idx.shape[-1]
+        if block_idx.shape != (B, Hkv, 1, S):
+            raise BsaError("block_idx must be [B,Hkv,1,S]", 2)
+    written = []
+    if out is not None:
+        _in_place(what, "out", out, q.shape, torch.bfloat16)
+        written.append(out)
+    if lse is not None:
+        _in_place(what, "lse", lse, (B, Hq, 1), torch.float32)
+        written.append(lse)
+    q = _aligned(q.contiguous())
+    table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
+    idx = None if block_idx is None else _int32(torch, block_idx)
+    if workspace is None:
+        need = nsa_cache4_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S)
+        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    elif not workspace.is_contiguous():
+        raise BsaError(f"{what}: workspace must be contiguous", 2)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and return_lse:
+        lse = torch.empty((B, Hq, 1), device=q.device, dtype=torch.float32)
+    st = nsa_cache4_decode_raw(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                               v_scale.data_ptr(), _ptr(k_factor), _ptr(v_factor), table.data_ptr(), lens.data_ptr(),
+                               _ptr(idx), out.data_ptr(), _ptr(lse), B, Hq, Hkv, D, page_size, max_pages, pages, S,
                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                torch.cuda.current_stream(dev).cuda_stream)
     _check(st, what)

@@ -107,6 +107,57 @@ int check_cache_shape(int B, int Hq, int Hkv, int D, int page_size, int max_page
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+bool finite_value(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// Norm and rotation of rows: sizes and parameters of qk_norm_rope and nsa_cache4_append.
+int check_rows(int D, int rotary_dim, float rotary_scale, float eps) {
+  if (D < 16 || D > 128 || D % 16 != 0) return BSA_ERR_UNSUPPORTED;
+  if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 16 != 0) return BSA_ERR_UNSUPPORTED;
+  if (!finite_value(rotary_scale) || !(eps > 0.0f) || !finite_value(eps)) return BSA_ERR_UNSUPPORTED;
+  return BSA_OK;
+}
+// `count` tensors' strides (batch, head, token) from the caller's list, or those of contiguous [., heads[i], T, D].
+int take_strides(const int64_t* from, int count, const int* heads, int T, int D, int elsize, int64_t (*to)[3]) {
+  for (int i = 0; i < count; ++i) {
+    const int64_t own[3] = {static_cast<int64_t>(heads[i]) * T * D, static_cast<int64_t>(T) * D, D};
+    for (int j = 0; j < 3; ++j) {
+      to[i][j] = from != nullptr ? from[3 * i + j] : own[j];
+      if (to[i][j] < 0 || to[i][j] >= (1LL << 40)) return BSA_ERR_SHAPE;
+      if (to[i][j] * elsize % 16 != 0) return BSA_ERR_ALIGN;
+    }
+  }
+  return BSA_OK;
+}
+int check_dtypes(int dtype, int weight_dtype) {
+  if (dtype != BSA_F32 && dtype != BSA_BF16) return BSA_ERR_DTYPE;
+  if (weight_dtype != BSA_F32 && weight_dtype != BSA_BF16) return BSA_ERR_DTYPE;
+  return BSA_OK;
+}
+int check_rope_shape(int B, int Hq, int Hkv, int T, int D) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || Hq > 65535 || Hkv > 65535) return BSA_ERR_SHAPE;
+  if (static_cast<long long>(B) * T > 0x7fffffffLL) return BSA_ERR_SHAPE;
+  if (static_cast<long long>(B) * T * (Hq > Hkv ? Hq : Hkv) >= (1LL << 40) / (D > 0 ? D : 1)) return BSA_ERR_SHAPE;
+  return BSA_OK;
+}
+// The 4-bit cache's tensors.
+int check_cache4(const Cache4& c, int Hq) {
+  if (c.k == nullptr || c.v == nullptr || c.k_scale == nullptr || c.v_scale == nullptr || c.table == nullptr)
+    return BSA_ERR_NULLPTR;
+  const int sh = check_cache_shape(c.B, Hq, c.Hkv, c.D, c.page, c.max_pages, c.num_pages);
+  if (sh != BSA_OK) return sh;
+  const void* ptrs[4] = {c.k, c.v, c.k_scale, c.v_scale};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return BSA_ERR_ALIGN;
+  return aligned4(c.k_factor) && aligned4(c.v_factor) && aligned4(c.table) ? BSA_OK : BSA_ERR_ALIGN;
+}
+Cache4 cache4_of(const void* k, const void* v, const void* k_scale, const void* v_scale, const float* k_factor,
+                 const float* v_factor, const int32_t* table, int B, int Hkv, int D, int page, int max_pages,
+                 int num_pages) {
+  auto bytes = [](const void* p) { return static_cast<uint8_t*>(const_cast<void*>(p)); };
+  return {bytes(k), bytes(v), bytes(k_scale), bytes(v_scale), k_factor, v_factor, table,
+          B,        Hkv,      D,              page,           max_pages, num_pages};
+}
+
 // The kernels are built for sm_103a only; refuse other devices up front
 // instead of failing inside the launch.
 int check_device() {
@@ -495,6 +546,174 @@ int nsa_select_decode(const void* q, const void* k_cache, const void* v_cache, c
                            Hkv, D, page_size, max_pages, num_pages, S, workspace, stream);
 }
 
+int qk_norm_rope_forward(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
+                         const void* k_weight, const int32_t* positions, const float* inv_freq,
+                         const int64_t* strides, int B, int Hq, int Hkv, int T, int D, int rotary_dim, int interleaved,
+                         float rotary_scale, float eps, int dtype, int weight_dtype, cudaStream_t stream) {
+  if (q == nullptr || k == nullptr || q_out == nullptr || k_out == nullptr || (rotary_dim != 0 && inv_freq == nullptr))
+    return BSA_ERR_NULLPTR;
+  int st = check_dtypes(dtype, weight_dtype);
+  if (st == BSA_OK) st = check_rope_shape(B, Hq, Hkv, T, D);
+  if (st == BSA_OK) st = check_rows(D, rotary_dim, rotary_scale, eps);
+  if (st != BSA_OK) return st;
+  RopeCall r{};
+  const int heads[4] = {Hq, Hkv, Hq, Hkv};
+  int64_t to[4][3];
+  st = take_strides(strides, 4, heads, T, D, dtype == BSA_F32 ? 4 : 2, to);
+  if (st != BSA_OK) return st;
+  const void* ptrs[7] = {q, k, q_out, k_out, q_weight, k_weight, inv_freq};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return BSA_ERR_ALIGN;
+  if (!aligned4(positions)) return BSA_ERR_ALIGN;
+  for (int s = 0; s < 2; ++s)
+    for (int j = 0; j < 3; ++j) {
+      r.x_stride[s][j] = to[s][j];
+      r.out_stride[s][j] = to[2 + s][j];
+    }
+  r.q = q; r.k = k; r.q_out = q_out; r.k_out = k_out;
+  r.q_weight = q_weight; r.k_weight = k_weight;
+  r.positions = positions; r.inv_freq = inv_freq;
+  r.B = B; r.Hq = Hq; r.Hkv = Hkv; r.T = T; r.D = D; r.rotary = rotary_dim;
+  r.interleaved = interleaved != 0; r.weight_f32 = weight_dtype == BSA_F32; r.f32 = dtype == BSA_F32;
+  r.factor = rotary_scale; r.eps = eps;
+  const int dev = check_device();
+  return dev != OK ? dev : launch_qk_rope_forward(r, stream);
+}
+
+size_t qk_norm_rope_backward_workspace_size(int B, int Hq, int Hkv, int T, int D) {
+  if (check_rope_shape(B, Hq, Hkv, T, D) != BSA_OK || check_rows(D, 0, 1.0f, 1.0f) != BSA_OK) return 0;
+  return qk_rope_backward_workspace_bytes(B, Hq, Hkv, T, D);
+}
+
+int qk_norm_rope_backward(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                          float* dq_weight, float* dk_weight, const void* q_weight, const void* k_weight,
+                          const int32_t* positions, const float* inv_freq, const int64_t* strides, int B, int Hq,
+                          int Hkv, int T, int D, int rotary_dim, int interleaved, float rotary_scale, float eps,
+                          int dtype, int weight_dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (q == nullptr || k == nullptr || dq_out == nullptr || dk_out == nullptr || dq == nullptr || dk == nullptr ||
+      workspace == nullptr || (rotary_dim != 0 && inv_freq == nullptr) ||
+      (q_weight != nullptr && dq_weight == nullptr) || (k_weight != nullptr && dk_weight == nullptr))
+    return BSA_ERR_NULLPTR;
+  int st = check_dtypes(dtype, weight_dtype);
+  if (st == BSA_OK) st = check_rope_shape(B, Hq, Hkv, T, D);
+  if (st == BSA_OK) st = check_rows(D, rotary_dim, rotary_scale, eps);
+  if (st != BSA_OK) return st;
+  RopeCall r{};
+  const int heads[6] = {Hq, Hkv, Hq, Hkv, Hq, Hkv};
+  int64_t to[6][3];
+  st = take_strides(strides, 6, heads, T, D, dtype == BSA_F32 ? 4 : 2, to);
+  if (st != BSA_OK) return st;
+  const void* ptrs[9] = {q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, inv_freq};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return BSA_ERR_ALIGN;
+  if (!aligned4(positions) || !aligned4(dq_weight) || !aligned4(dk_weight) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return BSA_ERR_ALIGN;
+  const size_t need = qk_norm_rope_backward_workspace_size(B, Hq, Hkv, T, D);
+  if (need == 0) return BSA_ERR_SHAPE;
+  if (workspace_bytes < need) return BSA_ERR_SCRATCH_LIMIT;
+  for (int s = 0; s < 2; ++s)
+    for (int j = 0; j < 3; ++j) {
+      r.x_stride[s][j] = to[s][j];
+      r.dy_stride[s][j] = to[2 + s][j];
+      r.out_stride[s][j] = to[4 + s][j];
+    }
+  r.q = q; r.k = k; r.dq_out = dq_out; r.dk_out = dk_out; r.q_out = dq; r.k_out = dk;
+  r.q_weight = q_weight; r.k_weight = k_weight;
+  r.dq_weight = q_weight != nullptr ? dq_weight : nullptr;
+  r.dk_weight = k_weight != nullptr ? dk_weight : nullptr;
+  r.positions = positions; r.inv_freq = inv_freq;
+  r.B = B; r.Hq = Hq; r.Hkv = Hkv; r.T = T; r.D = D; r.rotary = rotary_dim;
+  r.interleaved = interleaved != 0; r.weight_f32 = weight_dtype == BSA_F32; r.f32 = dtype == BSA_F32;
+  r.factor = rotary_scale; r.eps = eps;
+  const int dev = check_device();
+  return dev != OK ? dev : launch_qk_rope_backward(r, workspace, stream);
+}
+
+int nsa_cache4_append(const void* k, const void* v, const void* q, void* q_out, void* k_cache, void* v_cache,
+                      void* k_scale, void* v_scale, const float* k_factor, const float* v_factor,
+                      const int32_t* page_table, const int32_t* cache_lens, const int32_t* new_lens,
+                      const void* q_weight, const void* k_weight, const float* inv_freq, const int64_t* strides, int B,
+                      int Hq, int Hkv, int n, int D, int page_size, int max_pages, int num_pages, int rotary_dim,
+                      int interleaved, float rotary_scale, float eps, int dtype, int weight_dtype,
+                      cudaStream_t stream) {
+  if (k == nullptr || v == nullptr || cache_lens == nullptr || (q == nullptr) != (q_out == nullptr) ||
+      (rotary_dim != 0 && inv_freq == nullptr))
+    return BSA_ERR_NULLPTR;
+  Append4Call r{};
+  r.cache = cache4_of(k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table, B, Hkv, D, page_size,
+                      max_pages, num_pages);
+  int st = check_dtypes(dtype, weight_dtype);
+  if (st == BSA_OK) st = check_cache4(r.cache, Hq);
+  if (st != BSA_OK) return st;
+  if (n < 1 || static_cast<long long>(B) * n > 0x7fffffffLL || static_cast<long long>(B) * Hq * n >= (1LL << 40) / D)
+    return BSA_ERR_SHAPE;
+  st = check_rows(D, rotary_dim, rotary_scale, eps);
+  if (st != BSA_OK) return st;
+  const int heads[3] = {Hkv, Hkv, Hq};
+  int64_t to[3][3];
+  st = take_strides(strides, q != nullptr ? 3 : 2, heads, n, D, dtype == BSA_F32 ? 4 : 2, to);
+  if (st != BSA_OK) return st;
+  const void* ptrs[7] = {k, v, q, q_out, q_weight, k_weight, inv_freq};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return BSA_ERR_ALIGN;
+  if (!aligned4(cache_lens) || !aligned4(new_lens)) return BSA_ERR_ALIGN;
+  for (int j = 0; j < 3; ++j) {
+    r.stride[1][j] = to[0][j];
+    r.stride[2][j] = to[1][j];
+    r.stride[0][j] = q != nullptr ? to[2][j] : 0;
+  }
+  r.k = k; r.v = v; r.q = q; r.q_out = q_out;
+  r.q_weight = q_weight; r.k_weight = k_weight;
+  r.lens = cache_lens; r.new_lens = new_lens; r.inv_freq = inv_freq;
+  r.Hq = Hq; r.n = n; r.rotary = rotary_dim;
+  r.interleaved = interleaved != 0; r.weight_f32 = weight_dtype == BSA_F32; r.f32 = dtype == BSA_F32;
+  r.factor = rotary_scale; r.eps = eps;
+  const int dev = check_device();
+  return dev != OK ? dev : launch_nsa_cache4_append(r, stream);
+}
+
+int nsa_cache4_read(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                    const float* k_factor, const float* v_factor, const int32_t* page_table, const int32_t* starts,
+                    const int32_t* cache_lens, void* k_out, void* v_out, int B, int Hkv, int n, int D, int page_size,
+                    int max_pages, int num_pages, int dtype, cudaStream_t stream) {
+  if (cache_lens == nullptr || k_out == nullptr || v_out == nullptr) return BSA_ERR_NULLPTR;
+  if (dtype != BSA_F32 && dtype != BSA_BF16) return BSA_ERR_DTYPE;
+  const Cache4 c = cache4_of(k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table, B, Hkv, D, page_size,
+                             max_pages, num_pages);
+  const int st = check_cache4(c, Hkv);
+  if (st != BSA_OK) return st;
+  if (n < 1 || static_cast<long long>(B) * Hkv * n >= (1LL << 40) / D) return BSA_ERR_SHAPE;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(starts) || !aligned4(cache_lens)) return BSA_ERR_ALIGN;
+  const int dev = check_device();
+  return dev != OK ? dev : launch_nsa_cache4_read(c, starts, cache_lens, k_out, v_out, n, dtype == BSA_F32, stream);
+}
+
+size_t nsa_cache4_decode_workspace_size(int B, int Hq, int Hkv, int D, int page_size, int max_pages, int S) {
+  return nsa_select_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S);
+}
+
+int nsa_cache4_decode(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                      const void* v_scale, const float* k_factor, const float* v_factor, const int32_t* page_table,
+                      const int32_t* cache_lens, const int32_t* block_idx, void* out, float* lse, int B, int Hq,
+                      int Hkv, int D, int page_size, int max_pages, int num_pages, int S, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream) {
+  if (q == nullptr || cache_lens == nullptr || out == nullptr || workspace == nullptr) return BSA_ERR_NULLPTR;
+  const Cache4 c = cache4_of(k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table, B, Hkv, D, page_size,
+                             max_pages, num_pages);
+  const int st = check_cache4(c, Hq);
+  if (st != BSA_OK) return st;
+  if (block_idx != nullptr ? (S < 1 || S > 32) : S != 0) return BSA_ERR_SHAPE;
+  const void* ptrs[3] = {q, out, workspace};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return BSA_ERR_ALIGN;
+  if (!aligned4(cache_lens) || !aligned4(block_idx) || !aligned4(lse)) return BSA_ERR_ALIGN;
+  if (workspace_bytes < nsa_cache4_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S))
+    return BSA_ERR_SCRATCH_LIMIT;
+  const int dev = check_device();
+  return dev != OK ? dev : launch_nsa_decode4(c, q, cache_lens, block_idx, out, lse, Hq, S, workspace, stream);
+}
+
 const char* bsa_status_string(int status) {
   switch (status) {
     case BSA_OK: return "success";
@@ -555,10 +774,10 @@ int bsa_read_probe(const void* buf, size_t bytes, int reps, unsigned int* sink, 
 }
 
 int bsa_device_error(void) {
-  const unsigned codes[10] = {tra_bf16_device_error(), tra_f32_device_error(), nsa_device_error(),
+  const unsigned codes[11] = {tra_bf16_device_error(), tra_f32_device_error(), nsa_device_error(),
                               tra_bwd_device_error(), tra_diff_device_error(), nsa_fsa_device_error(),
                               nsa_bwd_device_error(), nsa_bwd_tc_device_error(), nsa_decode_device_error(),
-                              selftest_device_error()};
+                              nsa_decode4_device_error(), selftest_device_error()};
   unsigned worst = 0;
   for (unsigned c : codes) {
     if (c == 0xffffffffu) return -1;

@@ -158,6 +158,61 @@ int launch_nsa_decode(const void* q, const void* k_cache, const void* v_cache, c
                       void* out, float* lse, int B, int Hq, int Hkv, int D, int page, int max_pages, int num_pages,
                       int S, void* workspace, cudaStream_t stream);
 
+// RMS norm of query and key heads and their rotation (qk_rope.cu): x from q
+// and k, results to q_out and k_out; backward: gradients dq_out, dk_out of the
+// results, gradients of x to q_out and k_out and of the weights to dq_weight,
+// dk_weight (fp32, where there are weights).  Strides in elements: batch, head,
+// token.  Weights null: no norm.  inv_freq holds rotary / 2 floats, 16-byte
+// aligned; positions null: 0 .. T - 1.
+struct RopeCall {
+  const void *q, *k, *dq_out, *dk_out;
+  void *q_out, *k_out;
+  const void *q_weight, *k_weight;
+  float *dq_weight, *dk_weight;
+  const int32_t* positions;
+  const float* inv_freq;
+  int64_t x_stride[2][3], dy_stride[2][3], out_stride[2][3];
+  int B, Hq, Hkv, T, D, rotary;
+  bool interleaved, weight_f32, f32;
+  float factor, eps;
+};
+int launch_qk_rope_forward(const RopeCall& r, cudaStream_t stream);
+// `workspace` holds qk_rope_backward_workspace_bytes(...) bytes, 256-byte
+// aligned: a row of weight gradients for each block of the first launch.
+size_t qk_rope_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int D);
+int launch_qk_rope_backward(const RopeCall& r, void* workspace, cudaStream_t stream);
+
+// The paged cache of e2m1 codes, two to a byte, with an e4m3 scale for every
+// 16 elements (nsa_cache4.cu, nsa_decode4.cu).
+struct Cache4 {
+  uint8_t *k, *v, *k_scale, *v_scale;
+  const float *k_factor, *v_factor;  // per kv head, or null
+  const int32_t* table;
+  int B, Hkv, D, page, max_pages, num_pages;
+};
+// New tokens into it, keys normalised and rotated (and q into q_out, both
+// nullable).  Strides in elements (batch, head, token) of k, v and q.
+struct Append4Call {
+  Cache4 cache;
+  const void *k, *v, *q;
+  void* q_out;
+  const void *q_weight, *k_weight;
+  const int32_t *lens, *new_lens;
+  const float* inv_freq;
+  int64_t stride[3][3];
+  int Hq, n, rotary;
+  bool interleaved, weight_f32, f32;
+  float factor, eps;
+};
+int launch_nsa_cache4_append(const Append4Call& r, cudaStream_t stream);
+// The values of tokens starts[b] .. starts[b] + n - 1 (starts null: from 0), as far as lens[b].
+int launch_nsa_cache4_read(const Cache4& c, const int32_t* starts, const int32_t* lens, void* k_out, void* v_out,
+                           int n, bool f32, cudaStream_t stream);
+// Attention of one query token per sequence over it (nsa_decode4.cu), in
+// nsa_decode_workspace_bytes(D, S) bytes of workspace.
+int launch_nsa_decode4(const Cache4& c, const void* q, const int32_t* lens, const int32_t* block_idx, void* out,
+                       float* lse, int Hq, int S, void* workspace, cudaStream_t stream);
+
 // Self tests (selftest.cu): the bounded wait's expiry branch (result = 0 when
 // the wait gave up, 1 if it unexpectedly completed) and the FMA-pipe log2
 // beside CUDA's log2f.
@@ -178,6 +233,7 @@ unsigned int nsa_fsa_device_error();
 unsigned int nsa_bwd_device_error();
 unsigned int nsa_bwd_tc_device_error();
 unsigned int nsa_decode_device_error();
+unsigned int nsa_decode4_device_error();
 unsigned int selftest_device_error();
 
 // Power class of the TRA epilogue: p == 1, p == 2, or the general exp2/log2

@@ -35,12 +35,12 @@
 
 #include "kernels.h"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 namespace bsa {
 namespace {
 
 constexpr int E_MIN = -96;        // exponent of the least page scale
-constexpr int UNIT = 16;          // elements a thread handles of one row
 constexpr int KV_UNITS = 2;       // units of a page per thread
 constexpr int Q_HEADS = 8;        // query heads per block
 constexpr int MAX_THREADS = 512;  // a page of 128 tokens of 128
@@ -57,89 +57,6 @@ struct AppendArgs {
   long long kv_blocks;     // blocks of the cache part; the rest rotate queries
   int q_rows, q_chunks, q_groups;  // rows per query block, blocks over a sequence's rows, blocks over its heads
 };
-
-// f / 2 pi as a fraction of a turn in 2^-64 units, modulo one turn, of a
-// finite f >= 0: 24-bit mantissa times 2^64 / 2 pi in 128 bits.
-__device__ uint64_t turns_of(float f) {
-  const uint32_t bits = __float_as_uint(fabsf(f));
-  const int ex = static_cast<int>(bits >> 23);
-  if (ex == 255 || bits == 0u) return 0ull;
-  const uint64_t m = ex == 0 ? (bits & 0x7fffffu) : ((bits & 0x7fffffu) | 0x800000u);
-  const int sh = (ex == 0 ? 1 : ex) - 150;  // f = m * 2^sh
-  constexpr uint64_t C = 2935890503282001226ull;  // 2^64 / 2 pi to the nearest integer
-  const uint64_t lo = m * C, hi = __umul64hi(m, C);
-  uint64_t u;
-  if (sh >= 0) u = sh < 64 ? lo << sh : 0ull;
-  else if (sh > -64) u = (lo >> -sh) | (hi << (64 + sh));
-  else u = sh > -128 ? hi >> (-sh - 64) : 0ull;
-  return f < 0.0f ? 0ull - u : u;
-}
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float* x) {
-  if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-  } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
-}
-
-// The 16 elements of unit u of a row: two runs of eight, starting at lo and
-// hi, and the first of their eight frequencies (-1: not rotated).  In halves,
-// the runs are the two partners of eight pairs; interleaved, and past the
-// rotated part, they follow each other.
-struct UnitMap {
-  int lo, hi, freq;
-};
-__device__ __forceinline__ UnitMap unit_map(int u, int rotary, bool interleaved) {
-  const bool rot = u * UNIT < rotary;
-  if (rot && !interleaved) return {8 * u, rotary / 2 + 8 * u, 8 * u};
-  return {UNIT * u, UNIT * u + 8, rot ? 8 * u : -1};
-}
-
-__device__ __forceinline__ void sincos8(const uint64_t* turns, int freq, int pos, float (&c)[8], float (&w)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint64_t t = turns[freq + j] * static_cast<uint64_t>(static_cast<int64_t>(pos));
-    // the signed top 32 bits: half-turns in [-1, 1)
-    sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f, &w[j], &c[j]);
-  }
-}
-__device__ __forceinline__ void rotate16(float (&x)[UNIT], const float (&c)[8], const float (&w)[8], bool interleaved) {
-  if (interleaved) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = x[2 * j], b = x[2 * j + 1];
-      x[2 * j] = a * c[j] - b * w[j];
-      x[2 * j + 1] = a * w[j] + b * c[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = x[j], b = x[8 + j];
-      x[j] = a * c[j] - b * w[j];
-      x[8 + j] = a * w[j] + b * c[j];
-    }
-  }
-}
 
 __device__ __forceinline__ uint32_t codes4(const float* x, float inv) {
   const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);

@@ -1,0 +1,634 @@
+// nsa_decode4.cu -- selection attention of one query token per sequence over a
+// paged cache of e2m1 codes with an e4m3 scale for every 16 elements.
+//
+// The formulas are nsa_decode.cu's; a key or value element is scale * code
+// (times a factor of the kv head, which goes into the scores and the result).
+// A code has two significant bits and a scale four, so their product is exact
+// in f16, and no key or value is rounded on the way: a lane turns pairs of
+// codes into f16x2 by one conversion and multiplies them by their scales
+// before the products, mma.sync.m16n8k16 over 16 query rows as there.
+//  - scores: D is summed over, so its order is free: lane (g, t) takes the D/4
+//    dims of its own quarter of a token's row.
+//  - output: lane (g, t) takes, of four tokens, the D/8 dims that are its
+//    column g of the D/8 column tiles; the nibbles of two tokens are laid side
+//    by side (a shift and a select for four pairs), and a pair's scales are
+//    one f16x2.  The tokens of a slice of 16 are numbered so that the four
+//    that a lane has probabilities of follow each other.
+// Query rows, probabilities (f16 over 2^-11 to 2^-15 of the largest so far),
+// sums and joins are those of nsa_decode.cu.
+//
+// A warp works for itself: chunks of 32 tokens (16 where pages hold 16) of its
+// pages come by four bulk copies each (codes and scales of keys and values)
+// into a ring of its own in shared memory, whose places it alone fills and
+// empties, so that warps wait for nothing but their copies.
+//
+// Selected pages: a block of four warps a (sequence, kv head), or with few of
+// them a cluster that shares out the slots.  Every page: the list of
+// (sequence, kv head, 128 tokens) is cut into equal contiguous ranges, one a
+// block; pairs that several ranges cover are joined by a second launch.
+#include <cooperative_groups.h>
+
+#include "kernels.h"
+#include "nsa_decode.cuh"
+#include "nsa_slots.cuh"
+#include "ptx.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int WARPS = 4;
+constexpr int THREADS = WARPS * 32;
+
+struct Decode4Args {
+  const __nv_bfloat16* q;
+  const uint8_t *k, *v, *k_scale, *v_scale;
+  const float *k_factor, *v_factor;         // per kv head, or null
+  const int32_t *table, *lens, *block_idx;  // block_idx null: every page
+  __nv_bfloat16* out;
+  float* lse;
+  float* ws;
+  int B, Hq, Hkv, G, page, max_pages, num_pages, S;
+  int ranges;  // blocks of the first kernel over every page
+  float scale_log2;
+};
+
+template <int D, int C>
+struct Dec4 {
+  static constexpr int CTAS = D == 128 ? 3 : 4;  // blocks of a SM
+  static constexpr int RING = 128 / C;           // chunks of a warp in flight or in use
+  static constexpr int RB = D / 2, SB = D / 16;  // bytes of a token's codes, of its scales
+  static constexpr int V_OFF = C * RB, KS_OFF = 2 * C * RB, VS_OFF = KS_OFF + C * SB;
+  static constexpr int SLOT = VS_OFF + C * SB;  // a chunk of a warp
+  static constexpr int CST = D + 8;             // row stride of the merge area
+  // the ring, and over it (a range's chunks are done with then) the merge area
+  static constexpr int MERGE = WARPS * ROWS * CST * 4;
+  static constexpr int BYTES = WARPS * RING * SLOT > MERGE ? WARPS * RING * SLOT : MERGE;
+  static_assert(SLOT % 16 == 0 && (C * SB) % 16 == 0, "bulk copies");
+};
+
+// The eight codes of a word as four f16x2, two neighbours each.
+__device__ __forceinline__ void f16_of_codes(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+// Two e4m3 scales (the low 16 bits) as f16x2.
+__device__ __forceinline__ uint32_t f16_of_scales(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t load_u8(uint32_t p) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(p) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t load_u16(uint32_t p) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(p) : "memory");
+  return r;
+}
+// N bytes in 32-bit words (fewer than four: the low ones of one).
+template <int N>
+__device__ __forceinline__ void load_bytes(uint32_t p, uint32_t (&w)[(N + 3) / 4]) {
+  if constexpr (N >= 4) {
+    const Words<N> x = load_shared<N>(p);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = x.w[i];
+  } else {
+    w[0] = N == 2 ? load_u16(p) : load_u8(p);
+  }
+}
+
+// The chunks of one warp: its share of a range, page by page, and their way into its ring.
+template <int D, int C, bool SELECT>
+struct Feed {
+  using L = Dec4<D, C>;
+  const Decode4Args& a;
+  int h, len, page_log, x, end;  // next chunk, chunks of the range
+  int first;                     // SELECT: first slot; else first token
+  int my_tok, my_id;             // SELECT: the slots' first tokens (-1: none) and pool pages, one a lane
+  int w0, id, id_next;           // else: pool pages w0 + lane and the 32 behind them
+  uint8_t* ring;
+  uint64_t* full;
+  const int32_t* row;
+  int n_pages;
+
+  __device__ __forceinline__ int page_id(int p) const {
+    if (p >= n_pages) return -1;
+    const int i = row[p];
+    return i < a.num_pages ? i : -1;
+  }
+  // Next chunk into place `place`: its first token, or -1.
+  __device__ __forceinline__ int put(int place) {
+    const int lane = threadIdx.x & 31;
+    while (x < end) {
+      int tok0, page;
+      if constexpr (SELECT) {
+        const int cpp_log = page_log - (C == 32 ? 5 : 4), u = first + (x >> cpp_log);
+        const int sub = x & ((1 << cpp_log) - 1);
+        tok0 = __shfl_sync(0xffffffffu, my_tok, u);
+        page = __shfl_sync(0xffffffffu, my_id, u);
+        x += WARPS;
+        if (tok0 < 0) continue;
+        tok0 += sub * C;
+        if (tok0 >= len) continue;
+      } else {
+        tok0 = first + x * C;
+        x += WARPS;
+        const int p = tok0 >> page_log;
+        while (p >= w0 + 32) {
+          w0 += 32;
+          id = id_next;
+          id_next = page_id(w0 + 32 + lane);
+        }
+        page = __shfl_sync(0xffffffffu, id, p - w0);
+        if (page < 0) continue;
+      }
+      debug_check(page >= 0 && page < a.num_pages && tok0 + C <= n_pages << page_log);
+      if (lane == 0) {
+        const size_t at = ((static_cast<size_t>(page) * a.Hkv + h) << page_log) + (tok0 & ((1 << page_log) - 1));
+        uint8_t* dst = ring + place * L::SLOT;
+        uint64_t* bar = full + place;
+        mbar_arrive_expect_tx(bar, L::SLOT);
+        bulk_load(dst, a.k + at * L::RB, C * L::RB, bar);
+        bulk_load(dst + L::KS_OFF, a.k_scale + at * L::SB, C * L::SB, bar);
+        bulk_load(dst + L::V_OFF, a.v + at * L::RB, C * L::RB, bar);
+        bulk_load(dst + L::VS_OFF, a.v_scale + at * L::SB, C * L::SB, bar);
+      }
+      return tok0;
+    }
+    return -1;
+  }
+};
+
+// The places of a warp's ring in order, over all the ranges that it works on.
+struct RingAt {
+  int put, use;  // chunks put and used so far
+};
+
+// Slots [p0, p1) of (b, h)'s selection, or tokens [p0, p1) of the sequence: the block's 128 threads leave the range's
+// unnormalised accumulator, weighted into one, in y (row threadIdx.x / 8, dims (threadIdx.x % 8) D/8 ..), its maximum
+// (log2 domain) in M and its sum of exponentials in sum.
+template <int D, int C, bool SELECT>
+__device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h, int p0, int p1, uint8_t* smem,
+                                             uint64_t (*bars)[128 / C], float (*ml)[ROWS][2], RingAt& at,
+                                             float (&y)[D / 8], float& M, float& sum) {
+  using L = Dec4<D, C>;
+  constexpr int NT = D / 8, KS = D / 16, RING = L::RING;
+  float(*merge)[ROWS][L::CST] = reinterpret_cast<float(*)[ROWS][L::CST]>(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int len = tokens_of(a, b);
+  const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
+
+  Feed<D, C, SELECT> feed{a};
+  feed.h = h;
+  feed.len = len;
+  feed.page_log = 31 - __clz(a.page);
+  feed.x = warp;
+  feed.first = p0;
+  feed.ring = smem + warp * RING * L::SLOT;
+  feed.full = bars[warp];
+  feed.row = a.table + static_cast<size_t>(b) * a.max_pages;
+  feed.n_pages = pieces_of(len, feed.page_log);
+  if constexpr (SELECT) {
+    const SlotRow sel = nsa_live_slots(a.block_idx + (static_cast<size_t>(b) * a.Hkv + h) * a.S, a.S, len - 1,
+                                       feed.n_pages, a.page);
+    feed.my_tok = -1;
+    feed.my_id = 0;
+    if (lane >= p0 && lane < p1 && ((sel.live >> lane) & 1u)) {
+      const int id = feed.row[sel.blk_lane];
+      if (id >= 0 && id < a.num_pages) {
+        feed.my_id = id;
+        feed.my_tok = sel.blk_lane * a.page;
+      }
+    }
+    feed.end = (p1 - p0) << (feed.page_log - (C == 32 ? 5 : 4));
+  } else {
+    feed.w0 = p0 >> feed.page_log;
+    feed.id = feed.page_id(feed.w0 + lane);
+    feed.id_next = feed.page_id(feed.w0 + 32 + lane);
+    feed.end = (p1 - p0 + C - 1) / C;
+  }
+  int ahead[RING - 1];  // first tokens of those on their way, the next first
+#pragma unroll
+  for (int i = 0; i < RING - 1; ++i) {
+    ahead[i] = feed.put(at.put % RING);
+    at.put += ahead[i] >= 0;
+  }
+
+  // query fragments, in the order of the keys' codes; each row under its own power of two
+  uint32_t qa[KS][4];
+  float f0, f1;  // score factors of rows g and g + 8
+  {
+    uint2 w[2][KS];
+    float m[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = g + 8 * r;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        w[r][ks] = make_uint2(0u, 0u);
+        if (row < a.G) w[r][ks] = *reinterpret_cast<const uint2*>(a.q + (qrow + row) * D + t * (D / 4) + 4 * ks);
+        m[r] = fmaxf(m[r], fmaxf(fmaxf(fabsf(__uint_as_float(w[r][ks].x << 16)),
+                                       fabsf(__uint_as_float(w[r][ks].x & 0xffff0000u))),
+                                 fmaxf(fabsf(__uint_as_float(w[r][ks].y << 16)),
+                                       fabsf(__uint_as_float(w[r][ks].y & 0xffff0000u)))));
+      }
+      m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 1));
+      m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 2));
+    }
+    const float factor = a.scale_log2 * (a.k_factor != nullptr ? a.k_factor[h] : 1.0f);
+    float up[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      // 2^e with the row's maximum in [2^14, 2^15) (1 for zero rows and infinities)
+      const int ex = static_cast<int>(__float_as_uint(m[r]) >> 23) - 127;
+      const int e = ex >= -100 && ex < 128 ? 14 - ex : 0;
+      up[r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      (r ? f1 : f0) = factor * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        qa[ks][r] = pack_f16x2(__uint_as_float(w[r][ks].x << 16) * up[r],
+                               __uint_as_float(w[r][ks].x & 0xffff0000u) * up[r]);
+        qa[ks][2 + r] = pack_f16x2(__uint_as_float(w[r][ks].y << 16) * up[r],
+                                   __uint_as_float(w[r][ks].y & 0xffff0000u) * up[r]);
+      }
+  }
+
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+  float acc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+
+  while (ahead[0] >= 0) {
+    const int tok0 = ahead[0];
+#pragma unroll
+    for (int i = 0; i < RING - 2; ++i) ahead[i] = ahead[i + 1];
+    __syncwarp();  // every lane is done with the chunk used last, whose place is filled now
+    ahead[RING - 2] = feed.put(at.put % RING);
+    at.put += ahead[RING - 2] >= 0;
+    const int place = at.use % RING;
+    if (!mbar_wait(feed.full + place, (at.use / RING) & 1)) break;
+    ++at.use;
+    const uint32_t src = smem_u32(feed.ring) + place * L::SLOT;
+    // ---- scores: slices of 16 tokens, two tiles of 8 each; tile j's column n is token 4 (n / 2) + 2 j + n % 2
+    float sc[C / 8][4];
+#pragma unroll
+    for (int jj = 0; jj < C / 8; jj += 2) {
+      uint32_t kw[2][(D / 8 + 3) / 4], ks2[2][D == 128 ? 2 : 1];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tk = 8 * jj + 4 * (g >> 1) + 2 * j + (g & 1);
+        load_bytes<D / 8>(src + tk * L::RB + t * (D / 8), kw[j]);
+        const uint32_t sp = src + L::KS_OFF + tk * L::SB + t * (D / 4) / 16;
+        if constexpr (D == 128) {
+          const uint32_t s = load_u16(sp);
+          ks2[j][0] = f16_of_scales(__byte_perm(s, 0u, 0x4400));
+          ks2[j][1] = f16_of_scales(__byte_perm(s, 0u, 0x4411));
+        } else {
+          ks2[j][0] = f16_of_scales(load_u8(sp) * 0x101u);
+        }
+        sc[jj + j][0] = sc[jj + j][1] = sc[jj + j][2] = sc[jj + j][3] = 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < (KS + 1) / 2; ++k) {  // a word of the row: two k-steps (D = 16: half a word, one)
+        uint32_t x[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          f16_of_codes(kw[j][k], x[j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[j][i] = mul_f16x2(x[j][i], ks2[j][D == 128 ? k / 2 : 0]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 && 2 * k + i < KS; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) mma_f16(sc[jj + j], qa[2 * k + i], x[j][2 * i], x[j][2 * i + 1]);
+      }
+    }
+    const bool tail = tok0 + C > len;
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < C / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool in = !tail || tok0 + 16 * (j >> 1) + 4 * t + 2 * (j & 1) + e < len;
+        sc[j][e] = in ? sc[j][e] * f0 : -INFINITY;
+        sc[j][2 + e] = in ? sc[j][2 + e] * f1 : -INFINITY;
+        mx0 = fmaxf(mx0, sc[j][e]);
+        mx1 = fmaxf(mx1, sc[j][2 + e]);
+      }
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+    // lazy rescale: the reference moves only when a probability would exceed 2^15
+    if (__any_sync(0xffffffffu, mx0 - m0 > P_MAX || mx1 - m1 > P_MAX)) {
+      const float n0 = fmaxf(m0, reference_of(mx0)), n1 = fmaxf(m1, reference_of(mx1));
+      // (a row of -inf scores so far keeps zero sums: exp2(-inf - -inf) is not taken)
+      const float s0 = n0 == -INFINITY ? 1.0f : ex2f(m0 - n0), s1 = n1 == -INFINITY ? 1.0f : ex2f(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= s0;
+      l1 *= s1;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        acc[j][0] *= s0;
+        acc[j][1] *= s0;
+        acc[j][2] *= s1;
+        acc[j][3] *= s1;
+      }
+    }
+    const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+    for (int s = 0; s < C / 16; ++s) {
+      uint32_t pa[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float y0 = ex2f(sc[2 * s + j][0] - b0), y1 = ex2f(sc[2 * s + j][1] - b0);
+        const float y2 = ex2f(sc[2 * s + j][2] - b1), y3 = ex2f(sc[2 * s + j][3] - b1);
+        l0 += y0 + y1;
+        l1 += y2 + y3;
+        pa[2 * j] = pack_f16x2(y0, y1);
+        pa[2 * j + 1] = pack_f16x2(y2, y3);
+      }
+      // ---- acc += P V of tokens 4t .. 4t + 3 of the slice
+      uint32_t vw[4][(D / 16 + 3) / 4], vs[4];
+      const int tk = 16 * s + 4 * t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        load_bytes<D / 16>(src + L::V_OFF + (tk + i) * L::RB + g * (D / 16), vw[i]);
+        vs[i] = load_u8(src + L::VS_OFF + (tk + i) * L::SB + g * (D / 8) / 16);
+        if (tail && tok0 + tk + i >= len) vs[i] = 0u;  // scales behind the last token may be anything
+      }
+      const uint32_t s01 = f16_of_scales(vs[0] | vs[1] << 8), s23 = f16_of_scales(vs[2] | vs[3] << 8);
+#pragma unroll
+      for (int w = 0; w < (D / 16 + 3) / 4; ++w) {
+        // even and odd nibbles of tokens 0 and 1, 2 and 3 side by side
+        constexpr uint32_t LOW = 0x0f0f0f0fu;
+        uint32_t x01[2][4], x23[2][4];
+        f16_of_codes((vw[0][w] & LOW) | (vw[1][w] << 4 & ~LOW), x01[0]);
+        f16_of_codes((vw[0][w] >> 4 & LOW) | (vw[1][w] & ~LOW), x01[1]);
+        f16_of_codes((vw[2][w] & LOW) | (vw[3][w] << 4 & ~LOW), x23[0]);
+        f16_of_codes((vw[2][w] >> 4 & LOW) | (vw[3][w] & ~LOW), x23[1]);
+#pragma unroll
+        for (int i = 0; i < 8 && i < NT; ++i)
+          mma_f16(acc[8 * w + i], pa, mul_f16x2(x01[i & 1][i >> 1], s01), mul_f16x2(x23[i & 1][i >> 1], s23));
+      }
+    }
+  }
+  // (never leave a copy landing behind a wait that gave up)
+  for (; at.use < at.put; ++at.use) mbar_wait(feed.full + at.use % RING, (at.use / RING) & 1);
+
+  // ---- the warps' states into one (over the ring: every warp is done with its chunks)
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  __syncthreads();
+  // column n = 2t, 2t + 1 of tile j, which is dim n D/8 + j, at place 8 j + n: no bank conflicts here or below
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    *reinterpret_cast<float2*>(&merge[warp][g][8 * j + 2 * t]) = make_float2(acc[j][0], acc[j][1]);
+    *reinterpret_cast<float2*>(&merge[warp][g + 8][8 * j + 2 * t]) = make_float2(acc[j][2], acc[j][3]);
+  }
+  if (t == 0) {
+    ml[warp][g][0] = m0;
+    ml[warp][g][1] = l0 * P_UNIT;
+    ml[warp][g + 8][0] = m1;
+    ml[warp][g + 8][1] = l1 * P_UNIT;
+  }
+  __syncthreads();
+  const int row = threadIdx.x >> 3;
+  const float unit = P_UNIT * (a.v_factor != nullptr ? a.v_factor[h] : 1.0f);
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, ml[w][row][0]);
+  const float mb = M == -INFINITY ? 0.0f : M;
+  sum = 0.0f;
+  float wt[WARPS];
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    wt[w] = ex2f(ml[w][row][0] - mb);
+    sum += wt[w] * ml[w][row][1];
+  }
+#pragma unroll
+  for (int e = 0; e < NT; ++e) {
+    y[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) y[e] += wt[w] * merge[w][row][8 * e + (threadIdx.x & 7)];
+    y[e] *= unit;
+  }
+}
+
+template <int RING>
+__device__ __forceinline__ void init_bars(uint64_t (*bars)[RING]) {
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < WARPS; ++w)
+      for (int i = 0; i < RING; ++i) mbar_init(&bars[w][i], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+}
+
+// A row's result, from y of its eight threads.
+template <int D>
+__device__ __forceinline__ void store_result(const Decode4Args& a, size_t row, int d0, const float (&y)[D / 8], float M,
+                                             float sum) {
+  const float inv = inverse_sum(sum);
+#pragma unroll
+  for (int e = 0; e < D / 8; e += 2)
+    *reinterpret_cast<uint32_t*>(a.out + row * D + d0 + e) = pack_bf16x2(y[e] * inv, y[e + 1] * inv);
+  if (a.lse != nullptr && d0 == 0) a.lse[row] = lse_of(M, sum);
+}
+
+// Selected pages: a cluster for each (sequence, kv head), its slots shared out over the cluster's blocks.
+template <int D, int C>
+__global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_select_kernel(const Decode4Args a) {
+  using L = Dec4<D, C>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[WARPS][L::RING];
+  __shared__ float ml[WARPS][ROWS][2];
+  __shared__ float part_ml[ROWS][2];
+  const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  const int cs = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int item = blockIdx.x / cs, b = item / a.Hkv, h = item % a.Hkv;
+  const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
+  const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
+  init_bars(bars);
+  float y[D / 8], M, sum;
+  RingAt at{0, 0};
+  decode_range<D, C, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, bars, ml, at, y, M, sum);
+  if (cs == 1) {
+    if (row < a.G) store_result<D>(a, qrow + row, d0, y, M, sum);
+    return;
+  }
+  // this block's rows, over the merge area of its warps
+  float(*part)[L::CST] = reinterpret_cast<float(*)[L::CST]>(smem);
+  __syncthreads();
+  if ((threadIdx.x & 7) == 0) {
+    part_ml[row][0] = M;
+    part_ml[row][1] = sum;
+  }
+#pragma unroll
+  for (int e = 0; e < D / 8; e += 2) *reinterpret_cast<float2*>(&part[row][d0 + e]) = make_float2(y[e], y[e + 1]);
+  cluster.sync();
+  // rank r joins rows r, r + cs, ...
+  for (int e = threadIdx.x; e < ROWS / cs * (D / 2); e += THREADS) {
+    const int r = e / (D / 2) * cs + rank, d = e % (D / 2) * 2;
+    if (r >= a.G) break;
+    float top = -INFINITY, total = 0.0f, x0 = 0.0f, x1 = 0.0f;
+    for (int k = 0; k < cs; ++k) top = fmaxf(top, cluster.map_shared_rank(&part_ml[r][0], k)[0]);
+    const float tb = top == -INFINITY ? 0.0f : top;
+    for (int k = 0; k < cs; ++k) {
+      const float* pm = cluster.map_shared_rank(&part_ml[r][0], k);
+      const float w = ex2f(pm[0] - tb);
+      const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(&part[r][d], k));
+      total += w * pm[1];
+      x0 += w * v.x;
+      x1 += w * v.y;
+    }
+    const float inv = inverse_sum(total);
+    *reinterpret_cast<uint32_t*>(a.out + (qrow + r) * D + d) = pack_bf16x2(x0 * inv, x1 * inv);
+    if (a.lse != nullptr && d == 0) a.lse[qrow + r] = lse_of(top, total);
+  }
+  cluster.sync();  // no block leaves while another reads its rows
+}
+
+// Every page: a block on one contiguous range of the (sequence, kv head, stage) list; stage k holds tokens 128 k .. of
+// the sequence.
+template <int D, int C>
+__global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_stream_kernel(const Decode4Args a) {
+  using L = Dec4<D, C>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[WARPS][L::RING];
+  __shared__ float ml[WARPS][ROWS][2];
+  // the joining kernel's blocks may take the places that this one's leave (they wait for all of it)
+  asm volatile("griddepcontrol.launch_dependents;");
+  init_bars(bars);
+  const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
+  const long long units = units_of_warp(a);
+  const long long u0 = range_start(units, blockIdx.x, a.ranges), u1 = range_start(units, blockIdx.x + 1, a.ranges);
+  if (u0 >= u1) return;
+  long long before;
+  int b = sequence_of(a, u0, &before);
+  int n_st = stages_of(a, b);
+  int h = static_cast<int>((u0 - before) / n_st), s0 = static_cast<int>((u0 - before) % n_st);
+  RingAt at{0, 0};
+  for (long long u = u0; u < u1;) {
+    const int s1 = static_cast<int>(min(static_cast<long long>(n_st), s0 + (u1 - u)));
+    const int end = static_cast<int>(min(static_cast<uint32_t>(s1) << STAGE_LOG, static_cast<uint32_t>(tokens_of(a, b))));
+    float y[D / 8], M, sum;
+    decode_range<D, C, false>(a, b, h, s0 << STAGE_LOG, end, smem, bars, ml, at, y, M, sum);
+    if (row < a.G) {
+      if (s0 == 0 && s1 == n_st) {
+        store_result<D>(a, static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G + row, d0, y, M, sum);
+      } else {  // partial: [m, l] of every row, then the accumulator rows
+        float* part = a.ws + (2 * static_cast<size_t>(blockIdx.x) + (u != u0 ? 1 : 0)) * part_floats(D);
+        if ((threadIdx.x & 7) == 0) *reinterpret_cast<float2*>(part + 2 * row) = make_float2(M, sum);
+#pragma unroll
+        for (int e = 0; e < D / 8; e += 2)
+          *reinterpret_cast<float2*>(part + 2 * ROWS + row * D + d0 + e) = make_float2(y[e], y[e + 1]);
+      }
+    }
+    u += s1 - s0;
+    s0 = 0;
+    if (u < u1) {
+      if (++h == a.Hkv) {
+        h = 0;
+        do n_st = stages_of(a, ++b);
+        while (n_st == 0);
+      }
+      fence_proxy_async_smem();  // the merge area's reads and writes before the next copies over it
+      __syncthreads();
+    }
+  }
+}
+
+template <int D, int C>
+int launch_select(const Decode4Args& a, cudaStream_t stream) {
+  using L = Dec4<D, C>;
+  const long long items = static_cast<long long>(a.B) * a.Hkv;
+  // Blocks of a cluster: as many, of whole slots, as leave each a SM.
+  int cs = 1;
+  while (cs < 8 && 2 * cs <= a.S && 2 * items * cs <= sm_count()) cs *= 2;
+  auto kern = nsa_decode4_select_kernel<D, C>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
+    return ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items * cs));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = L::BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? OK : ERR_LAUNCH;
+}
+
+template <int D, int C>
+int launch_stream(Decode4Args a, cudaStream_t stream) {
+  using L = Dec4<D, C>;
+  const int sms = sm_count();
+  if (sms < 1) return ERR_DEVICE;
+  const long long units = static_cast<long long>(a.B) * a.Hkv *
+                          ((static_cast<long long>(a.max_pages) * a.page + STAGE_TOK - 1) / STAGE_TOK);
+  const long long places = static_cast<long long>(sms) * L::CTAS;
+  const long long most = places < DECODE_MAX_RANGES ? places : DECODE_MAX_RANGES;
+  a.ranges = static_cast<int>(units < most ? units : most);
+  auto kern = nsa_decode4_stream_kernel<D, C>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
+    return ERR_LAUNCH;
+  kern<<<static_cast<unsigned>(a.ranges), THREADS, L::BYTES, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
+  return launch_decode_join<D>(a, stream);
+}
+
+template <int D>
+int launch_decode4(const Decode4Args& a, cudaStream_t stream) {
+  // chunks of 32 tokens (half the work for masks and maxima per token) where a page holds them
+  if (a.block_idx == nullptr) return a.page >= 32 ? launch_stream<D, 32>(a, stream) : launch_stream<D, 16>(a, stream);
+  return a.page >= 32 ? launch_select<D, 32>(a, stream) : launch_select<D, 16>(a, stream);
+}
+
+}  // namespace
+
+int launch_nsa_decode4(const Cache4& c, const void* q, const int32_t* lens, const int32_t* block_idx, void* out,
+                       float* lse, int Hq, int S, void* workspace, cudaStream_t stream) {
+  Decode4Args a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = c.k; a.v = c.v; a.k_scale = c.k_scale; a.v_scale = c.v_scale;
+  a.k_factor = c.k_factor; a.v_factor = c.v_factor;
+  a.table = c.table; a.lens = lens; a.block_idx = block_idx;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.ws = static_cast<float*>(workspace);
+  a.B = c.B; a.Hq = Hq; a.Hkv = c.Hkv; a.G = Hq / c.Hkv; a.page = c.page;
+  a.max_pages = c.max_pages; a.num_pages = c.num_pages; a.S = block_idx != nullptr ? S : 0;
+  a.scale_log2 = LOG2E / sqrtf(static_cast<float>(c.D));
+  switch (c.D) {
+    case 16: return launch_decode4<16>(a, stream);
+    case 32: return launch_decode4<32>(a, stream);
+    case 64: return launch_decode4<64>(a, stream);
+    case 128: return launch_decode4<128>(a, stream);
+    default: return ERR_UNSUPPORTED;
+  }
+}
+
+unsigned int nsa_decode4_device_error() { return read_and_clear_device_error(); }
+
+}  // namespace bsa

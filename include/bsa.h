@@ -641,6 +641,168 @@ BSA_API int nsa_select_decode(const void* q, const void* k_cache,
                               void* workspace, size_t workspace_bytes,
                               cudaStream_t stream);
 
+/*
+ * qk_norm_rope_forward -- the RMS norm of every query and key head and its
+ * rotation by position, in one pass: what stands between a projection and the
+ * attention entry points (the pages take q and k as they are).  For a row x (a
+ * head of a token at position m), r = (mean x^2 + eps)^-1/2 and weights w,
+ *
+ *   y = R_m (r x w),
+ *
+ * where R_m turns the pair (x_a, x_b) of j < rotary_dim / 2 by the angle m *
+ * inv_freq[j] and multiplies it by rotary_scale (the factor that some scalings
+ * for long contexts give attention; 1 otherwise), with pairs as in
+ * nsa_cache_append, and leaves elements past rotary_dim.  Angles are reduced to
+ * one turn in 64-bit fixed point.  Arithmetic is fp32, rounded once.
+ *
+ *   q, q_out   : [B, Hq, T, D] of `dtype`.    k, k_out : [B, Hkv, T, D].
+ *   q_weight, k_weight : [D] of `weight_dtype`, or NULL: that tensor is not
+ *                normalised (each for itself).
+ *   positions  : [B, T] int32 (any value), or NULL: 0 .. T - 1.
+ *   inv_freq   : [rotary_dim / 2] fp32, finite; may be NULL if rotary_dim is 0.
+ *   strides    : host memory, in elements: batch, head and token stride of q,
+ *                k, q_out and k_out (12 numbers), or NULL: all are contiguous.
+ *                The elements of a row follow each other.  Strides are multiples
+ *                of 16 bytes and not negative (0 repeats rows of an input), so a
+ *                fused projection's output is read in place.
+ *   B, T, Hq, Hkv >= 1; B * T <= 2^31 - 1; Hq, Hkv <= 65535.
+ *   D          : a multiple of 16 from 16 to 128.
+ *   rotary_dim : a multiple of 16 from 0 to D.
+ *   eps        : > 0 and finite.    rotary_scale : finite.
+ *   q_out and k_out overlap no input and not each other.  q, k, q_out, k_out,
+ *   inv_freq and the weights start on a 16-byte boundary.  Rows with a NaN, an
+ *   infinity or elements of 2^60 and more (their squares leave fp32) have
+ *   unspecified results; other rows are not touched by them.
+ *
+ * qk_norm_rope_backward -- its gradients: with g = R_m^T dy and h = r x,
+ *
+ *   dx = r (g w - h mean(g w h)),   dw = sum over batch, heads and tokens of g h
+ *
+ * (dx = g without weights).  Results repeat bit for bit.
+ *
+ *   dq_out, dk_out : gradients of q_out and k_out, of `dtype`.
+ *   dq, dk     : gradients of q and k, of `dtype`; they overlap nothing else.
+ *   dq_weight, dk_weight : [D] fp32; not NULL where the weight is not NULL.
+ *   strides    : of q, k, dq_out, dk_out, dq and dk (18 numbers), or NULL.
+ *   workspace  : caller-owned device memory of at least
+ *                qk_norm_rope_backward_workspace_size(...) bytes, 256-byte
+ *                aligned; overwritten, in use until the work on `stream`
+ *                completes (one workspace per concurrent call).
+ *
+ * Errors: BSA_ERR_NULLPTR, BSA_ERR_SHAPE (sizes, negative strides),
+ * BSA_ERR_DTYPE, BSA_ERR_UNSUPPORTED (D, rotary_dim, eps, rotary_scale),
+ * BSA_ERR_ALIGN, BSA_ERR_SCRATCH_LIMIT, BSA_ERR_DEVICE, BSA_ERR_LAUNCH.
+ */
+BSA_API int qk_norm_rope_forward(const void* q, const void* k, void* q_out,
+                                 void* k_out, const void* q_weight,
+                                 const void* k_weight,
+                                 const int32_t* positions,
+                                 const float* inv_freq, const int64_t* strides,
+                                 int B, int Hq, int Hkv, int T, int D,
+                                 int rotary_dim, int interleaved,
+                                 float rotary_scale, float eps, int dtype,
+                                 int weight_dtype, cudaStream_t stream);
+BSA_API size_t qk_norm_rope_backward_workspace_size(int B, int Hq, int Hkv,
+                                                    int T, int D);
+BSA_API int qk_norm_rope_backward(const void* q, const void* k,
+                                  const void* dq_out, const void* dk_out,
+                                  void* dq, void* dk, float* dq_weight,
+                                  float* dk_weight, const void* q_weight,
+                                  const void* k_weight,
+                                  const int32_t* positions,
+                                  const float* inv_freq,
+                                  const int64_t* strides, int B, int Hq,
+                                  int Hkv, int T, int D, int rotary_dim,
+                                  int interleaved, float rotary_scale,
+                                  float eps, int dtype, int weight_dtype,
+                                  void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/*
+ * The paged cache of 4-bit codes of nsa_cache4_append, nsa_cache4_read and
+ * nsa_cache4_decode (no counterpart in the pages): 9/16 of the e4m3 cache's
+ * bytes.  Page table, lengths, page sizes, D, group sizes and limits are those
+ * of the e4m3 cache above; what differs:
+ *
+ *   k_cache, v_cache : [num_pages, Hkv, page_size, D / 2] bytes: e2m1 codes (0,
+ *                      0.5, 1, 1.5, 2, 3, 4, 6; the fourth bit the sign), element
+ *                      2 i of a row in the low half of byte i, 2 i + 1 in the
+ *                      high half.
+ *   k_scale, v_scale : [num_pages, Hkv, page_size, D / 16] e4m3: the scale of
+ *                      elements 16 j .. 16 j + 15.  All four start on a 16-byte
+ *                      boundary.
+ *   k_factor, v_factor : [Hkv] fp32, finite and > 0, or NULL (1): a factor of
+ *                      the kv head, the same in every call on a cache.  An
+ *                      element stands for factor * scale * code: a head whose
+ *                      magnitudes leave what e4m3 scales cover (largest elements
+ *                      of groups from 2^-9 * 6 to 448 * 6) takes one.
+ *
+ * nsa_cache4_append -- new tokens' keys and values into it, keys (and queries
+ * beside them) normalised and rotated as in qk_norm_rope_forward.  The scale of
+ * a group x is the e4m3 value nearest to max |x / factor| / 6 (ties to even, at
+ * most 448), and the codes are the ones nearest to x / factor / scale, ties to
+ * even, at most 6 (a scale of 0 has codes of 0).  A group that holds a NaN or an
+ * infinity gets a NaN for its scale, and its codes are unspecified.  Nothing is
+ * kept of the tokens held before, and no value of theirs changes; slots that get
+ * no token are left as they were.
+ *
+ *   k, v, q, q_out, page_table, cache_lens, new_lens : as for
+ *                nsa_cache_append (q and q_out may be NULL; q_out is contiguous
+ *                and overlaps no input, but may be q where q is contiguous).
+ *   q_weight, k_weight, inv_freq, rotary_dim, rotary_scale, eps : as for
+ *                qk_norm_rope_forward (values are neither normalised nor
+ *                rotated).
+ *   strides    : batch, head and token stride of k, v and q (9 numbers), as for
+ *                qk_norm_rope_forward, or NULL.
+ *   No token slot may be written twice in one call.
+ *
+ * nsa_cache4_read -- the values of tokens starts[b] + i, i < n, of each
+ * sequence, as far as i < n and starts[b] + i < cache_lens[b]:
+ *
+ *   k_out, v_out : [B, Hkv, n, D] of `dtype`; rows without a token, or whose
+ *                page is not in the pool, are zero.
+ *   starts     : [B] int32 or NULL (0); a negative one has no tokens.
+ *
+ * nsa_cache4_decode -- nsa_select_decode over it, with the same arguments, sums,
+ * roundings and workspace size rule (k_t and v_t enter the products unrounded).
+ *
+ * Errors: as for the e4m3 cache, and those of qk_norm_rope_forward.
+ */
+BSA_API int nsa_cache4_append(const void* k, const void* v, const void* q,
+                              void* q_out, void* k_cache, void* v_cache,
+                              void* k_scale, void* v_scale,
+                              const float* k_factor, const float* v_factor,
+                              const int32_t* page_table,
+                              const int32_t* cache_lens,
+                              const int32_t* new_lens, const void* q_weight,
+                              const void* k_weight, const float* inv_freq,
+                              const int64_t* strides, int B, int Hq, int Hkv,
+                              int n, int D, int page_size, int max_pages,
+                              int num_pages, int rotary_dim, int interleaved,
+                              float rotary_scale, float eps, int dtype,
+                              int weight_dtype, cudaStream_t stream);
+BSA_API int nsa_cache4_read(const void* k_cache, const void* v_cache,
+                            const void* k_scale, const void* v_scale,
+                            const float* k_factor, const float* v_factor,
+                            const int32_t* page_table, const int32_t* starts,
+                            const int32_t* cache_lens, void* k_out, void* v_out,
+                            int B, int Hkv, int n, int D, int page_size,
+                            int max_pages, int num_pages, int dtype,
+                            cudaStream_t stream);
+BSA_API size_t nsa_cache4_decode_workspace_size(int B, int Hq, int Hkv, int D,
+                                                int page_size, int max_pages,
+                                                int S);
+BSA_API int nsa_cache4_decode(const void* q, const void* k_cache,
+                              const void* v_cache, const void* k_scale,
+                              const void* v_scale, const float* k_factor,
+                              const float* v_factor, const int32_t* page_table,
+                              const int32_t* cache_lens,
+                              const int32_t* block_idx, void* out, float* lse,
+                              int B, int Hq, int Hkv, int D, int page_size,
+                              int max_pages, int num_pages, int S,
+                              void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
 /* Static, NUL-terminated description of a bsa_status value (never NULL). */
 BSA_API const char* bsa_status_string(int status);
 
