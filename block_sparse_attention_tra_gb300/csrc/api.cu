@@ -160,13 +160,19 @@ Cache4 cache4_of(const void* k, const void* v, const void* k_scale, const void* 
 
 // The kernels are built for sm_103a only; refuse other devices up front
 // instead of failing inside the launch.
+// (Asked once for each device.)
 int check_device() {
+  constexpr int MAX_DEVICES = 64;
+  static std::atomic<int> known[MAX_DEVICES];  // 0: not asked, 1: fits, 2: does not
   int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ERR_DEVICE;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return ERR_DEVICE;
+  if (dev < MAX_DEVICES && known[dev].load(std::memory_order_relaxed) != 0)
+    return known[dev].load(std::memory_order_relaxed) == 1 ? OK : ERR_DEVICE;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return ERR_DEVICE;
   if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return ERR_DEVICE;
-  if (major != 10 || minor != 3) return ERR_DEVICE;
-  return OK;
+  const bool fits = major == 10 && minor == 3;
+  if (dev < MAX_DEVICES) known[dev].store(fits ? 1 : 2, std::memory_order_relaxed);
+  return fits ? OK : ERR_DEVICE;
 }
 
 }  // namespace
@@ -646,7 +652,7 @@ int nsa_cache4_append(const void* k, const void* v, const void* q, void* q_out, 
   int st = check_dtypes(dtype, weight_dtype);
   if (st == BSA_OK) st = check_cache4(r.cache, Hq);
   if (st != BSA_OK) return st;
-  if (n < 1 || static_cast<long long>(B) * n > 0x7fffffffLL || static_cast<long long>(B) * Hq * n >= (1LL << 40) / D)
+  if (n < 1 || n > (1 << 30) || static_cast<long long>(B) * n > 0x7fffffffLL || static_cast<long long>(B) * Hq * n >= (1LL << 40) / D)
     return BSA_ERR_SHAPE;
   st = check_rows(D, rotary_dim, rotary_scale, eps);
   if (st != BSA_OK) return st;
@@ -683,14 +689,15 @@ int nsa_cache4_read(const void* k_cache, const void* v_cache, const void* k_scal
                              max_pages, num_pages);
   const int st = check_cache4(c, Hkv);
   if (st != BSA_OK) return st;
-  if (n < 1 || static_cast<long long>(B) * Hkv * n >= (1LL << 40) / D) return BSA_ERR_SHAPE;
+  if (n < 1 || n > (1 << 30) || static_cast<long long>(B) * Hkv * n >= (1LL << 40) / D) return BSA_ERR_SHAPE;
   if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(starts) || !aligned4(cache_lens)) return BSA_ERR_ALIGN;
   const int dev = check_device();
   return dev != OK ? dev : launch_nsa_cache4_read(c, starts, cache_lens, k_out, v_out, n, dtype == BSA_F32, stream);
 }
 
 size_t nsa_cache4_decode_workspace_size(int B, int Hq, int Hkv, int D, int page_size, int max_pages, int S) {
-  return nsa_select_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S);
+  if (S < 0 || S > 32 || check_cache_shape(B, Hq, Hkv, D, page_size, max_pages, 1) != BSA_OK) return 0;
+  return nsa_decode4_workspace_bytes(D, S);
 }
 
 int nsa_cache4_decode(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,

@@ -209,7 +209,9 @@ int launch_nsa_cache4_append(const Append4Call& r, cudaStream_t stream);
 int launch_nsa_cache4_read(const Cache4& c, const int32_t* starts, const int32_t* lens, void* k_out, void* v_out,
                            int n, bool f32, cudaStream_t stream);
 // Attention of one query token per sequence over it (nsa_decode4.cu), in
-// nsa_decode_workspace_bytes(D, S) bytes of workspace.
+// nsa_decode4_workspace_bytes(D, S) bytes of workspace (as for nsa_decode).
+constexpr int DECODE4_MAX_RANGES = 640;
+size_t nsa_decode4_workspace_bytes(int D, int S);
 int launch_nsa_decode4(const Cache4& c, const void* q, const int32_t* lens, const int32_t* block_idx, void* out,
                        float* lse, int Hq, int S, void* workspace, cudaStream_t stream);
 

@@ -18,9 +18,10 @@
 // sums and joins are those of nsa_decode.cu.
 //
 // A warp works for itself: chunks of 32 tokens (16 where pages hold 16) of its
-// pages come by four bulk copies each (codes and scales of keys and values)
-// into a ring of its own in shared memory, whose places it alone fills and
-// empties, so that warps wait for nothing but their copies.
+// pages come by cp.async into a ring of its own in shared memory, whose places
+// it alone fills and empties, so that warps wait for nothing but their copies.
+// (By four bulk copies a chunk, codes and scales of keys and values, four
+// sequences of up to 131072 tokens took 34 us in place of 30.)
 //
 // Selected pages: a block of four warps a (sequence, kv head), or with few of
 // them a cluster that shares out the slots.  Every page: the list of
@@ -28,6 +29,7 @@
 // block; pairs that several ranges cover are joined by a second launch.
 #include <cooperative_groups.h>
 
+#include "codes4.cuh"
 #include "kernels.h"
 #include "nsa_decode.cuh"
 #include "nsa_slots.cuh"
@@ -54,26 +56,36 @@ struct Decode4Args {
 
 template <int D, int C>
 struct Dec4 {
-  static constexpr int CTAS = D == 128 ? 3 : 4;  // blocks of a SM
-  static constexpr int RING = 128 / C;           // chunks of a warp in flight or in use
+  static constexpr int CTAS = D == 128 ? 3 : 4;           // blocks of a SM
+  static constexpr int RING = (D == 128 ? 64 : 128) / C;  // chunks of a warp in flight or in use
   static constexpr int RB = D / 2, SB = D / 16;  // bytes of a token's codes, of its scales
   static constexpr int V_OFF = C * RB, KS_OFF = 2 * C * RB, VS_OFF = KS_OFF + C * SB;
   static constexpr int SLOT = VS_OFF + C * SB;  // a chunk of a warp
   static constexpr int CST = D + 8;             // row stride of the merge area
   // the ring, and over it (a range's chunks are done with then) the merge area
   static constexpr int MERGE = WARPS * ROWS * CST * 4;
-  static constexpr int BYTES = WARPS * RING * SLOT > MERGE ? WARPS * RING * SLOT : MERGE;
-  static_assert(SLOT % 16 == 0 && (C * SB) % 16 == 0, "bulk copies");
+  static constexpr int Q_OFF = WARPS * RING * SLOT > MERGE ? WARPS * RING * SLOT : MERGE;
+  static constexpr int BYTES = Q_OFF + D / 16 * 512;  // query fragments: a uint4 a lane for each 16 dims
+  static_assert(SLOT % 16 == 0 && (C * SB) % 16 == 0 && C * SB <= 256, "16-byte copies");
 };
 
-// The eight codes of a word as four f16x2, two neighbours each.
-__device__ __forceinline__ void f16_of_codes(uint32_t w, uint32_t (&r)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w));
+// Where byte `off` of a chunk's codes lies: 16-byte pieces of a 128-byte line change places so that neither keys (whole
+// quarters of rows) nor values (runs of four rows) meet in a bank.
+template <int D>
+__device__ __forceinline__ uint32_t place_of(uint32_t off) {
+  if constexpr (D == 128) return off ^ (off >> 3 & 0x60u);
+  else if constexpr (D == 64) return off ^ (off >> 1 & 0x40u) ^ (off >> 3 & 0x20u);
+  else return off;
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Two e4m3 scales (the low 16 bits) as f16x2.
 __device__ __forceinline__ uint32_t f16_of_scales(uint32_t w) {
   uint32_t r;
@@ -116,8 +128,7 @@ struct Feed {
   int first;                     // SELECT: first slot; else first token
   int my_tok, my_id;             // SELECT: the slots' first tokens (-1: none) and pool pages, one a lane
   int w0, id, id_next;           // else: pool pages w0 + lane and the 32 behind them
-  uint8_t* ring;
-  uint64_t* full;
+  uint32_t ring;
   const int32_t* row;
   int n_pages;
 
@@ -126,8 +137,13 @@ struct Feed {
     const int i = row[p];
     return i < a.num_pages ? i : -1;
   }
-  // Next chunk into place `place`: its first token, or -1.
+  // Next chunk into place `place` (a group of copies, empty behind the last): its first token, or -1.
   __device__ __forceinline__ int put(int place) {
+    const int tok0 = next(place);
+    copy_commit();
+    return tok0;
+  }
+  __device__ __forceinline__ int next(int place) {
     const int lane = threadIdx.x & 31;
     while (x < end) {
       int tok0, page;
@@ -153,25 +169,24 @@ struct Feed {
         if (page < 0) continue;
       }
       debug_check(page >= 0 && page < a.num_pages && tok0 + C <= n_pages << page_log);
-      if (lane == 0) {
-        const size_t at = ((static_cast<size_t>(page) * a.Hkv + h) << page_log) + (tok0 & ((1 << page_log) - 1));
-        uint8_t* dst = ring + place * L::SLOT;
-        uint64_t* bar = full + place;
-        mbar_arrive_expect_tx(bar, L::SLOT);
-        bulk_load(dst, a.k + at * L::RB, C * L::RB, bar);
-        bulk_load(dst + L::KS_OFF, a.k_scale + at * L::SB, C * L::SB, bar);
-        bulk_load(dst + L::V_OFF, a.v + at * L::RB, C * L::RB, bar);
-        bulk_load(dst + L::VS_OFF, a.v_scale + at * L::SB, C * L::SB, bar);
-      }
+      const size_t at = ((static_cast<size_t>(page) * a.Hkv + h) << page_log) + (tok0 & ((1 << page_log) - 1));
+      const uint32_t dst = ring + place * L::SLOT;
+      const uint8_t *k = a.k + at * L::RB + lane * 16, *v = a.v + at * L::RB + lane * 16;
+#pragma unroll
+      for (int i = 0; i < (C * L::RB + 511) / 512; ++i)
+        if (C * L::RB >= 512 || lane * 16 < C * L::RB) {
+          const uint32_t off = place_of<D>(lane * 16 + i * 512);
+          copy16(dst + off, k + i * 512);
+          copy16(dst + L::V_OFF + off, v + i * 512);
+        }
+      // scales of keys by the first half of the warp, of values by the second
+      const uint8_t* sc = (lane < 16 ? a.k_scale : a.v_scale) + at * L::SB;
+      if ((lane & 15) * 16 < C * L::SB)
+        copy16(dst + (lane < 16 ? L::KS_OFF : L::VS_OFF) + (lane & 15) * 16, sc + (lane & 15) * 16);
       return tok0;
     }
     return -1;
   }
-};
-
-// The places of a warp's ring in order, over all the ranges that it works on.
-struct RingAt {
-  int put, use;  // chunks put and used so far
 };
 
 // Slots [p0, p1) of (b, h)'s selection, or tokens [p0, p1) of the sequence: the block's 128 threads leave the range's
@@ -179,8 +194,7 @@ struct RingAt {
 // (log2 domain) in M and its sum of exponentials in sum.
 template <int D, int C, bool SELECT>
 __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h, int p0, int p1, uint8_t* smem,
-                                             uint64_t (*bars)[128 / C], float (*ml)[ROWS][2], RingAt& at,
-                                             float (&y)[D / 8], float& M, float& sum) {
+                                             float (*ml)[ROWS][2], float (&y)[D / 8], float& M, float& sum) {
   using L = Dec4<D, C>;
   constexpr int NT = D / 8, KS = D / 16, RING = L::RING;
   float(*merge)[ROWS][L::CST] = reinterpret_cast<float(*)[ROWS][L::CST]>(smem);
@@ -195,8 +209,7 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
   feed.page_log = 31 - __clz(a.page);
   feed.x = warp;
   feed.first = p0;
-  feed.ring = smem + warp * RING * L::SLOT;
-  feed.full = bars[warp];
+  feed.ring = smem_u32(smem) + warp * RING * L::SLOT;
   feed.row = a.table + static_cast<size_t>(b) * a.max_pages;
   feed.n_pages = pieces_of(len, feed.page_log);
   if constexpr (SELECT) {
@@ -220,13 +233,11 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
   }
   int ahead[RING - 1];  // first tokens of those on their way, the next first
 #pragma unroll
-  for (int i = 0; i < RING - 1; ++i) {
-    ahead[i] = feed.put(at.put % RING);
-    at.put += ahead[i] >= 0;
-  }
+  for (int i = 0; i < RING - 1; ++i) ahead[i] = feed.put(i);
 
-  // query fragments, in the order of the keys' codes; each row under its own power of two
-  uint32_t qa[KS][4];
+  // query fragments, in the order of the keys' codes; each row under its own power of two.  The warps share them, and
+  // write a share each.
+  const uint32_t q_frag = smem_u32(smem) + L::Q_OFF + lane * 16;
   float f0, f1;  // score factors of rows g and g + 8
   {
     uint2 w[2][KS];
@@ -256,33 +267,34 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
       up[r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       (r ? f1 : f0) = factor * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
+    auto two = [](uint32_t x, float u) {
+      return pack_f16x2(__uint_as_float(x << 16) * u, __uint_as_float(x & 0xffff0000u) * u);
+    };
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        qa[ks][r] = pack_f16x2(__uint_as_float(w[r][ks].x << 16) * up[r],
-                               __uint_as_float(w[r][ks].x & 0xffff0000u) * up[r]);
-        qa[ks][2 + r] = pack_f16x2(__uint_as_float(w[r][ks].y << 16) * up[r],
-                                   __uint_as_float(w[r][ks].y & 0xffff0000u) * up[r]);
-      }
+      if (ks % WARPS == warp)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_frag + ks * 512), "r"(two(w[0][ks].x, up[0])),
+                     "r"(two(w[1][ks].x, up[1])), "r"(two(w[0][ks].y, up[0])), "r"(two(w[1][ks].y, up[1]))
+                     : "memory");
   }
+  __syncthreads();
 
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
   float acc[NT][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
 
+  int place = 0;
   while (ahead[0] >= 0) {
     const int tok0 = ahead[0];
 #pragma unroll
     for (int i = 0; i < RING - 2; ++i) ahead[i] = ahead[i + 1];
     __syncwarp();  // every lane is done with the chunk used last, whose place is filled now
-    ahead[RING - 2] = feed.put(at.put % RING);
-    at.put += ahead[RING - 2] >= 0;
-    const int place = at.use % RING;
-    if (!mbar_wait(feed.full + place, (at.use / RING) & 1)) break;
-    ++at.use;
-    const uint32_t src = smem_u32(feed.ring) + place * L::SLOT;
+    ahead[RING - 2] = feed.put(place == 0 ? RING - 1 : place - 1);
+    copy_wait<RING - 1>();
+    __syncwarp();  // and every lane's copies of this one are there
+    const uint32_t src = feed.ring + place * L::SLOT;
+    place = place == RING - 1 ? 0 : place + 1;
     // ---- scores: slices of 16 tokens, two tiles of 8 each; tile j's column n is token 4 (n / 2) + 2 j + n % 2
     float sc[C / 8][4];
 #pragma unroll
@@ -291,7 +303,7 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int tk = 8 * jj + 4 * (g >> 1) + 2 * j + (g & 1);
-        load_bytes<D / 8>(src + tk * L::RB + t * (D / 8), kw[j]);
+        load_bytes<D / 8>(src + place_of<D>(tk * L::RB + t * (D / 8)), kw[j]);
         const uint32_t sp = src + L::KS_OFF + tk * L::SB + t * (D / 4) / 16;
         if constexpr (D == 128) {
           const uint32_t s = load_u16(sp);
@@ -312,9 +324,11 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
           for (int i = 0; i < 4; ++i) x[j][i] = mul_f16x2(x[j][i], ks2[j][D == 128 ? k / 2 : 0]);
         }
 #pragma unroll
-        for (int i = 0; i < 2 && 2 * k + i < KS; ++i)
+        for (int i = 0; i < 2 && 2 * k + i < KS; ++i) {
+          const Words<16> q = load_shared<16>(q_frag + (2 * k + i) * 512);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) mma_f16(sc[jj + j], qa[2 * k + i], x[j][2 * i], x[j][2 * i + 1]);
+          for (int j = 0; j < 2; ++j) mma_f16(sc[jj + j], q.w, x[j][2 * i], x[j][2 * i + 1]);
+        }
       }
     }
     const bool tail = tok0 + C > len;
@@ -323,12 +337,21 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
     for (int j = 0; j < C / 8; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const bool in = !tail || tok0 + 16 * (j >> 1) + 4 * t + 2 * (j & 1) + e < len;
-        sc[j][e] = in ? sc[j][e] * f0 : -INFINITY;
-        sc[j][2 + e] = in ? sc[j][2 + e] * f1 : -INFINITY;
-        mx0 = fmaxf(mx0, sc[j][e]);
-        mx1 = fmaxf(mx1, sc[j][2 + e]);
+        sc[j][e] *= f0;
+        sc[j][2 + e] *= f1;
       }
+    if (tail) {
+#pragma unroll
+      for (int j = 0; j < C / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (tok0 + 16 * (j >> 1) + 4 * t + 2 * (j & 1) + e >= len) sc[j][e] = sc[j][2 + e] = -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < C / 8; ++j) {
+      mx0 = fmaxf(mx0, fmaxf(sc[j][0], sc[j][1]));
+      mx1 = fmaxf(mx1, fmaxf(sc[j][2], sc[j][3]));
+    }
     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
@@ -368,9 +391,13 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
       const int tk = 16 * s + 4 * t;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        load_bytes<D / 16>(src + L::V_OFF + (tk + i) * L::RB + g * (D / 16), vw[i]);
+        load_bytes<D / 16>(src + L::V_OFF + place_of<D>((tk + i) * L::RB + g * (D / 16)), vw[i]);
         vs[i] = load_u8(src + L::VS_OFF + (tk + i) * L::SB + g * (D / 8) / 16);
-        if (tail && tok0 + tk + i >= len) vs[i] = 0u;  // scales behind the last token may be anything
+      }
+      if (tail) {  // scales behind the last token may be anything
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tok0 + tk + i >= len) vs[i] = 0u;
       }
       const uint32_t s01 = f16_of_scales(vs[0] | vs[1] << 8), s23 = f16_of_scales(vs[2] | vs[3] << 8);
 #pragma unroll
@@ -388,8 +415,7 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
       }
     }
   }
-  // (never leave a copy landing behind a wait that gave up)
-  for (; at.use < at.put; ++at.use) mbar_wait(feed.full + at.use % RING, (at.use / RING) & 1);
+  copy_wait<0>();
 
   // ---- the warps' states into one (over the ring: every warp is done with its chunks)
   l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
@@ -432,16 +458,6 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
   }
 }
 
-template <int RING>
-__device__ __forceinline__ void init_bars(uint64_t (*bars)[RING]) {
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < WARPS; ++w)
-      for (int i = 0; i < RING; ++i) mbar_init(&bars[w][i], 1);
-    fence_barrier_init();
-  }
-  __syncthreads();
-}
-
 // A row's result, from y of its eight threads.
 template <int D>
 __device__ __forceinline__ void store_result(const Decode4Args& a, size_t row, int d0, const float (&y)[D / 8], float M,
@@ -458,7 +474,6 @@ template <int D, int C>
 __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_select_kernel(const Decode4Args a) {
   using L = Dec4<D, C>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t bars[WARPS][L::RING];
   __shared__ float ml[WARPS][ROWS][2];
   __shared__ float part_ml[ROWS][2];
   const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
@@ -466,10 +481,8 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_selec
   const int item = blockIdx.x / cs, b = item / a.Hkv, h = item % a.Hkv;
   const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
   const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
-  init_bars(bars);
   float y[D / 8], M, sum;
-  RingAt at{0, 0};
-  decode_range<D, C, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, bars, ml, at, y, M, sum);
+  decode_range<D, C, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, ml, y, M, sum);
   if (cs == 1) {
     if (row < a.G) store_result<D>(a, qrow + row, d0, y, M, sum);
     return;
@@ -512,11 +525,9 @@ template <int D, int C>
 __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_stream_kernel(const Decode4Args a) {
   using L = Dec4<D, C>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t bars[WARPS][L::RING];
   __shared__ float ml[WARPS][ROWS][2];
   // the joining kernel's blocks may take the places that this one's leave (they wait for all of it)
   asm volatile("griddepcontrol.launch_dependents;");
-  init_bars(bars);
   const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
   const long long units = units_of_warp(a);
   const long long u0 = range_start(units, blockIdx.x, a.ranges), u1 = range_start(units, blockIdx.x + 1, a.ranges);
@@ -525,12 +536,11 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_strea
   int b = sequence_of(a, u0, &before);
   int n_st = stages_of(a, b);
   int h = static_cast<int>((u0 - before) / n_st), s0 = static_cast<int>((u0 - before) % n_st);
-  RingAt at{0, 0};
   for (long long u = u0; u < u1;) {
     const int s1 = static_cast<int>(min(static_cast<long long>(n_st), s0 + (u1 - u)));
     const int end = static_cast<int>(min(static_cast<uint32_t>(s1) << STAGE_LOG, static_cast<uint32_t>(tokens_of(a, b))));
     float y[D / 8], M, sum;
-    decode_range<D, C, false>(a, b, h, s0 << STAGE_LOG, end, smem, bars, ml, at, y, M, sum);
+    decode_range<D, C, false>(a, b, h, s0 << STAGE_LOG, end, smem, ml, y, M, sum);
     if (row < a.G) {
       if (s0 == 0 && s1 == n_st) {
         store_result<D>(a, static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G + row, d0, y, M, sum);
@@ -550,8 +560,7 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_strea
         do n_st = stages_of(a, ++b);
         while (n_st == 0);
       }
-      fence_proxy_async_smem();  // the merge area's reads and writes before the next copies over it
-      __syncthreads();
+      __syncthreads();  // the merge area is read before the next copies over it
     }
   }
 }
@@ -588,7 +597,7 @@ int launch_stream(Decode4Args a, cudaStream_t stream) {
   const long long units = static_cast<long long>(a.B) * a.Hkv *
                           ((static_cast<long long>(a.max_pages) * a.page + STAGE_TOK - 1) / STAGE_TOK);
   const long long places = static_cast<long long>(sms) * L::CTAS;
-  const long long most = places < DECODE_MAX_RANGES ? places : DECODE_MAX_RANGES;
+  const long long most = places < DECODE4_MAX_RANGES ? places : DECODE4_MAX_RANGES;
   a.ranges = static_cast<int>(units < most ? units : most);
   auto kern = nsa_decode4_stream_kernel<D, C>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
@@ -606,6 +615,11 @@ int launch_decode4(const Decode4Args& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// The partials of the most ranges (the size does not depend on the device); selected pages leave none.
+size_t nsa_decode4_workspace_bytes(int D, int S) {
+  return S > 0 ? 256 : 2 * static_cast<size_t>(DECODE4_MAX_RANGES) * part_floats(D) * sizeof(float);
+}
 
 int launch_nsa_decode4(const Cache4& c, const void* q, const int32_t* lens, const int32_t* block_idx, void* out,
                        float* lse, int Hq, int S, void* workspace, cudaStream_t stream) {

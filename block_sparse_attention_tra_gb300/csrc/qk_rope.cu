@@ -35,166 +35,190 @@ struct RopeArgs {
   const int32_t* positions;
   const float* inv_freq;
   float* ws;
-  int T, D, rotary, interleaved, w_f32;
+  int T, D, rotary, w_f32;
   long long tokens;
   float factor, eps;
-  RowTile tile;
-  int q_groups, groups;  // blocks over the heads of q, of both
-  long long q_blocks, k_blocks;  // blocks in all: rows of the workspace
+  RowPlan<2> plan;
 };
 
-// What a thread holds: its token, its unit of the rows, and its first head.
-struct Place {
-  int s, group, u, slot, head;
-  long long tile, token, b;
-  int t;
-  bool live;
-};
-__device__ __forceinline__ Place place_of(const RopeArgs& a) {
-  Place p;
-  p.group = static_cast<int>(blockIdx.x % a.groups);
-  p.tile = blockIdx.x / a.groups;
-  p.s = p.group >= a.q_groups ? 1 : 0;
-  if (p.s) p.group -= a.q_groups;
-  p.u = threadIdx.x & ((1 << a.tile.lanes_log) - 1);
-  p.slot = static_cast<int>(threadIdx.x) >> a.tile.lanes_log;
-  p.token = (p.tile << a.tile.tokens_log) + (p.slot & ((1 << a.tile.tokens_log) - 1));
-  p.head = p.group * row_heads(a.tile) + (p.slot >> a.tile.tokens_log);
-  p.live = p.token < a.tokens && p.u * UNIT < a.D;
-  // (all tokens together are a 31-bit number)
-  p.b = p.live ? static_cast<uint32_t>(p.token) / static_cast<uint32_t>(a.T) : 0;
-  p.t = p.live ? static_cast<int>(static_cast<uint32_t>(p.token) % static_cast<uint32_t>(a.T)) : 0;
-  return p;
+// The first run of eight of the thread's unit in its first row.
+template <typename T>
+__device__ __forceinline__ T* first_row(T* x, const long long (&stride)[3], uint32_t b, int head, uint32_t t, int lo) {
+  return x + b * stride[0] + head * stride[1] + t * stride[2] + lo;
 }
 
-template <typename T>
+__device__ __forceinline__ int position_of(const RopeArgs& a, const RowPlace& p, uint32_t t) {
+  return a.positions != nullptr ? a.positions[p.token] : static_cast<int>(t);
+}
+
+template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(ROW_THREADS, 3) qk_rope_forward_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int AHEAD = sizeof(T) == 2 ? 2 : 1;  // rows on their way
-  const Place p = place_of(a);
-  const Side& sd = a.side[p.s];
-  const bool il = a.interleaved != 0, norm = sd.w != nullptr;
-  const int head_step = ROW_THREADS >> a.tile.lanes_log >> a.tile.tokens_log;
-  const UnitMap m = unit_map(p.u, a.rotary, il);
-  const T* src = static_cast<const T*>(sd.x) + p.b * sd.x_stride[0] + p.t * sd.x_stride[2];
-  T* dst = static_cast<T*>(sd.out) + p.b * sd.out_stride[0] + p.t * sd.out_stride[2];
-  RawUnit<T> raw[AHEAD];
-  auto fetch = [&](int r0) {
+  using Ring = RowRing<T, 1>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint64_t turns[64];
+  const Ring ring(smem);
+  const RowPlace p = place_of(a.plan, a.tokens, {a.side[0].H, a.side[1].H}, a.D);
+  const Side& sd = a.side[p.side];
+  const bool norm = sd.w != nullptr;
+  const UnitMap m = unit_map(p.unit, a.rotary, INTERLEAVED);
+  const int apart = m.hi - m.lo;
+  const uint32_t b = p.token / static_cast<uint32_t>(a.T), t = p.token % static_cast<uint32_t>(a.T);
+  const T* src = first_row(static_cast<const T*>(sd.x), sd.x_stride, b, p.head, t, m.lo);
+  T* dst = first_row(static_cast<T*>(sd.out), sd.out_stride, b, p.head, t, m.lo);
+  const long long src_step = p.head_step * sd.x_stride[1], dst_step = p.head_step * sd.out_stride[1];
+  auto ask = [&](int r0) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int h = p.head + (r0 + i) * head_step;
-      if (p.live && r0 + i < a.tile.rows && h < sd.H) raw[i].load(src + h * sd.x_stride[1], m);
-      else raw[i].clear();
+    for (int i = 0; i < Ring::BATCH; ++i) {
+      if (r0 + i < p.rows) ring.ask((r0 + i) % (2 * Ring::BATCH), 0, src, apart);
+      src += src_step;
     }
+    Ring::commit();
   };
-  fetch(0);
-  float c[8], w[8], wt[UNIT];
-  const bool turn = p.live && m.freq >= 0;
-  if (turn)
-    sincos8_of(a.inv_freq + m.freq, a.positions != nullptr ? a.positions[p.token] : p.t, a.factor, c, w);
-  if (norm && p.live) load_weights(sd.w, a.w_f32 != 0, m, wt);
-  const float inv_d = 1.0f / static_cast<float>(a.D);
-  for (int r0 = 0; r0 < a.tile.rows; r0 += AHEAD) {
-    if (r0 > 0) fetch(r0);
+  ask(0);
+  ask(Ring::BATCH);
+  float c[8], w[8], g[UNIT];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      if (r0 + i >= a.tile.rows) break;
+  for (int j = 0; j < UNIT; ++j) g[j] = 1.0f;
+  const bool turn = m.freq >= 0, in_row = p.unit * UNIT < a.D;
+  if (norm && in_row) load_weights(sd.w, a.w_f32 != 0, m, g);
+  UnitMap2 map;
+  if (a.rotary > 0) block_turns(turns, a.inv_freq, a.rotary);
+  if (turn) {
+    unit_sincos(turns, m.freq, position_of(a, p, t), a.factor, c, w);
+    make_map<INTERLEAVED>(map, c, w, g);
+  } else {  // the weights alone, in the map's place
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      map.aa[j] = g[INTERLEAVED ? 2 * j : j];
+      map.bb[j] = g[INTERLEAVED ? 2 * j + 1 : 8 + j];
+      map.ab[j] = map.ba[j] = 0.0f;
+    }
+  }
+  const float inv_d = 1.0f / static_cast<float>(a.D);
+  for (int r0 = 0; r0 < p.most; r0 += Ring::BATCH) {
+    Ring::wait();
+#pragma unroll
+    for (int i = 0; i < Ring::BATCH; ++i) {
+      if (i > 0 && r0 + i >= p.most) break;
+      const bool mine = r0 + i < p.rows;
       float x[UNIT];
-      raw[i].unpack(x);
+      ring.take((r0 + i) % (2 * Ring::BATCH), 0, x);  // (anything where no row was asked for; it stays in its row)
+      float s = 1.0f;
       if (norm) {
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < UNIT; ++j) ss = fmaf(x[j], x[j], ss);
-        const float r = rsqrtf(fmaf(row_sum(ss, a.tile.lanes_log), inv_d, a.eps));
-#pragma unroll
-        for (int j = 0; j < UNIT; ++j) x[j] = x[j] * r * wt[j];
+        s = rsqrtf(fmaf(row_sum(ss, a.plan.lanes_log, in_row), inv_d, a.eps));
       }
-      const int h = p.head + (r0 + i) * head_step;
-      if (!p.live || h >= sd.H) continue;
-      if (turn) rotate16(x, c, w, il);
-      T* row = dst + h * sd.out_stride[1];
-      store8(row + m.lo, x);
-      store8(row + m.hi, x + 8);
+      if (mine) {
+        if (turn) {
+          apply_map<INTERLEAVED>(map, s, x);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[INTERLEAVED ? 2 * j : j] *= s * map.aa[j];
+            x[INTERLEAVED ? 2 * j + 1 : 8 + j] *= s * map.bb[j];
+          }
+        }
+        store8(dst, x);
+        store8(dst + apart, x + 8);
+      }
+      dst += dst_step;
     }
+    ask(r0 + 2 * Ring::BATCH);
   }
 }
 
-template <typename T>
+template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(ROW_THREADS, 2) qk_rope_backward_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int AHEAD = sizeof(T) == 2 ? 2 : 1;  // rows on their way
-  __shared__ float part[ROW_THREADS / 32][128];
+  using Ring = RowRing<T, 2>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint64_t turns[64];
   // the second launch's blocks may take the places that this one's leave (they wait for all of it)
   asm volatile("griddepcontrol.launch_dependents;");
-  const Place p = place_of(a);
-  const Side& sd = a.side[p.s];
-  const bool il = a.interleaved != 0, norm = sd.w != nullptr;
-  const int head_step = ROW_THREADS >> a.tile.lanes_log >> a.tile.tokens_log;
-  const UnitMap m = unit_map(p.u, a.rotary, il);
-  const T* src = static_cast<const T*>(sd.x) + p.b * sd.x_stride[0] + p.t * sd.x_stride[2];
-  const T* up = static_cast<const T*>(sd.dy) + p.b * sd.dy_stride[0] + p.t * sd.dy_stride[2];
-  T* dst = static_cast<T*>(sd.out) + p.b * sd.out_stride[0] + p.t * sd.out_stride[2];
-  RawUnit<T> raw_x[AHEAD], raw_g[AHEAD];
-  auto fetch = [&](int r0) {
+  const Ring ring(smem);
+  const RowPlace p = place_of(a.plan, a.tokens, {a.side[0].H, a.side[1].H}, a.D);
+  const Side& sd = a.side[p.side];
+  const bool norm = sd.w != nullptr;
+  const UnitMap m = unit_map(p.unit, a.rotary, INTERLEAVED);
+  const int apart = m.hi - m.lo;
+  const uint32_t b = p.token / static_cast<uint32_t>(a.T), t = p.token % static_cast<uint32_t>(a.T);
+  const T* src = first_row(static_cast<const T*>(sd.x), sd.x_stride, b, p.head, t, m.lo);
+  const T* up = first_row(static_cast<const T*>(sd.dy), sd.dy_stride, b, p.head, t, m.lo);
+  T* dst = first_row(static_cast<T*>(sd.out), sd.out_stride, b, p.head, t, m.lo);
+  const long long src_step = p.head_step * sd.x_stride[1], up_step = p.head_step * sd.dy_stride[1];
+  const long long dst_step = p.head_step * sd.out_stride[1];
+  auto ask = [&](int r0) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int h = p.head + (r0 + i) * head_step;
-      const bool in = p.live && r0 + i < a.tile.rows && h < sd.H;
-      if (in) raw_g[i].load(up + h * sd.dy_stride[1], m);
-      else raw_g[i].clear();
-      if (in && norm) raw_x[i].load(src + h * sd.x_stride[1], m);
-      else raw_x[i].clear();
+    for (int i = 0; i < Ring::BATCH; ++i) {
+      if (r0 + i < p.rows) {
+        ring.ask((r0 + i) % (2 * Ring::BATCH), 0, up, apart);
+        if (norm) ring.ask((r0 + i) % (2 * Ring::BATCH), 1, src, apart);
+      }
+      up += up_step;
+      src += src_step;
     }
+    Ring::commit();
   };
-  fetch(0);
+  ask(0);
+  ask(Ring::BATCH);
   float c[8], w[8], wt[UNIT], dw[UNIT];
-  const bool turn = p.live && m.freq >= 0;
+#pragma unroll
+  for (int j = 0; j < UNIT; ++j) wt[j] = dw[j] = 0.0f;
+  const bool turn = m.freq >= 0, in_row = p.unit * UNIT < a.D;
+  if (norm && in_row) load_weights(sd.w, a.w_f32 != 0, m, wt);
+  if (a.rotary > 0) block_turns(turns, a.inv_freq, a.rotary);
   if (turn) {
-    sincos8_of(a.inv_freq + m.freq, a.positions != nullptr ? a.positions[p.token] : p.t, a.factor, c, w);
+    unit_sincos(turns, m.freq, position_of(a, p, t), a.factor, c, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = -w[j];  // the transpose
   }
-#pragma unroll
-  for (int j = 0; j < UNIT; ++j) wt[j] = dw[j] = 0.0f;
-  if (norm && p.live) load_weights(sd.w, a.w_f32 != 0, m, wt);
   const float inv_d = 1.0f / static_cast<float>(a.D);
-  for (int r0 = 0; r0 < a.tile.rows; r0 += AHEAD) {
-    if (r0 > 0) fetch(r0);
+  for (int r0 = 0; r0 < p.most; r0 += Ring::BATCH) {
+    Ring::wait();
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      if (r0 + i >= a.tile.rows) break;
-      float g[UNIT];
-      raw_g[i].unpack(g);
-      if (turn) rotate16(g, c, w, il);
+    for (int i = 0; i < Ring::BATCH; ++i) {
+      if (i > 0 && r0 + i >= p.most) break;
+      const bool mine = r0 + i < p.rows;
+      float g[UNIT], x[UNIT];
+      ring.take((r0 + i) % (2 * Ring::BATCH), 0, g);  // (anything where no row was asked for; it stays in its row)
+      if (turn) rotate16(g, c, w, INTERLEAVED);
       if (norm) {
-        float x[UNIT], ss = 0.0f, dot = 0.0f;
-        raw_x[i].unpack(x);
+        ring.take((r0 + i) % (2 * Ring::BATCH), 1, x);
+        float ss = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < UNIT; ++j) ss = fmaf(x[j], x[j], ss);
-        const float r = rsqrtf(fmaf(row_sum(ss, a.tile.lanes_log), inv_d, a.eps));
+        const float rs = rsqrtf(fmaf(row_sum(ss, a.plan.lanes_log, in_row), inv_d, a.eps));
 #pragma unroll
-        for (int j = 0; j < UNIT; ++j) {
-          x[j] *= r;
-          dw[j] = fmaf(g[j], x[j], dw[j]);
+        for (int j = 0; j < UNIT; ++j) {  // r g, the weights' gradient r g x, then z = r g w
+          g[j] *= rs;
+          if (mine) dw[j] = fmaf(g[j], x[j], dw[j]);
           g[j] *= wt[j];
           dot = fmaf(g[j], x[j], dot);
         }
-        dot = row_sum(dot, a.tile.lanes_log) * inv_d;
+        const float k = row_sum(dot, a.plan.lanes_log, in_row) * inv_d * rs * rs;  // dx = z - x r^2 mean(z x)
 #pragma unroll
-        for (int j = 0; j < UNIT; ++j) g[j] = r * fmaf(-x[j], dot, g[j]);
+        for (int j = 0; j < UNIT; ++j) g[j] = fmaf(-k, x[j], g[j]);
       }
-      const int h = p.head + (r0 + i) * head_step;
-      if (!p.live || h >= sd.H) continue;
-      T* row = dst + h * sd.out_stride[1];
-      store8(row + m.lo, g);
-      store8(row + m.hi, g + 8);
+      if (mine) {
+        store8(dst, g);
+        store8(dst + apart, g + 8);
+      }
+      dst += dst_step;
     }
+    ask(r0 + 2 * Ring::BATCH);
   }
   if (!norm) return;
-  // the block's rows: lanes of a warp that hold the same unit, then the warps
+  // the block's sums: the lanes of a warp that hold the same unit, then the warps (over the ring)
+  float(*part)[128] = reinterpret_cast<float(*)[128]>(smem);
+  __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < UNIT; ++j)
-    for (int d = 16; d >= 1 << a.tile.lanes_log; d >>= 1) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], d);
-  if (lane < 1 << a.tile.lanes_log && p.u * UNIT < a.D) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+      if (d >= 1 << a.plan.lanes_log) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], d);
+  if (lane < 1 << a.plan.lanes_log && p.unit * UNIT < a.D) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       part[warp][m.lo + j] = dw[j];
@@ -206,53 +230,52 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) qk_rope_backward_kernel(const 
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < ROW_THREADS / 32; ++k) sum += part[k][j];
-    const long long row = p.s ? a.q_blocks + p.tile * (a.groups - a.q_groups) + p.group : p.tile * a.q_groups + p.group;
-    a.ws[row * a.D + j] = sum;
+    const size_t row = p.side ? static_cast<size_t>(a.plan.tiles) * a.plan.groups[0] : 0;
+    a.ws[(row + static_cast<size_t>(p.tile) * a.plan.groups[p.side] + p.group) * a.D + j] = sum;
   }
 }
 
-// Adds up the blocks' rows: one block for 16 columns of one tensor's weights.
-__global__ void __launch_bounds__(256) qk_rope_weights_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float4 part[64][4];
-  const int per = a.D / 16, s = blockIdx.x / per, col = blockIdx.x % per * 16 + (threadIdx.x & 3) * 4;
-  const int lane = threadIdx.x >> 2;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel is complete
+// Adds up the blocks' rows: one block for 16 columns of one tensor's weights, four columns a thread.
+constexpr int SUM_THREADS = 1024;
+__global__ void __launch_bounds__(SUM_THREADS) qk_rope_weights_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ float4 part[SUM_THREADS / 32][4];
+  const int per = a.D / 16, s = blockIdx.x / per, col = blockIdx.x % per * 16;
   const Side& sd = a.side[s];
   if (sd.dw == nullptr) return;
-  const long long rows = s ? a.k_blocks : a.q_blocks;
-  const float* from = a.ws + (s ? a.q_blocks : 0) * a.D + col;
+  const size_t rows = static_cast<size_t>(a.plan.tiles) * a.plan.groups[s];
+  const float* from = a.ws + (s ? static_cast<size_t>(a.plan.tiles) * a.plan.groups[0] : 0) * a.D + col +
+                      (threadIdx.x & 3) * 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel is complete
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (long long r = lane; r < rows; r += 64) {
+  for (size_t r = threadIdx.x >> 2; r < rows; r += SUM_THREADS / 4) {
     const float4 v = *reinterpret_cast<const float4*>(from + r * a.D);
     sum.x += v.x;
     sum.y += v.y;
     sum.z += v.z;
     sum.w += v.w;
   }
-  part[lane][threadIdx.x & 3] = sum;
+#pragma unroll
+  for (int d = 16; d >= 4; d >>= 1) {
+    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, d);
+    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, d);
+    sum.z += __shfl_xor_sync(0xffffffffu, sum.z, d);
+    sum.w += __shfl_xor_sync(0xffffffffu, sum.w, d);
+  }
+  if ((threadIdx.x & 31) < 4) part[threadIdx.x >> 5][threadIdx.x & 3] = sum;
   __syncthreads();
   if (threadIdx.x >= 16) return;
   float total = 0.0f;
-  for (int k = 0; k < 64; ++k) total += reinterpret_cast<const float*>(&part[k][0])[threadIdx.x];
-  static_cast<float*>(sd.dw)[blockIdx.x % per * 16 + threadIdx.x] = total;
+#pragma unroll
+  for (int k = 0; k < SUM_THREADS / 32; ++k) total += reinterpret_cast<const float*>(&part[k][0])[threadIdx.x];
+  static_cast<float*>(sd.dw)[col + threadIdx.x] = total;
 }
 
-// Rows a thread walks at most: sines, weights and the weights' gradients are paid once for them.
-constexpr int FORWARD_ROWS = 8, BACKWARD_ROWS = 8;
-
-// Fills in the blocks; false if there are too many.
-bool plan(RopeArgs& a, int B, int most) {
+// Rows a thread walks at most: sines, weights and the sums' reduction are paid once for them.
+constexpr int MOST_ROWS = 16;
+bool plan(RopeArgs& a, int B) {
   a.tokens = static_cast<long long>(B) * a.T;
-  const int Hq = a.side[0].H, Hk = a.side[1].H;
-  a.tile = row_tile(a.tokens, Hq + Hk, a.D, most);
-  const int heads = row_heads(a.tile);
-  a.q_groups = (Hq + heads - 1) / heads;
-  a.groups = a.q_groups + (Hk + heads - 1) / heads;
-  const long long tiles = (a.tokens + (1LL << a.tile.tokens_log) - 1) >> a.tile.tokens_log;
-  a.q_blocks = tiles * a.q_groups;
-  a.k_blocks = tiles * (a.groups - a.q_groups);
-  return a.q_blocks + a.k_blocks <= 0x7fffffffLL;
+  return plan_rows<2>(a.plan, a.tokens, {a.side[0].H, a.side[1].H}, a.D, MOST_ROWS);
 }
 
 RopeArgs args_of(const RopeCall& r) {
@@ -271,21 +294,36 @@ RopeArgs args_of(const RopeCall& r) {
   }
   a.positions = r.positions;
   a.inv_freq = r.inv_freq;
-  a.T = r.T; a.D = r.D; a.rotary = r.rotary; a.interleaved = r.interleaved ? 1 : 0;
+  a.T = r.T; a.D = r.D; a.rotary = r.rotary;
   a.w_f32 = r.weight_f32 ? 1 : 0;
   a.factor = r.factor; a.eps = r.eps;
   return a;
+}
+
+template <typename T>
+int launch_forward(const RopeArgs& a, bool interleaved, cudaStream_t stream) {
+  auto kern = interleaved ? qk_rope_forward_kernel<T, true> : qk_rope_forward_kernel<T, false>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowRing<T, 1>::BYTES) != cudaSuccess)
+    return ERR_LAUNCH;
+  kern<<<a.plan.tiles * a.plan.all_groups, ROW_THREADS, RowRing<T, 1>::BYTES, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
+}
+template <typename T>
+int launch_backward(const RopeArgs& a, bool interleaved, cudaStream_t stream) {
+  auto kern = interleaved ? qk_rope_backward_kernel<T, true> : qk_rope_backward_kernel<T, false>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowRing<T, 2>::BYTES) != cudaSuccess)
+    return ERR_LAUNCH;
+  kern<<<a.plan.tiles * a.plan.all_groups, ROW_THREADS, RowRing<T, 2>::BYTES, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
 }  // namespace
 
 int launch_qk_rope_forward(const RopeCall& r, cudaStream_t stream) {
   RopeArgs a = args_of(r);
-  if (!plan(a, r.B, FORWARD_ROWS)) return ERR_SHAPE;
-  const unsigned blocks = static_cast<unsigned>(a.q_blocks + a.k_blocks);
-  if (r.f32) qk_rope_forward_kernel<float><<<blocks, ROW_THREADS, 0, stream>>>(a);
-  else qk_rope_forward_kernel<__nv_bfloat16><<<blocks, ROW_THREADS, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
+  if (!plan(a, r.B)) return ERR_SHAPE;
+  return r.f32 ? launch_forward<float>(a, r.interleaved, stream)
+               : launch_forward<__nv_bfloat16>(a, r.interleaved, stream);
 }
 
 size_t qk_rope_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int D) {
@@ -293,22 +331,20 @@ size_t qk_rope_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int D) {
   a.side[0].H = Hq;
   a.side[1].H = Hkv;
   a.T = T; a.D = D;
-  if (!plan(a, B, BACKWARD_ROWS)) return 0;
-  return (static_cast<size_t>(a.q_blocks + a.k_blocks) * D * sizeof(float) + 255) / 256 * 256;
+  if (!plan(a, B)) return 0;
+  return (static_cast<size_t>(a.plan.tiles) * a.plan.all_groups * D * sizeof(float) + 255) / 256 * 256;
 }
 
 int launch_qk_rope_backward(const RopeCall& r, void* workspace, cudaStream_t stream) {
   RopeArgs a = args_of(r);
   a.ws = static_cast<float*>(workspace);
-  if (!plan(a, r.B, BACKWARD_ROWS)) return ERR_SHAPE;
-  const unsigned blocks = static_cast<unsigned>(a.q_blocks + a.k_blocks);
-  if (r.f32) qk_rope_backward_kernel<float><<<blocks, ROW_THREADS, 0, stream>>>(a);
-  else qk_rope_backward_kernel<__nv_bfloat16><<<blocks, ROW_THREADS, 0, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
-  if (r.q_weight == nullptr && r.k_weight == nullptr) return OK;
+  if (!plan(a, r.B)) return ERR_SHAPE;
+  const int st = r.f32 ? launch_backward<float>(a, r.interleaved, stream)
+                       : launch_backward<__nv_bfloat16>(a, r.interleaved, stream);
+  if (st != OK || (r.q_weight == nullptr && r.k_weight == nullptr)) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (a.D / 16)));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(SUM_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -94,83 +94,190 @@ __device__ __forceinline__ void rotate16(float (&x)[UNIT], const float (&c)[8], 
   }
 }
 
-// The same from the pairs' frequencies themselves, times a factor.
-__device__ __forceinline__ void sincos8_of(const float* inv_freq, int pos, float factor, float (&c)[8], float (&w)[8]) {
-  const float4 f0 = reinterpret_cast<const float4*>(inv_freq)[0], f1 = reinterpret_cast<const float4*>(inv_freq)[1];
-  const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+// Rows of D elements over a block of ROW_THREADS threads: 2^lanes_log lanes a
+// row (its units, rounded up to a power of two: idle lanes hold zeros),
+// 2^tokens_log tokens side by side, where tokens are fewer than the block's
+// rows several heads of each, and then `rows` heads a thread, one after the
+// other.  Blocks over the heads of one tile of tokens follow each other.
+//
+// Tokens side by side, not heads: [B, H, T, D] tensors have their heads
+// megabytes apart, often by a power of two, and with four heads of eight tokens
+// side by side 2 x 8192 tokens of 32 + 2 heads of 128 took 123 us in place of
+// 54, their gradients 188 in place of 90.
+constexpr int ROW_THREADS = 256;
+template <int SIDES>
+struct RowPlan {
+  int lanes_log, tokens_log, rows;
+  int groups[SIDES], all_groups;  // blocks over each tensor's heads, over all
+  uint32_t tiles;
+  __host__ __device__ int head_step() const { return ROW_THREADS >> lanes_log >> tokens_log; }
+};
+// False if there are too many blocks.  A thread gets up to `most` rows (a power of two): as many as leave six blocks a
+// SM (4 x 1031 fp32 rows of 16 + 2 heads of 64: 12.8 us; three blocks 15.0, nine 14.6).
+template <int SIDES>
+bool plan_rows(RowPlan<SIDES>& p, long long tokens, const int (&heads)[SIDES], int D, int most) {
+  p.lanes_log = p.tokens_log = 0;
+  while ((UNIT << p.lanes_log) < D) ++p.lanes_log;
+  const int slots = ROW_THREADS >> p.lanes_log;
+  while ((2 << p.tokens_log) <= slots && (1LL << p.tokens_log) < tokens) ++p.tokens_log;
+  const long long tiles = (tokens + (1LL << p.tokens_log) - 1) >> p.tokens_log;
+  long long steps = 0;
+  for (int s = 0; s < SIDES; ++s) steps += tiles * ((heads[s] + p.head_step() - 1) / p.head_step());
+  p.rows = 1;
+  while (2 * p.rows <= most && steps > 6LL * 152 * p.rows) p.rows *= 2;
+  p.all_groups = 0;
+  for (int s = 0; s < SIDES; ++s) {
+    const int per = p.head_step() * p.rows;
+    p.groups[s] = (heads[s] + per - 1) / per;
+    p.all_groups += p.groups[s];
+  }
+  p.tiles = static_cast<uint32_t>(tiles);
+  return tiles * p.all_groups <= 0x7fffffffLL;
+}
+
+// What a thread holds: tensor and its group of heads, tile, token (and whether it and the unit are there), first head
+// and how many heads, `head_step` apart; `most`: the most of the block's threads.
+struct RowPlace {
+  int side, group;
+  uint32_t tile, token;
+  int head, rows, most, head_step, unit;
+  bool live;
+};
+template <int SIDES>
+__device__ __forceinline__ RowPlace place_of(const RowPlan<SIDES>& p, long long tokens, const int (&heads)[SIDES], int D) {
+  RowPlace x;
+  x.tile = blockIdx.x / p.all_groups;
+  x.group = static_cast<int>(blockIdx.x % p.all_groups);
+  x.side = 0;
+  int H = heads[0];
+#pragma unroll
+  for (int s = 1; s < SIDES; ++s)
+    if (x.side == s - 1 && x.group >= p.groups[s - 1]) {
+      x.group -= p.groups[s - 1];
+      x.side = s;
+      H = heads[s];
+    }
+  x.unit = threadIdx.x & ((1 << p.lanes_log) - 1);
+  const int slot = static_cast<int>(threadIdx.x) >> p.lanes_log;
+  x.head_step = p.head_step();
+  const long long token =
+      (static_cast<long long>(x.tile) << p.tokens_log) + (slot & ((1 << p.tokens_log) - 1));
+  x.live = token < tokens && x.unit * UNIT < D;
+  x.token = x.live ? static_cast<uint32_t>(token) : 0u;  // (all tokens together are a 31-bit number)
+  const int head0 = x.group * x.head_step * p.rows;
+  x.head = head0 + (slot >> p.tokens_log);
+  x.most = min(p.rows, (H - head0 - 1) / x.head_step + 1);
+  const int left = H - x.head;  // heads from this thread's first on
+  x.rows = x.live && left > 0 ? min(p.rows, (left - 1) / x.head_step + 1) : 0;
+  return x;
+}
+
+// Sum over a row's lanes (those behind its last unit: zero).
+__device__ __forceinline__ float row_sum(float x, int lanes_log, bool in_row) {
+  if (!in_row) x = 0.0f;
+  if (lanes_log > 2) x += __shfl_xor_sync(0xffffffffu, x, 4);
+  if (lanes_log > 1) x += __shfl_xor_sync(0xffffffffu, x, 2);
+  if (lanes_log > 0) x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x;
+}
+
+// A block's frequencies as fractions of a turn (rotary / 2 <= 64 of them); block-wide.
+__device__ __forceinline__ void block_turns(uint64_t (&turns)[64], const float* inv_freq, int rotary) {
+  if (static_cast<int>(threadIdx.x) < rotary / 2) turns[threadIdx.x] = turns_of(inv_freq[threadIdx.x]);
+  __syncthreads();
+}
+// Cosines and sines of a unit's eight pairs at a position, times a factor.
+__device__ __forceinline__ void unit_sincos(const uint64_t (&turns)[64], int freq, int pos, float factor, float (&c)[8],
+                                            float (&w)[8]) {
+  sincos8(turns, freq, pos, c, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint64_t t = turns_of(f[j]) * static_cast<uint64_t>(static_cast<int64_t>(pos));
-    sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f, &w[j], &c[j]);
     c[j] *= factor;
     w[j] *= factor;
   }
 }
 
-// Rows of D elements over a block of ROW_THREADS threads: 2^lanes_log lanes a
-// row (the units of a row, rounded up to a power of two: idle lanes hold
-// zeros), `tokens` of them at once for each of ROW_THREADS / lanes / tokens
-// heads, and `rows` heads a thread one after the other.
-constexpr int ROW_THREADS = 256;
-struct RowTile {
-  int lanes_log, tokens_log;
-  int rows;
-};
-
-// Fills a block's slots with tokens, then with heads, and gives a thread up to `most` rows once every SM has
-// blocks enough (152 x 128 row slots are four blocks a SM of rows of 128).
-inline RowTile row_tile(long long tokens, int heads, int D, int most) {
-  RowTile t{0, 0, 1};
-  while ((UNIT << t.lanes_log) < D) ++t.lanes_log;
-  const int slots = ROW_THREADS >> t.lanes_log;
-  while ((2 << t.tokens_log) <= slots && (1LL << t.tokens_log) < tokens) ++t.tokens_log;
-  const long long share = tokens * heads / (152LL * 4 * slots);
-  while (2 * t.rows <= most && 2 * t.rows <= share) t.rows *= 2;
-  return t;
-}
-// Heads of one block.
-__host__ __device__ inline int row_heads(const RowTile& t) {
-  return (ROW_THREADS >> t.lanes_log >> t.tokens_log) * t.rows;
-}
-
-// Sum over a row's lanes.
-__device__ __forceinline__ float row_sum(float x, int lanes_log) {
-  for (int d = (1 << lanes_log) >> 1; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-  return x;
-}
-
-// A unit as it lies in memory, read ahead of its use.
+// A unit's 16-byte pieces as numbers.
 template <typename T>
-struct RawUnit {
-  uint4 v[sizeof(T)];
-  __device__ __forceinline__ void load(const T* row, const UnitMap& m) {
-    const uint4 *lo = reinterpret_cast<const uint4*>(row + m.lo), *hi = reinterpret_cast<const uint4*>(row + m.hi);
+__device__ __forceinline__ void unpack(const uint4 (&v)[sizeof(T)], float (&x)[UNIT]) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
-      v[i] = lo[i];
-      v[sizeof(T) / 2 + i] = hi[i];
-    }
-  }
-  __device__ __forceinline__ void clear() {
+  for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  __device__ __forceinline__ void unpack(float (&x)[UNIT]) const {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(T) == 2) {
-          x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-          x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        } else {
-          x[4 * i + j] = __uint_as_float(w[j]);
-        }
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 2) {
+        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      } else {
+        x[4 * i + j] = __uint_as_float(w[j]);
       }
     }
   }
+}
+
+// Rows on their way to a thread: a ring in shared memory that each thread fills and reads for itself, so that it needs
+// no barrier and no registers, in batches of BATCH rows, one in work and one on its way.  A batch's rows are asked for
+// at once: out of a projection's layout that is a kilobyte a token.  (In registers, two rows ahead one by one, 2 x 8192
+// tokens of 32 + 2 heads of 128 took 54 us in place of 47, their gradients 90 in place of 72.)
+template <typename T, int TENSORS>
+struct RowRing {
+  static constexpr int BATCH = 8 / (static_cast<int>(sizeof(T)) * TENSORS);  // bf16: 4; two tensors or fp32: half
+  static constexpr int PIECES = static_cast<int>(sizeof(T));                 // 16-byte pieces of a unit
+  static constexpr int BYTES = 2 * BATCH * TENSORS * PIECES * ROW_THREADS * 16;
+  uint32_t mine;
+  __device__ __forceinline__ explicit RowRing(const void* smem) : mine(smem_u32(smem) + threadIdx.x * 16) {}
+  __device__ __forceinline__ uint32_t at(int slot, int tensor, int piece) const {
+    return mine + ((slot * TENSORS + tensor) * PIECES + piece) * (ROW_THREADS * 16);
+  }
+  // A unit whose first run starts at lo, its second `apart` elements behind it.
+  __device__ __forceinline__ void ask(int slot, int tensor, const T* lo, int apart) const {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const void* from = reinterpret_cast<const uint4*>(i < PIECES / 2 ? lo : lo + apart) + i % (PIECES / 2);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(slot, tensor, i)), "l"(from) : "memory");
+    }
+  }
+  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Until all but the batch asked for last are there.
+  __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+  __device__ __forceinline__ void take(int slot, int tensor, float (&x)[UNIT]) const {
+    uint4 v[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                   : "r"(at(slot, tensor, i))
+                   : "memory");
+    unpack<T>(v, x);
+  }
 };
+
+// Norm and rotation of a unit as one linear map times the row's factor: with c, w the pairs' cosines and sines and g the
+// weights (1 without), y_a = s (g_a c x_a - g_b w x_b), y_b = s (g_a w x_a + g_b c x_b).
+struct UnitMap2 {
+  float aa[8], ab[8], ba[8], bb[8];
+};
+template <bool INTERLEAVED>
+__device__ __forceinline__ void make_map(UnitMap2& m, const float (&c)[8], const float (&w)[8], const float (&g)[UNIT]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float ga = g[INTERLEAVED ? 2 * j : j], gb = g[INTERLEAVED ? 2 * j + 1 : 8 + j];
+    m.aa[j] = ga * c[j];
+    m.ab[j] = -gb * w[j];
+    m.ba[j] = ga * w[j];
+    m.bb[j] = gb * c[j];
+  }
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ void apply_map(const UnitMap2& m, float s, float (&x)[UNIT]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int ia = INTERLEAVED ? 2 * j : j, ib = INTERLEAVED ? 2 * j + 1 : 8 + j;
+    const float a = x[ia], b = x[ib];
+    x[ia] = s * fmaf(m.ab[j], b, m.aa[j] * a);
+    x[ib] = s * fmaf(m.bb[j], b, m.ba[j] * a);
+  }
+}
 
 // Sixteen weights of a unit.
 __device__ __forceinline__ void load_weights(const void* w, bool f32, const UnitMap& m, float (&x)[UNIT]) {

@@ -754,6 +754,7 @@ BSA_API int qk_norm_rope_backward(const void* q, const void* k,
  *                rotated).
  *   strides    : batch, head and token stride of k, v and q (9 numbers), as for
  *                qk_norm_rope_forward, or NULL.
+ *   n          : 1 to 2^30.   B * n <= 2^31 - 1.
  *   No token slot may be written twice in one call.
  *
  * nsa_cache4_read -- the values of tokens starts[b] + i, i < n, of each
@@ -762,9 +763,11 @@ BSA_API int qk_norm_rope_backward(const void* q, const void* k,
  *   k_out, v_out : [B, Hkv, n, D] of `dtype`; rows without a token, or whose
  *                page is not in the pool, are zero.
  *   starts     : [B] int32 or NULL (0); a negative one has no tokens.
+ *   n          : 1 to 2^30.
  *
- * nsa_cache4_decode -- nsa_select_decode over it, with the same arguments, sums,
- * roundings and workspace size rule (k_t and v_t enter the products unrounded).
+ * nsa_cache4_decode -- nsa_select_decode over it, with the same arguments, sums
+ * and roundings (k_t and v_t enter the products unrounded), in a workspace of
+ * nsa_cache4_decode_workspace_size(...) bytes.
  *
  * Errors: as for the e4m3 cache, and those of qk_norm_rope_forward.
  */
