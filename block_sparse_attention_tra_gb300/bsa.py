@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -270,9 +271,14 @@ def nsa_select_decode_raw(q, k_cache, v_cache, k_scale, v_scale, page_table, cac
                                             int(workspace_bytes), stream)
 
 
+@functools.lru_cache(maxsize=256)
+def _stride_array(numbers):
+    return (ctypes.c_int64 * len(numbers))(*numbers)
+
+
 def _strides(numbers):
-    """Strides in elements as the C entry points take them (None: all contiguous)."""
-    return None if numbers is None else (ctypes.c_int64 * len(numbers))(*numbers)
+    """Strides in elements as the C entry points take them (None: all contiguous); made once for each tuple."""
+    return None if numbers is None else _stride_array(tuple(numbers))
 
 
 def qk_norm_rope_forward_raw(q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq, strides, B, Hq, Hkv, T, D,
@@ -992,15 +998,20 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
 def _row_strides(t):
     """``t`` [B, H, T, D] as the kernels read rows in place, and its (batch, head, token) strides; a copy where a row's
     elements do not follow each other or do not start on a 16-byte boundary."""
-    unit = 16 // t.element_size()
-    sizes, st = t.shape, t.stride()
-    s = [0 if n == 1 else x for n, x in zip(sizes, st)]
-    if st[3] != 1 or s[0] % unit or s[1] % unit or s[2] % unit or t.data_ptr() % 16:
+    sb, sh, st, sd = t.stride()
+    nb, nh, nt, _ = t.shape
+    if nb == 1:
+        sb = 0
+    if nh == 1:
+        sh = 0
+    if nt == 1:
+        st = 0
+    if sd != 1 or (sb | sh | st) % (16 // t.element_size()) or t.data_ptr() % 16:
         t = t.contiguous()
         if t.data_ptr() % 16:
             t = t.clone()
-        s = t.stride()
-    return t, s[:3]
+        sb, sh, st, _ = t.stride()
+    return t, (sb, sh, st)
 
 
 def _rows_like(torch, t):
@@ -1018,40 +1029,58 @@ def _aligned(t):
 def _row_parameters(torch, what, q_weight, k_weight, inv_freq, D):
     """Weights of one dtype and frequencies as the kernels take them; (q_weight, k_weight, their dtype, inv_freq)."""
     kind = BSA_F32
-    given = [w for w in (q_weight, k_weight) if w is not None]
-    if given:
-        if any(w.shape != (D,) for w in given):
-            raise BsaError(f"{what}: weights must be [{D}]", 2)
-        if all(w.dtype is torch.bfloat16 for w in given):
+    if q_weight is not None or k_weight is not None:
+        types = []
+        for w in (q_weight, k_weight):
+            if w is not None:
+                if w.shape != (D,):
+                    raise BsaError(f"{what}: weights must be [{D}]", 2)
+                types.append(w.dtype)
+        if types[0] is types[-1] is torch.bfloat16:
             kind = BSA_BF16
-        elif any(w.dtype not in (torch.bfloat16, torch.float32) for w in given):
-            raise BsaError(f"{what}: weights must be float32 or bfloat16", 3)
-        if kind == BSA_F32:
-            q_weight, k_weight = (None if w is None else w.to(torch.float32) for w in (q_weight, k_weight))
-        q_weight, k_weight = (None if w is None else _aligned(w.contiguous()) for w in (q_weight, k_weight))
+        elif not (types[0] is types[-1] is torch.float32):
+            if any(x not in (torch.bfloat16, torch.float32) for x in types):
+                raise BsaError(f"{what}: weights must be float32 or bfloat16", 3)
+            q_weight, k_weight = q_weight.to(torch.float32), k_weight.to(torch.float32)
+        if q_weight is not None and (q_weight.data_ptr() % 16 or not q_weight.is_contiguous()):
+            q_weight = _aligned(q_weight.contiguous())
+        if k_weight is not None and (k_weight.data_ptr() % 16 or not k_weight.is_contiguous()):
+            k_weight = _aligned(k_weight.contiguous())
     if inv_freq is not None:
         if inv_freq.dim() != 1:
             raise BsaError(f"{what}: inv_freq must be [rotary_dim / 2]", 2)
-        inv_freq = _aligned(inv_freq.to(torch.float32).contiguous()) if inv_freq.numel() else None
+        if inv_freq.dtype is not torch.float32 or inv_freq.data_ptr() % 16 or not inv_freq.is_contiguous():
+            inv_freq = _aligned(inv_freq.to(torch.float32).contiguous())
+        if not inv_freq.numel():
+            inv_freq = None
     return q_weight, k_weight, kind, inv_freq
 
 
 def _row_inputs(torch, what, q, k, q_weight, k_weight, inv_freq, positions):
     """Checks of ``qk_norm_rope``'s inputs; (q_weight, k_weight, their dtype, inv_freq, positions)."""
-    if q.dim() != 4 or k.dim() != 4 or q.shape[0] != k.shape[0] or q.shape[2:] != k.shape[2:]:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or qs[0] != ks[0] or qs[2:] != ks[2:]:
         raise BsaError(f"{what}: q [B,Hq,T,D] and k [B,Hkv,T,D] expected", 2)
-    if q.dtype != k.dtype:
+    if q.dtype is not k.dtype:
         raise BsaError(f"{what}: q and k must share one dtype", 3)
-    B, T = q.shape[0], q.shape[2]
     if positions is not None:
-        if positions.shape not in ((B, T), (T,)):
-            raise BsaError(f"{what}: positions must be [B,T] or [T]", 2)
-        positions = _int32(torch, positions.expand(B, T))
-    return (*_row_parameters(torch, what, q_weight, k_weight, inv_freq, q.shape[3]), positions)
+        shape = (qs[0], qs[2])
+        if positions.shape != shape:
+            if positions.shape != shape[1:]:
+                raise BsaError(f"{what}: positions must be [B,T] or [T]", 2)
+            positions = positions.expand(shape)
+        positions = _int32(torch, positions)
+    return (*_row_parameters(torch, what, q_weight, k_weight, inv_freq, qs[3]), positions)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _raw_stream(torch, dev):
+    """The handle of the device's current stream (without a stream object around it, which takes a microsecond)."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(dev).cuda_stream if get is None else get(dev)
 
 
 def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, interleaved: bool = False,
@@ -1083,21 +1112,26 @@ def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, inv_freq=None, posi
     qw, kw, kind, freq, pos = _row_inputs(torch, what, q, k, q_weight, k_weight, inv_freq, positions)
     B, Hq, T, D = q.shape
     Hkv = k.shape[1]
-    written = []
-    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is not None:
-            _in_place(what, name, t, like.shape, like.dtype)
-            written.append(t)
+    written = None
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _in_place(what, "q_out", q_out, q.shape, q.dtype)
+        written = [q_out]
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    else:
+        _in_place(what, "k_out", k_out, k.shape, k.dtype)
+        written = [*(written or ()), k_out]
     (q, qs), (k, ks) = _row_strides(q), _row_strides(k)
-    st = qk_norm_rope_forward_raw(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(qw), _ptr(kw),
-                                  _ptr(pos), _ptr(freq), (*qs, *ks, Hq * T * D, T * D, D, Hkv * T * D, T * D, D), B,
-                                  Hq, Hkv, T, D, 0 if freq is None else 2 * freq.numel(), interleaved, rotary_scale,
-                                  eps, _dtype_code(q), kind, torch.cuda.current_stream(dev).cuda_stream)
-    _check(st, what)
+    row = T * D
+    st = load_library().qk_norm_rope_forward(
+        q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(qw), _ptr(kw), _ptr(pos), _ptr(freq),
+        _stride_array((*qs, *ks, Hq * row, row, D, Hkv * row, row, D)), B, Hq, Hkv, T, D,
+        0 if freq is None else 2 * freq.numel(), 1 if interleaved else 0, rotary_scale, eps, _dtype_code(q), kind,
+        _raw_stream(torch, dev))
+    if st:
+        _check(st, what)
     if written:
         torch.autograd.graph.increment_version(written)
     return q_out, k_out
@@ -1138,15 +1172,15 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, in
         raise BsaError(f"{what}: workspace must be contiguous", 2)
     dq, dk = _rows_like(torch, q), _rows_like(torch, k)
     dqw, dkw = (None if w is None else torch.empty(D, dtype=torch.float32, device=q.device) for w in (qw, kw))
-    rows = [_row_strides(t) for t in (q, k, dq_out, dk_out)]
-    strides = [x for _, s in rows for x in s] + [*dq.stride()[:3], *dk.stride()[:3]]
-    st = qk_norm_rope_backward_raw(*(t.data_ptr() for t, _ in rows), dq.data_ptr(), dk.data_ptr(), _ptr(dqw), _ptr(dkw),
-                                   _ptr(qw), _ptr(kw), _ptr(pos), _ptr(freq), strides, B, Hq, Hkv, T, D,
-                                   0 if freq is None else 2 * freq.numel(), interleaved, rotary_scale, eps,
-                                   _dtype_code(q), kind, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(),
-                                   torch.cuda.current_stream(dev).cuda_stream)
-    _check(st, what)
+    (q, s0), (k, s1), (dq_out, s2), (dk_out, s3) = (_row_strides(t) for t in (q, k, dq_out, dk_out))
+    st = load_library().qk_norm_rope_backward(
+        q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dqw),
+        _ptr(dkw), _ptr(qw), _ptr(kw), _ptr(pos), _ptr(freq),
+        _stride_array((*s0, *s1, *s2, *s3, *dq.stride()[:3], *dk.stride()[:3])), B, Hq, Hkv, T, D,
+        0 if freq is None else 2 * freq.numel(), 1 if interleaved else 0, rotary_scale, eps, _dtype_code(q), kind,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(torch, dev))
+    if st:
+        _check(st, what)
     return dq, dk, dqw, dkw
 
 
@@ -1201,24 +1235,26 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=No
 def _check_cache4(torch, what, k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table, cache_lens, B, Hkv,
                   D):
     """Shapes and types of the paged 4-bit cache; returns (num_pages, page_size, max_pages)."""
-    if k_cache.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != B or cache_lens.shape != (B,):
+    shape, table = k_cache.shape, page_table.shape
+    if len(shape) != 4 or len(table) != 2 or table[0] != B or cache_lens.shape != (B,):
         raise BsaError(f"{what}: k_cache [pages,Hkv,page_size,D/2], page_table [B,max_pages], cache_lens [B] expected",
                        2)
-    pages, _, page_size, _ = k_cache.shape
+    pages, _, page_size, _ = shape
     codes, scales = (pages, Hkv, page_size, D // 2), (pages, Hkv, page_size, D // 16)
-    if not (k_cache.shape == codes and v_cache.shape == codes and k_scale.shape == scales and v_scale.shape == scales
-            and k_cache.dtype is torch.uint8 and v_cache.dtype is torch.uint8
-            and k_scale.dtype in (torch.float8_e4m3fn, torch.uint8)
-            and v_scale.dtype in (torch.float8_e4m3fn, torch.uint8) and k_cache.is_contiguous()
-            and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+    kinds = torch.float8_e4m3fn, torch.uint8
+    if not (shape == codes == v_cache.shape and k_scale.shape == scales and v_scale.shape == scales
+            and k_cache.dtype is v_cache.dtype is torch.uint8 and k_scale.dtype in kinds and v_scale.dtype in kinds
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous()):
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
             _in_place(what, name, t, codes, torch.uint8)
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            _in_place(what, name, t, scales, torch.float8_e4m3fn, torch.uint8)
-    for name, t in (("k_factor", k_factor), ("v_factor", v_factor)):
-        if t is not None:
-            _in_place(what, name, t, (Hkv,), torch.float32)
-    return pages, page_size, page_table.shape[1]
+            _in_place(what, name, t, scales, *kinds)
+    if k_factor is not None:
+        _in_place(what, "k_factor", k_factor, (Hkv,), torch.float32)
+    if v_factor is not None:
+        _in_place(what, "v_factor", v_factor, (Hkv,), torch.float32)
+    return pages, page_size, table[1]
 
 
 def nsa_cache4_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, new_lens=None, inv_freq=None,
@@ -1269,7 +1305,7 @@ def nsa_cache4_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cach
         raise BsaError("new_lens must be [B]", 2)
     qw, kw, kind, freq = _row_parameters(torch, what, q_weight, k_weight, inv_freq, D)
     (k, ks), (v, vs) = _row_strides(k), _row_strides(v)
-    strides = [*ks, *vs, 0, 0, 0]
+    qs = (0, 0, 0)
     table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
     news = None if new_lens is None else _int32(torch, new_lens)
     written = [k_cache, v_cache, k_scale, v_scale]
@@ -1279,13 +1315,15 @@ def nsa_cache4_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cach
         else:
             make = torch.empty if news is None else torch.zeros
             q_out = make(q.shape, dtype=q.dtype, device=q.device)
-        q, strides[6:] = _row_strides(q)
-    st = nsa_cache4_append_raw(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
-                               k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_factor), _ptr(v_factor), table.data_ptr(),
-                               lens.data_ptr(), _ptr(news), _ptr(qw), _ptr(kw), _ptr(freq), strides, B, Hq, Hkv, n, D,
-                               page_size, max_pages, pages, 0 if freq is None else 2 * freq.numel(), interleaved,
-                               rotary_scale, eps, _dtype_code(k), kind, torch.cuda.current_stream(dev).cuda_stream)
-    _check(st, what)
+        q, qs = _row_strides(q)
+    st = load_library().nsa_cache4_append(
+        k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), _ptr(k_factor), _ptr(v_factor), table.data_ptr(), lens.data_ptr(), _ptr(news), _ptr(qw),
+        _ptr(kw), _ptr(freq), _stride_array((*ks, *vs, *qs)), B, Hq, Hkv, n, D, page_size, max_pages, pages,
+        0 if freq is None else 2 * freq.numel(), 1 if interleaved else 0, rotary_scale, eps, _dtype_code(k), kind,
+        _raw_stream(torch, dev))
+    if st:
+        _check(st, what)
     torch.autograd.graph.increment_version(written)  # a graph that saved one of them must not use it any more
     return q_out
 
@@ -1330,14 +1368,15 @@ def nsa_cache4_read(k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, 
     else:
         if n < 1:
             raise BsaError(f"{what}: n must be at least 1", 2)
-        k_out, v_out = torch.empty((2, *shape), dtype=dtype, device=k_cache.device)
+        k_out, v_out = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
     table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
     begin = None if starts is None else _int32(torch, starts)
-    st = nsa_cache4_read_raw(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                             _ptr(k_factor), _ptr(v_factor), table.data_ptr(), _ptr(begin), lens.data_ptr(),
-                             k_out.data_ptr(), v_out.data_ptr(), B, Hkv, n, D, page_size, max_pages, pages,
-                             _dtype_code(k_out), torch.cuda.current_stream(dev).cuda_stream)
-    _check(st, what)
+    st = load_library().nsa_cache4_read(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_factor), _ptr(v_factor),
+        table.data_ptr(), _ptr(begin), lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, Hkv, n, D, page_size,
+        max_pages, pages, _dtype_code(k_out), _raw_stream(torch, dev))
+    if st:
+        _check(st, what)
     if written:
         torch.autograd.graph.increment_version(written)
     return k_out, v_out
@@ -1350,7 +1389,8 @@ def nsa_cache4_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
 
     q ``[B, Hq, 1, D]`` bf16 (normalised and rotated), the cache and its factors
     as for ``nsa_cache4_append``, everything else as for ``nsa_select_decode``
-    (``workspace``: ``nsa_cache4_decode_workspace_size(...)`` bytes).
+    (``workspace``: ``nsa_cache4_decode_workspace_size(...)`` bytes; selected
+    pages use none).
     """
     import torch
 
@@ -1386,21 +1426,24 @@ def nsa_cache4_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
     q = _aligned(q.contiguous())
     table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
     idx = None if block_idx is None else _int32(torch, block_idx)
-    if workspace is None:
-        need = nsa_cache4_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S)
-        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
-    elif not workspace.is_contiguous():
-        raise BsaError(f"{what}: workspace must be contiguous", 2)
+    space = 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise BsaError(f"{what}: workspace must be contiguous", 2)
+        space = workspace.numel() * workspace.element_size()
+    elif block_idx is None:  # (selected pages need none)
+        space = max(nsa_cache4_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S), 1)
+        workspace = torch.empty(space, device=q.device, dtype=torch.uint8)
     if out is None:
         out = torch.empty_like(q)
     if lse is None and return_lse:
         lse = torch.empty((B, Hq, 1), device=q.device, dtype=torch.float32)
-    st = nsa_cache4_decode_raw(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                               v_scale.data_ptr(), _ptr(k_factor), _ptr(v_factor), table.data_ptr(), lens.data_ptr(),
-                               _ptr(idx), out.data_ptr(), _ptr(lse), B, Hq, Hkv, D, page_size, max_pages, pages, S,
-                               workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               torch.cuda.current_stream(dev).cuda_stream)
-    _check(st, what)
+    st = load_library().nsa_cache4_decode(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_factor),
+        _ptr(v_factor), table.data_ptr(), lens.data_ptr(), _ptr(idx), out.data_ptr(), _ptr(lse), B, Hq, Hkv, D,
+        page_size, max_pages, pages, S, _ptr(workspace), space, _raw_stream(torch, dev))
+    if st:
+        _check(st, what)
     if written:
         torch.autograd.graph.increment_version(written)
     return (out, lse) if return_lse else out

@@ -705,7 +705,8 @@ int nsa_cache4_decode(const void* q, const void* k_cache, const void* v_cache, c
                       const int32_t* cache_lens, const int32_t* block_idx, void* out, float* lse, int B, int Hq,
                       int Hkv, int D, int page_size, int max_pages, int num_pages, int S, void* workspace,
                       size_t workspace_bytes, cudaStream_t stream) {
-  if (q == nullptr || cache_lens == nullptr || out == nullptr || workspace == nullptr) return BSA_ERR_NULLPTR;
+  if (q == nullptr || cache_lens == nullptr || out == nullptr || (workspace == nullptr && block_idx == nullptr))
+    return BSA_ERR_NULLPTR;
   const Cache4 c = cache4_of(k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, page_table, B, Hkv, D, page_size,
                              max_pages, num_pages);
   const int st = check_cache4(c, Hq);
@@ -715,7 +716,7 @@ int nsa_cache4_decode(const void* q, const void* k_cache, const void* v_cache, c
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return BSA_ERR_ALIGN;
   if (!aligned4(cache_lens) || !aligned4(block_idx) || !aligned4(lse)) return BSA_ERR_ALIGN;
-  if (workspace_bytes < nsa_cache4_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S))
+  if (workspace != nullptr && workspace_bytes < nsa_cache4_decode_workspace_size(B, Hq, Hkv, D, page_size, max_pages, S))
     return BSA_ERR_SCRATCH_LIMIT;
   const int dev = check_device();
   return dev != OK ? dev : launch_nsa_decode4(c, q, cache_lens, block_idx, out, lse, Hq, S, workspace, stream);

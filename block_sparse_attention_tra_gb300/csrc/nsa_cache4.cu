@@ -370,9 +370,9 @@ constexpr int APPEND_ROWS = 8;  // rows a thread walks at most
 template <typename T>
 int launch_append(const Append4Args& a, bool interleaved, cudaStream_t stream) {
   auto kern = interleaved ? nsa_cache4_append_kernel<T, true> : nsa_cache4_append_kernel<T, false>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowRing<T, 1>::BYTES) != cudaSuccess)
-    return ERR_LAUNCH;
-  kern<<<a.plan.tiles * a.plan.all_groups, ROW_THREADS, RowRing<T, 1>::BYTES, stream>>>(a);
+  const int smem = RowRing<T, 1>::bytes_for(kern, a.plan.rows);
+  if (smem < 0) return ERR_LAUNCH;
+  kern<<<a.plan.tiles * a.plan.all_groups, ROW_THREADS, smem, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 

@@ -565,6 +565,111 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_strea
   }
 }
 
+// Joins the parts of a pair that several ranges cover, and answers for a sequence without tokens.  A block of two warps a
+// row, small enough to lie beside the first kernel's blocks: it works out which parts it joins while they run, and waits
+// for them before it reads one.  Each warp takes every other part, eight on their way at once.
+constexpr int JOIN_WARPS = 2, JOIN_AHEAD = 8;
+template <int D>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 16) nsa_decode4_join_kernel(const Decode4Args a) {
+  constexpr int V = D / 32 > 0 ? D / 32 : 1, LANES = D / V;  // dims of a lane, lanes of a row
+  __shared__ float2 state;
+  __shared__ float half[D];
+  const int b = static_cast<int>(blockIdx.x / a.Hq), hq = static_cast<int>(blockIdx.x % a.Hq);
+  const int h = hq / a.G, row = hq % a.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int np = stages_of(a, b);
+  float M = -INFINITY, sum = 0.0f, o[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) o[e] = 0.0f;
+  if (np > 0) {
+    // units before the sequence and in all
+    long long before = 0, units = 0;
+    for (int i = lane; i < a.B; i += 32) {
+      const int n = stages_of(a, i);
+      units += n;
+      if (i < b) before += n;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      units += __shfl_xor_sync(0xffffffffu, units, d);
+      before += __shfl_xor_sync(0xffffffffu, before, d);
+    }
+    units *= a.Hkv;
+    const long long u0 = before * a.Hkv + static_cast<long long>(h) * np, u1 = u0 + np;
+    const int c0 = range_of(units, u0, a.ranges), c1 = range_of(units, u1 - 1, a.ranges);
+    for (int base = c0; base <= c1; base += 32 * JOIN_WARPS) {
+      // this lane's part: the first that its range left if that begins within the pair, else the second (none if the
+      // range is empty: a list shorter than the ranges)
+      const int c = base + lane * JOIN_WARPS + warp;
+      const bool some = c <= c1;
+      const float* mine = a.ws + (2 * static_cast<size_t>(c) + (some && range_start(units, c, a.ranges) < u0 ? 1 : 0)) *
+                                     part_floats(D);
+      const unsigned live = __ballot_sync(0xffffffffu, some && range_start(units, c, a.ranges) <
+                                                                   range_start(units, c + 1, a.ranges));
+      if (base == c0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel is complete
+        if (c0 == c1) return;  // written by its only range
+      }
+      const float2 ml = (live >> lane & 1u) ? *reinterpret_cast<const float2*>(mine + 2 * row)
+                                            : make_float2(-INFINITY, 0.0f);
+      float n = fmaxf(M, ml.x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
+      const float nb = n == -INFINITY ? 0.0f : n, s = ex2f(M - nb), w = ex2f(ml.x - nb);
+      M = n;
+      float part_sum = ml.y * w;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) part_sum += __shfl_xor_sync(0xffffffffu, part_sum, d);
+      sum = sum * s + part_sum;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] *= s;
+      for (int k0 = 0; k0 < 32 && (live >> k0) != 0u; k0 += JOIN_AHEAD) {
+        float x[JOIN_AHEAD][V], wk[JOIN_AHEAD];
+#pragma unroll
+        for (int k = 0; k < JOIN_AHEAD; ++k) {
+          wk[k] = __shfl_sync(0xffffffffu, w, k0 + k);
+          const float* acc = reinterpret_cast<const float*>(__shfl_sync(
+                                 0xffffffffu, reinterpret_cast<unsigned long long>(mine), k0 + k)) +
+                             2 * ROWS + row * D + lane * V;
+          const bool in = (live >> (k0 + k) & 1u) && lane < LANES;
+          if constexpr (V == 4) {
+            const float4 v = in ? *reinterpret_cast<const float4*>(acc) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[k][0] = v.x;
+            x[k][1] = v.y;
+            x[k][2] = v.z;
+            x[k][3] = v.w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[k][e] = in ? acc[e] : 0.0f;
+          }
+          if (!in) wk[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < JOIN_AHEAD; ++k)
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = fmaf(wk[k], x[k][e], o[e]);
+      }
+    }
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+  if (warp == 1) {
+    if (lane == 0) state = make_float2(M, sum);
+    if (lane < LANES)
+#pragma unroll
+      for (int e = 0; e < V; ++e) half[lane * V + e] = o[e];
+  }
+  __syncthreads();
+  if (warp == 1) return;
+  const float top = fmaxf(M, state.x), tb = top == -INFINITY ? 0.0f : top, w0 = ex2f(M - tb), w1 = ex2f(state.x - tb);
+  const float total = w0 * sum + w1 * state.y, inv = inverse_sum(total);
+  if (lane < LANES)
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      a.out[static_cast<size_t>(blockIdx.x) * D + lane * V + e] =
+          __float2bfloat16_rn((w0 * o[e] + w1 * half[lane * V + e]) * inv);
+  if (a.lse != nullptr && lane == 0) a.lse[blockIdx.x] = lse_of(top, total);
+}
+
 template <int D, int C>
 int launch_select(const Decode4Args& a, cudaStream_t stream) {
   using L = Dec4<D, C>;
@@ -572,6 +677,9 @@ int launch_select(const Decode4Args& a, cudaStream_t stream) {
   // Blocks of a cluster: as many, of whole slots, as leave each a SM.
   int cs = 1;
   while (cs < 8 && 2 * cs <= a.S && 2 * items * cs <= sm_count()) cs *= 2;
+#ifdef V_CS
+  cs = V_CS;
+#endif
   auto kern = nsa_decode4_select_kernel<D, C>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
     return ERR_LAUNCH;
@@ -604,7 +712,16 @@ int launch_stream(Decode4Args a, cudaStream_t stream) {
     return ERR_LAUNCH;
   kern<<<static_cast<unsigned>(a.ranges), THREADS, L::BYTES, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
-  return launch_decode_join<D>(a, stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.B) * a.Hq));
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, nsa_decode4_join_kernel<D>, a) == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
 template <int D>

@@ -303,17 +303,17 @@ RopeArgs args_of(const RopeCall& r) {
 template <typename T>
 int launch_forward(const RopeArgs& a, bool interleaved, cudaStream_t stream) {
   auto kern = interleaved ? qk_rope_forward_kernel<T, true> : qk_rope_forward_kernel<T, false>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowRing<T, 1>::BYTES) != cudaSuccess)
-    return ERR_LAUNCH;
-  kern<<<a.plan.tiles * a.plan.all_groups, ROW_THREADS, RowRing<T, 1>::BYTES, stream>>>(a);
+  const int smem = RowRing<T, 1>::bytes_for(kern, a.plan.rows);
+  if (smem < 0) return ERR_LAUNCH;
+  kern<<<a.plan.tiles * a.plan.all_groups, ROW_THREADS, smem, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 template <typename T>
 int launch_backward(const RopeArgs& a, bool interleaved, cudaStream_t stream) {
   auto kern = interleaved ? qk_rope_backward_kernel<T, true> : qk_rope_backward_kernel<T, false>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowRing<T, 2>::BYTES) != cudaSuccess)
-    return ERR_LAUNCH;
-  kern<<<a.plan.tiles * a.plan.all_groups, ROW_THREADS, RowRing<T, 2>::BYTES, stream>>>(a);
+  const int smem = RowRing<T, 2>::bytes_for(kern, a.plan.rows);
+  if (smem < 0) return ERR_LAUNCH;
+  kern<<<a.plan.tiles * a.plan.all_groups, ROW_THREADS, smem, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? OK : ERR_LAUNCH;
 }
 

@@ -224,6 +224,15 @@ struct RowRing {
   static constexpr int BATCH = 8 / (static_cast<int>(sizeof(T)) * TENSORS);  // bf16: 4; two tensors or fp32: half
   static constexpr int PIECES = static_cast<int>(sizeof(T));                 // 16-byte pieces of a unit
   static constexpr int BYTES = 2 * BATCH * TENSORS * PIECES * ROW_THREADS * 16;
+  // Shared memory of a launch whose threads have `rows` rows, and the kernel made to take it (48 KB need no asking).
+  template <class Kernel>
+  static int bytes_for(Kernel kern, int rows) {
+    const int bytes = rows < 2 * BATCH ? BYTES / (2 * BATCH) * rows : BYTES;
+    if (bytes > 48 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES) != cudaSuccess)
+      return -1;
+    return bytes;
+  }
   uint32_t mine;
   __device__ __forceinline__ explicit RowRing(const void* smem) : mine(smem_u32(smem) + threadIdx.x * 16) {}
   __device__ __forceinline__ uint32_t at(int slot, int tensor, int piece) const {

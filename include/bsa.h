@@ -767,7 +767,8 @@ BSA_API int qk_norm_rope_backward(const void* q, const void* k,
  *
  * nsa_cache4_decode -- nsa_select_decode over it, with the same arguments, sums
  * and roundings (k_t and v_t enter the products unrounded), in a workspace of
- * nsa_cache4_decode_workspace_size(...) bytes.
+ * nsa_cache4_decode_workspace_size(...) bytes, which may be NULL where pages are
+ * selected.
  *
  * Errors: as for the e4m3 cache, and those of qk_norm_rope_forward.
  */

@@ -128,7 +128,7 @@ def decode(ws=P, nbytes=1 << 30, B=2, Hq=8, Hkv=2, D=64, page=64, max_pages=4, p
 def test_decode_refusals():
     for name in ("q", *CACHE, "table", "lens", "out"):
         assert decode(**{name: None}) == 1, name
-    assert decode(ws=None) == 1 and decode(ws=P + 8) == 7
+    assert decode(ws=None, idx=None, S=0) == 1 and decode(ws=P + 8) == 7
     for name in ("q", *CACHE, "out"):
         assert decode(**{name: P + 8}) == 7, name
     for name in ("kf", "vf", "table", "lens", "idx", "lse"):
@@ -141,6 +141,7 @@ def test_decode_refusals():
     assert bsa.nsa_cache4_decode_workspace_size(2, 8, 2, 48, 64, 4, 4) == 0
     if no_gpu:
         assert decode() == 6 and decode(idx=None, S=0, lse=None, kf=None, vf=None) == 6
+        assert decode(ws=None, nbytes=0) == 6  # selected pages need no workspace
 
 
 # ---------------------------------------------------------------- the binding
