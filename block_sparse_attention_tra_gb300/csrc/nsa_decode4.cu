@@ -27,6 +27,12 @@
 // them a cluster that shares out the slots.  Every page: the list of
 // (sequence, kv head, 128 tokens) is cut into equal contiguous ranges, one a
 // block; pairs that several ranges cover are joined by a second launch.
+//
+// Long lists run at 69% of what the measured copy rate takes for their bytes (32 sequences of 131072 tokens of 32 query
+// and 2 kv heads of 128: 1209 MB in 268 us, 4.5 TB/s): a chunk of 32 tokens is some 700 instructions of a warp (128
+// conversions, 128 products with scales, 64 matrix products of 8 cycles), and issue slots are 55% busy with eleven warps
+// or with fifteen.  About 7.5 us of every call are the chain at its start (lengths, pages, codes) and the blocks' joins:
+// four sequences of 20011 to 131072 tokens, 87 MB, take 29.5 us and the second launch; one sequence on 16 pages 6.4.
 #include <cooperative_groups.h>
 
 #include "codes4.cuh"
@@ -56,7 +62,10 @@ struct Decode4Args {
 
 template <int D, int C>
 struct Dec4 {
-  static constexpr int CTAS = D == 128 ? 3 : 4;           // blocks of a SM
+  // Blocks of a SM at most.  D = 128: 64 of a thread's registers are accumulators.  Of 128 each, sixteen warps fit (128
+  // sequences of 4 kv heads on 16 pages of 64: 27.5 us, twelve warps of 160 registers 28.4); the kernel over every page,
+  // with a range's state beside them, is faster with twelve (four sequences of up to 131072 tokens 29.5 us and 34.2).
+  static constexpr int SELECT_CTAS = 4, STREAM_CTAS = D == 128 ? 3 : 4;
   static constexpr int RING = (D == 128 ? 64 : 128) / C;  // chunks of a warp in flight or in use
   static constexpr int RB = D / 2, SB = D / 16;  // bytes of a token's codes, of its scales
   static constexpr int V_OFF = C * RB, KS_OFF = 2 * C * RB, VS_OFF = KS_OFF + C * SB;
@@ -97,43 +106,48 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t load_u8(uint32_t p) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(p) : "memory");
-  return r;
-}
-__device__ __forceinline__ uint32_t load_u16(uint32_t p) {
-  uint16_t r;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(p) : "memory");
-  return r;
-}
-// N bytes in 32-bit words (fewer than four: the low ones of one).
+// N bytes of shared memory in 32-bit words (fewer than four: the low ones of one).  (Plain loads: the compiler moves them
+// ahead of the products between two waits.)
 template <int N>
-__device__ __forceinline__ void load_bytes(uint32_t p, uint32_t (&w)[(N + 3) / 4]) {
-  if constexpr (N >= 4) {
-    const Words<N> x = load_shared<N>(p);
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) w[i] = x.w[i];
+__device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t (&w)[(N + 3) / 4]) {
+  if constexpr (N == 16) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  } else if constexpr (N == 8) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else if constexpr (N == 4) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
-    w[0] = N == 2 ? load_u16(p) : load_u8(p);
+    w[0] = N == 2 ? *reinterpret_cast<const uint16_t*>(p) : *p;
   }
 }
 
-// The chunks of one warp: its share of a range, page by page, and their way into its ring.
+// A warp's pages in shared memory: SELECT: first token (-1: none) and pool page of each slot; else the pool pages w0 + i.
+struct PageList {
+  int tok[32], id[32];
+};
+
+// The chunks of one warp: its share of a range, page by page, and their way into its ring.  (Kept small: what does not
+// fit into a thread's registers beside the accumulators is read again out of the L2, as the rings leave little L1.)
 template <int D, int C, bool SELECT>
 struct Feed {
   using L = Dec4<D, C>;
   const Decode4Args& a;
-  int h, len, page_log, x, end;  // next chunk, chunks of the range
-  int first;                     // SELECT: first slot; else first token
-  int my_tok, my_id;             // SELECT: the slots' first tokens (-1: none) and pool pages, one a lane
-  int w0, id, id_next;           // else: pool pages w0 + lane and the 32 behind them
-  uint32_t ring;
+  PageList& list;
+  int h, len, x, end;  // next chunk, chunks of the range
+  int first;           // SELECT: first slot; else first token
+  int w0, id_next;     // else: the list's first page; a page of the list after it
   const int32_t* row;
-  int n_pages;
+  uint32_t ring;
 
+  __device__ __forceinline__ int page_log() const { return 31 - __clz(a.page); }
   __device__ __forceinline__ int page_id(int p) const {
-    if (p >= n_pages) return -1;
+    if (p >= pieces_of(len, page_log())) return -1;
     const int i = row[p];
     return i < a.num_pages ? i : -1;
   }
@@ -148,10 +162,10 @@ struct Feed {
     while (x < end) {
       int tok0, page;
       if constexpr (SELECT) {
-        const int cpp_log = page_log - (C == 32 ? 5 : 4), u = first + (x >> cpp_log);
+        const int cpp_log = page_log() - (C == 32 ? 5 : 4), u = first + (x >> cpp_log);
         const int sub = x & ((1 << cpp_log) - 1);
-        tok0 = __shfl_sync(0xffffffffu, my_tok, u);
-        page = __shfl_sync(0xffffffffu, my_id, u);
+        tok0 = list.tok[u];
+        page = list.id[u];
         x += WARPS;
         if (tok0 < 0) continue;
         tok0 += sub * C;
@@ -159,17 +173,23 @@ struct Feed {
       } else {
         tok0 = first + x * C;
         x += WARPS;
-        const int p = tok0 >> page_log;
-        while (p >= w0 + 32) {
-          w0 += 32;
-          id = id_next;
-          id_next = page_id(w0 + 32 + lane);
+        const int p = tok0 >> page_log();
+        if (p >= w0 + 32) {
+          int id;
+          do {
+            w0 += 32;
+            id = id_next;
+            id_next = page_id(w0 + 32 + lane);
+          } while (p >= w0 + 32);
+          __syncwarp();
+          list.id[lane] = id;
+          __syncwarp();
         }
-        page = __shfl_sync(0xffffffffu, id, p - w0);
+        page = list.id[p - w0];
         if (page < 0) continue;
       }
-      debug_check(page >= 0 && page < a.num_pages && tok0 + C <= n_pages << page_log);
-      const size_t at = ((static_cast<size_t>(page) * a.Hkv + h) << page_log) + (tok0 & ((1 << page_log) - 1));
+      debug_check(page >= 0 && page < a.num_pages && tok0 + C <= pieces_of(len, page_log()) << page_log());
+      const size_t at = ((static_cast<size_t>(page) * a.Hkv + h) << page_log()) + (tok0 & (a.page - 1));
       const uint32_t dst = ring + place * L::SLOT;
       const uint8_t *k = a.k + at * L::RB + lane * 16, *v = a.v + at * L::RB + lane * 16;
 #pragma unroll
@@ -194,7 +214,8 @@ struct Feed {
 // (log2 domain) in M and its sum of exponentials in sum.
 template <int D, int C, bool SELECT>
 __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h, int p0, int p1, uint8_t* smem,
-                                             float (*ml)[ROWS][2], float (&y)[D / 8], float& M, float& sum) {
+                                             PageList* lists, float (*ml)[ROWS][2], float (&y)[D / 8], float& M,
+                                             float& sum) {
   using L = Dec4<D, C>;
   constexpr int NT = D / 8, KS = D / 16, RING = L::RING;
   float(*merge)[ROWS][L::CST] = reinterpret_cast<float(*)[ROWS][L::CST]>(smem);
@@ -203,41 +224,39 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
   const int len = tokens_of(a, b);
   const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
 
-  Feed<D, C, SELECT> feed{a};
+  Feed<D, C, SELECT> feed{a, lists[warp]};
   feed.h = h;
   feed.len = len;
-  feed.page_log = 31 - __clz(a.page);
   feed.x = warp;
   feed.first = p0;
   feed.ring = smem_u32(smem) + warp * RING * L::SLOT;
   feed.row = a.table + static_cast<size_t>(b) * a.max_pages;
-  feed.n_pages = pieces_of(len, feed.page_log);
   if constexpr (SELECT) {
     const SlotRow sel = nsa_live_slots(a.block_idx + (static_cast<size_t>(b) * a.Hkv + h) * a.S, a.S, len - 1,
-                                       feed.n_pages, a.page);
-    feed.my_tok = -1;
-    feed.my_id = 0;
+                                       pieces_of(len, feed.page_log()), a.page);
+    int tok = -1, id = 0;
     if (lane >= p0 && lane < p1 && ((sel.live >> lane) & 1u)) {
-      const int id = feed.row[sel.blk_lane];
-      if (id >= 0 && id < a.num_pages) {
-        feed.my_id = id;
-        feed.my_tok = sel.blk_lane * a.page;
-      }
+      id = feed.row[sel.blk_lane];
+      if (id >= 0 && id < a.num_pages) tok = sel.blk_lane * a.page;
     }
-    feed.end = (p1 - p0) << (feed.page_log - (C == 32 ? 5 : 4));
+    lists[warp].tok[lane] = tok;
+    lists[warp].id[lane] = id;
+    feed.end = (p1 - p0) << (feed.page_log() - (C == 32 ? 5 : 4));
   } else {
-    feed.w0 = p0 >> feed.page_log;
-    feed.id = feed.page_id(feed.w0 + lane);
+    feed.w0 = p0 >> feed.page_log();
+    lists[warp].id[lane] = feed.page_id(feed.w0 + lane);
     feed.id_next = feed.page_id(feed.w0 + 32 + lane);
     feed.end = (p1 - p0 + C - 1) / C;
   }
+  __syncwarp();
+  const uint8_t* ring = smem + warp * RING * L::SLOT;
   int ahead[RING - 1];  // first tokens of those on their way, the next first
 #pragma unroll
   for (int i = 0; i < RING - 1; ++i) ahead[i] = feed.put(i);
 
   // query fragments, in the order of the keys' codes; each row under its own power of two.  The warps share them, and
   // write a share each.
-  const uint32_t q_frag = smem_u32(smem) + L::Q_OFF + lane * 16;
+  uint8_t* q_frag = smem + L::Q_OFF + lane * 16;
   float f0, f1;  // score factors of rows g and g + 8
   {
     uint2 w[2][KS];
@@ -273,9 +292,8 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
       if (ks % WARPS == warp)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_frag + ks * 512), "r"(two(w[0][ks].x, up[0])),
-                     "r"(two(w[1][ks].x, up[1])), "r"(two(w[0][ks].y, up[0])), "r"(two(w[1][ks].y, up[1]))
-                     : "memory");
+        *reinterpret_cast<uint4*>(q_frag + ks * 512) = make_uint4(two(w[0][ks].x, up[0]), two(w[1][ks].x, up[1]),
+                                                                  two(w[0][ks].y, up[0]), two(w[1][ks].y, up[1]));
   }
   __syncthreads();
 
@@ -293,7 +311,7 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
     ahead[RING - 2] = feed.put(place == 0 ? RING - 1 : place - 1);
     copy_wait<RING - 1>();
     __syncwarp();  // and every lane's copies of this one are there
-    const uint32_t src = feed.ring + place * L::SLOT;
+    const uint8_t* src = ring + place * L::SLOT;
     place = place == RING - 1 ? 0 : place + 1;
     // ---- scores: slices of 16 tokens, two tiles of 8 each; tile j's column n is token 4 (n / 2) + 2 j + n % 2
     float sc[C / 8][4];
@@ -304,13 +322,13 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
       for (int j = 0; j < 2; ++j) {
         const int tk = 8 * jj + 4 * (g >> 1) + 2 * j + (g & 1);
         load_bytes<D / 8>(src + place_of<D>(tk * L::RB + t * (D / 8)), kw[j]);
-        const uint32_t sp = src + L::KS_OFF + tk * L::SB + t * (D / 4) / 16;
+        const uint8_t* sp = src + L::KS_OFF + tk * L::SB + t * (D / 4) / 16;
         if constexpr (D == 128) {
-          const uint32_t s = load_u16(sp);
+          const uint32_t s = *reinterpret_cast<const uint16_t*>(sp);
           ks2[j][0] = f16_of_scales(__byte_perm(s, 0u, 0x4400));
           ks2[j][1] = f16_of_scales(__byte_perm(s, 0u, 0x4411));
         } else {
-          ks2[j][0] = f16_of_scales(load_u8(sp) * 0x101u);
+          ks2[j][0] = f16_of_scales(*sp * 0x101u);
         }
         sc[jj + j][0] = sc[jj + j][1] = sc[jj + j][2] = sc[jj + j][3] = 0.0f;
       }
@@ -325,9 +343,10 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
         }
 #pragma unroll
         for (int i = 0; i < 2 && 2 * k + i < KS; ++i) {
-          const Words<16> q = load_shared<16>(q_frag + (2 * k + i) * 512);
+          uint32_t q[4];
+          load_bytes<16>(q_frag + (2 * k + i) * 512, q);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) mma_f16(sc[jj + j], q.w, x[j][2 * i], x[j][2 * i + 1]);
+          for (int j = 0; j < 2; ++j) mma_f16(sc[jj + j], q, x[j][2 * i], x[j][2 * i + 1]);
         }
       }
     }
@@ -392,7 +411,7 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         load_bytes<D / 16>(src + L::V_OFF + place_of<D>((tk + i) * L::RB + g * (D / 16)), vw[i]);
-        vs[i] = load_u8(src + L::VS_OFF + (tk + i) * L::SB + g * (D / 8) / 16);
+        vs[i] = src[L::VS_OFF + (tk + i) * L::SB + g * (D / 8) / 16];
       }
       if (tail) {  // scales behind the last token may be anything
 #pragma unroll
@@ -401,18 +420,17 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
       }
       const uint32_t s01 = f16_of_scales(vs[0] | vs[1] << 8), s23 = f16_of_scales(vs[2] | vs[3] << 8);
 #pragma unroll
-      for (int w = 0; w < (D / 16 + 3) / 4; ++w) {
-        // even and odd nibbles of tokens 0 and 1, 2 and 3 side by side
-        constexpr uint32_t LOW = 0x0f0f0f0fu;
-        uint32_t x01[2][4], x23[2][4];
-        f16_of_codes((vw[0][w] & LOW) | (vw[1][w] << 4 & ~LOW), x01[0]);
-        f16_of_codes((vw[0][w] >> 4 & LOW) | (vw[1][w] & ~LOW), x01[1]);
-        f16_of_codes((vw[2][w] & LOW) | (vw[3][w] << 4 & ~LOW), x23[0]);
-        f16_of_codes((vw[2][w] >> 4 & LOW) | (vw[3][w] & ~LOW), x23[1]);
+      for (int w = 0; w < (D / 16 + 3) / 4; ++w)
 #pragma unroll
-        for (int i = 0; i < 8 && i < NT; ++i)
-          mma_f16(acc[8 * w + i], pa, mul_f16x2(x01[i & 1][i >> 1], s01), mul_f16x2(x23[i & 1][i >> 1], s23));
-      }
+        for (int odd = 0; odd < 2; ++odd) {  // even and odd nibbles of tokens 0 and 1, 2 and 3 side by side
+          constexpr uint32_t LOW = 0x0f0f0f0fu;
+          uint32_t x01[4], x23[4];
+          f16_of_codes(odd ? (vw[0][w] >> 4 & LOW) | (vw[1][w] & ~LOW) : (vw[0][w] & LOW) | (vw[1][w] << 4 & ~LOW), x01);
+          f16_of_codes(odd ? (vw[2][w] >> 4 & LOW) | (vw[3][w] & ~LOW) : (vw[2][w] & LOW) | (vw[3][w] << 4 & ~LOW), x23);
+#pragma unroll
+          for (int i = 0; i < 4 && 2 * i + odd < NT; ++i)
+            mma_f16(acc[8 * w + 2 * i + odd], pa, mul_f16x2(x01[i], s01), mul_f16x2(x23[i], s23));
+        }
     }
   }
   copy_wait<0>();
@@ -471,9 +489,10 @@ __device__ __forceinline__ void store_result(const Decode4Args& a, size_t row, i
 
 // Selected pages: a cluster for each (sequence, kv head), its slots shared out over the cluster's blocks.
 template <int D, int C>
-__global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_select_kernel(const Decode4Args a) {
+__global__ void __launch_bounds__(THREADS, (Dec4<D, C>::SELECT_CTAS)) nsa_decode4_select_kernel(const Decode4Args a) {
   using L = Dec4<D, C>;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ PageList lists[WARPS];
   __shared__ float ml[WARPS][ROWS][2];
   __shared__ float part_ml[ROWS][2];
   const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
@@ -482,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_selec
   const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
   const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
   float y[D / 8], M, sum;
-  decode_range<D, C, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, ml, y, M, sum);
+  decode_range<D, C, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, lists, ml, y, M, sum);
   if (cs == 1) {
     if (row < a.G) store_result<D>(a, qrow + row, d0, y, M, sum);
     return;
@@ -522,9 +541,10 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_selec
 // Every page: a block on one contiguous range of the (sequence, kv head, stage) list; stage k holds tokens 128 k .. of
 // the sequence.
 template <int D, int C>
-__global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_stream_kernel(const Decode4Args a) {
+__global__ void __launch_bounds__(THREADS, (Dec4<D, C>::STREAM_CTAS)) nsa_decode4_stream_kernel(const Decode4Args a) {
   using L = Dec4<D, C>;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ PageList lists[WARPS];
   __shared__ float ml[WARPS][ROWS][2];
   // the joining kernel's blocks may take the places that this one's leave (they wait for all of it)
   asm volatile("griddepcontrol.launch_dependents;");
@@ -535,12 +555,21 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::CTAS)) nsa_decode4_strea
   long long before;
   int b = sequence_of(a, u0, &before);
   int n_st = stages_of(a, b);
-  int h = static_cast<int>((u0 - before) / n_st), s0 = static_cast<int>((u0 - before) % n_st);
+  // (a sequence's units are fewer than 2^31 heads of 2^24 stages; nearly always a 32-bit number)
+  const long long in = u0 - before;
+  int h, s0;
+  if (in >> 32 == 0) {
+    h = static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(n_st));
+    s0 = static_cast<int>(static_cast<uint32_t>(in) % static_cast<uint32_t>(n_st));
+  } else {
+    h = static_cast<int>(in / n_st);
+    s0 = static_cast<int>(in % n_st);
+  }
   for (long long u = u0; u < u1;) {
     const int s1 = static_cast<int>(min(static_cast<long long>(n_st), s0 + (u1 - u)));
     const int end = static_cast<int>(min(static_cast<uint32_t>(s1) << STAGE_LOG, static_cast<uint32_t>(tokens_of(a, b))));
     float y[D / 8], M, sum;
-    decode_range<D, C, false>(a, b, h, s0 << STAGE_LOG, end, smem, ml, y, M, sum);
+    decode_range<D, C, false>(a, b, h, s0 << STAGE_LOG, end, smem, lists, ml, y, M, sum);
     if (row < a.G) {
       if (s0 == 0 && s1 == n_st) {
         store_result<D>(a, static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G + row, d0, y, M, sum);
@@ -674,12 +703,10 @@ template <int D, int C>
 int launch_select(const Decode4Args& a, cudaStream_t stream) {
   using L = Dec4<D, C>;
   const long long items = static_cast<long long>(a.B) * a.Hkv;
-  // Blocks of a cluster: as many, of whole slots, as leave each a SM.
+  // Blocks of a cluster: as many, of whole slots, as leave each a SM.  More do not pay for their start and their join (512
+  // pairs: one block a pair 30 us, two 44, four 54).
   int cs = 1;
   while (cs < 8 && 2 * cs <= a.S && 2 * items * cs <= sm_count()) cs *= 2;
-#ifdef V_CS
-  cs = V_CS;
-#endif
   auto kern = nsa_decode4_select_kernel<D, C>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
     return ERR_LAUNCH;
@@ -704,7 +731,7 @@ int launch_stream(Decode4Args a, cudaStream_t stream) {
   if (sms < 1) return ERR_DEVICE;
   const long long units = static_cast<long long>(a.B) * a.Hkv *
                           ((static_cast<long long>(a.max_pages) * a.page + STAGE_TOK - 1) / STAGE_TOK);
-  const long long places = static_cast<long long>(sms) * L::CTAS;
+  const long long places = static_cast<long long>(sms) * L::STREAM_CTAS;
   const long long most = places < DECODE4_MAX_RANGES ? places : DECODE4_MAX_RANGES;
   a.ranges = static_cast<int>(units < most ? units : most);
   auto kern = nsa_decode4_stream_kernel<D, C>;
