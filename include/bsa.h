@@ -12,14 +12,18 @@
  * in a caller-provided workspace) and its gradients (nsa_select_backward, in a
  * workspace too), tra_forward_host, which takes host buffers and streams them
  * through the GPU, and for serving a paged e4m3 cache: nsa_cache_append writes
- * new tokens into it, nsa_select_decode attends to it with one query token.
+ * new tokens into it, nsa_select_decode attends to it with one query token;
+ * nsa_cache4_append, nsa_cache4_read and nsa_cache4_decode do so over a cache of
+ * 4-bit codes.  qk_norm_rope_forward (and _backward) is what stands before the
+ * attention: the norm of query and key heads and their rotation by position.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Every tensor pointer is caller-owned DEVICE memory (cudaMalloc or a
  *   framework allocator) on the current device, except the host tensors of
  *   tra_forward_host.  Tensors are dense, contiguous
- *   and row-major in the shapes given below; there are no stride arguments.
+ *   and row-major in the shapes given below; there are no stride arguments but
+ *   those of qk_norm_rope and nsa_cache4_append.
  *   q, k, v and out start on a 16-byte boundary.
  * - The library never synchronises: work is enqueued on `stream` (0 = legacy
  *   default stream) and the call returns after the launch.  It allocates no
