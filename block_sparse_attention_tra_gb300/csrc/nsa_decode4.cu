@@ -65,7 +65,11 @@ struct Dec4 {
   // Blocks of a SM at most.  D = 128: 64 of a thread's registers are accumulators.  Of 128 each, sixteen warps fit (128
   // sequences of 4 kv heads on 16 pages of 64: 27.5 us, twelve warps of 160 registers 28.4); the kernel over every page,
   // with a range's state beside them, is faster with twelve (four sequences of up to 131072 tokens 29.5 us and 34.2).
-  static constexpr int SELECT_CTAS = 4, STREAM_CTAS = D == 128 ? 3 : 4;
+  
+#ifndef V_CTAS
+#define V_CTAS 3
+#endif
+  static constexpr int SELECT_CTAS = 4, STREAM_CTAS = D == 128 ? V_CTAS : 4;
   static constexpr int RING = (D == 128 ? 64 : 128) / C;  // chunks of a warp in flight or in use
   static constexpr int RB = D / 2, SB = D / 16;  // bytes of a token's codes, of its scales
   static constexpr int V_OFF = C * RB, KS_OFF = 2 * C * RB, VS_OFF = KS_OFF + C * SB;
@@ -74,7 +78,7 @@ struct Dec4 {
   // the ring, and over it (a range's chunks are done with then) the merge area
   static constexpr int MERGE = WARPS * ROWS * CST * 4;
   static constexpr int Q_OFF = WARPS * RING * SLOT > MERGE ? WARPS * RING * SLOT : MERGE;
-  static constexpr int BYTES = Q_OFF + D / 16 * 512;  // query fragments: a uint4 a lane for each 16 dims
+  static constexpr int BYTES = Q_OFF + D / 16 * 512 + ROWS * 4;  // query fragments (a uint4 a lane for each 16 dims), factors
   static_assert(SLOT % 16 == 0 && (C * SB) % 16 == 0 && C * SB <= 256, "16-byte copies");
 };
 
@@ -124,6 +128,24 @@ __device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t (&w)[(N + 
     w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
     w[0] = N == 2 ? *reinterpret_cast<const uint16_t*>(p) : *p;
+  }
+}
+
+// N words of device memory, in pieces of up to 16 bytes.
+template <int N>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[N]) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = x.x;
+      w[4 * i + 1] = x.y;
+      w[4 * i + 2] = x.z;
+      w[4 * i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
   }
 }
 
@@ -224,6 +246,15 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
   const int len = tokens_of(a, b);
   const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
 
+  // The query rows, eight threads each, asked for before anything else.
+  constexpr int PAIRS = D / 16;  // of a thread
+  uint32_t qw[PAIRS];
+#pragma unroll
+  for (int i = 0; i < PAIRS; ++i) qw[i] = 0u;
+  if (static_cast<int>(threadIdx.x >> 3) < a.G)
+    load_words<PAIRS>(a.q + (qrow + (threadIdx.x >> 3)) * D + (threadIdx.x & 7) * (D / 8), qw);
+  const float factor = a.scale_log2 * (a.k_factor != nullptr ? a.k_factor[h] : 1.0f);
+
   Feed<D, C, SELECT> feed{a, lists[warp]};
   feed.h = h;
   feed.len = len;
@@ -249,53 +280,41 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
     feed.end = (p1 - p0 + C - 1) / C;
   }
   __syncwarp();
+  // Query fragments, in the order of the keys' codes, each row under its own power of two.  (Loaded behind the first
+  // chunks they came 5500 cycles later: after every SM's first copies.)
+  uint8_t* q_frag = smem + L::Q_OFF;
+  {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i)
+      m = fmaxf(m, fmaxf(fabsf(__uint_as_float(qw[i] << 16)), fabsf(__uint_as_float(qw[i] & 0xffff0000u))));
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    // 2^e with the row's maximum in [2^14, 2^15) (1 for zero rows and infinities)
+    const int ex = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+    const int e = ex >= -100 && ex < 128 ? 14 - ex : 0;
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if ((threadIdx.x & 7) == 0)
+      reinterpret_cast<float*>(q_frag + KS * 512)[threadIdx.x >> 3] =
+          factor * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      // lane (row % 8, part / 2) of k-step (4 dims of a lane's D/4 each), rows g and g + 8, dims 0, 1 and 2, 3 of the four
+      const int qr = threadIdx.x >> 3, part = threadIdx.x & 7, at = (part & 1) * (D / 8) + 2 * i;
+      *reinterpret_cast<uint32_t*>(q_frag + at / 4 * 512 + (4 * (qr & 7) + (part >> 1)) * 16 + (at >> 1 & 1) * 8 +
+                                   (qr >> 3) * 4) =
+          pack_f16x2(__uint_as_float(qw[i] << 16) * up, __uint_as_float(qw[i] & 0xffff0000u) * up);
+    }
+  }
   const uint8_t* ring = smem + warp * RING * L::SLOT;
   int ahead[RING - 1];  // first tokens of those on their way, the next first
 #pragma unroll
   for (int i = 0; i < RING - 1; ++i) ahead[i] = feed.put(i);
 
-  // query fragments, in the order of the keys' codes; each row under its own power of two.  The warps share them, and
-  // write a share each.
-  uint8_t* q_frag = smem + L::Q_OFF + lane * 16;
-  float f0, f1;  // score factors of rows g and g + 8
-  {
-    uint2 w[2][KS];
-    float m[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = g + 8 * r;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        w[r][ks] = make_uint2(0u, 0u);
-        if (row < a.G) w[r][ks] = *reinterpret_cast<const uint2*>(a.q + (qrow + row) * D + t * (D / 4) + 4 * ks);
-        m[r] = fmaxf(m[r], fmaxf(fmaxf(fabsf(__uint_as_float(w[r][ks].x << 16)),
-                                       fabsf(__uint_as_float(w[r][ks].x & 0xffff0000u))),
-                                 fmaxf(fabsf(__uint_as_float(w[r][ks].y << 16)),
-                                       fabsf(__uint_as_float(w[r][ks].y & 0xffff0000u)))));
-      }
-      m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 1));
-      m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 2));
-    }
-    const float factor = a.scale_log2 * (a.k_factor != nullptr ? a.k_factor[h] : 1.0f);
-    float up[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      // 2^e with the row's maximum in [2^14, 2^15) (1 for zero rows and infinities)
-      const int ex = static_cast<int>(__float_as_uint(m[r]) >> 23) - 127;
-      const int e = ex >= -100 && ex < 128 ? 14 - ex : 0;
-      up[r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      (r ? f1 : f0) = factor * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    }
-    auto two = [](uint32_t x, float u) {
-      return pack_f16x2(__uint_as_float(x << 16) * u, __uint_as_float(x & 0xffff0000u) * u);
-    };
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-      if (ks % WARPS == warp)
-        *reinterpret_cast<uint4*>(q_frag + ks * 512) = make_uint4(two(w[0][ks].x, up[0]), two(w[1][ks].x, up[1]),
-                                                                  two(w[0][ks].y, up[0]), two(w[1][ks].y, up[1]));
-  }
   __syncthreads();
+  const float f0 = reinterpret_cast<const float*>(q_frag + KS * 512)[g];  // score factors of rows g and g + 8
+  const float f1 = reinterpret_cast<const float*>(q_frag + KS * 512)[g + 8];
+  q_frag += lane * 16;
 
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
   float acc[NT][4];
@@ -352,6 +371,7 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
     }
     const bool tail = tok0 + C > len;
     float mx0 = -INFINITY, mx1 = -INFINITY;
+    // (rounded before the maximum is taken off: a fused form leaves the rounding of scores past 2^24 in the exponent)
 #pragma unroll
     for (int j = 0; j < C / 8; ++j)
 #pragma unroll
@@ -538,6 +558,12 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::SELECT_CTAS)) nsa_decode
   cluster.sync();  // no block leaves while another reads its rows
 }
 
+// range_start in 32 bits where its product is one.
+__device__ __forceinline__ long long range_begin(long long units, int c, int ranges) {
+  return units < (1LL << 21) ? static_cast<uint32_t>(units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ranges)
+                             : range_start(units, c, ranges);
+}
+
 // Every page: a block on one contiguous range of the (sequence, kv head, stage) list; stage k holds tokens 128 k .. of
 // the sequence.
 template <int D, int C>
@@ -550,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::STREAM_CTAS)) nsa_decode
   asm volatile("griddepcontrol.launch_dependents;");
   const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
   const long long units = units_of_warp(a);
-  const long long u0 = range_start(units, blockIdx.x, a.ranges), u1 = range_start(units, blockIdx.x + 1, a.ranges);
+  const long long u0 = range_begin(units, blockIdx.x, a.ranges), u1 = range_begin(units, blockIdx.x + 1, a.ranges);
   if (u0 >= u1) return;
   long long before;
   int b = sequence_of(a, u0, &before);
@@ -630,10 +656,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 16) nsa_decode4_join_kernel(c
       // range is empty: a list shorter than the ranges)
       const int c = base + lane * JOIN_WARPS + warp;
       const bool some = c <= c1;
-      const float* mine = a.ws + (2 * static_cast<size_t>(c) + (some && range_start(units, c, a.ranges) < u0 ? 1 : 0)) *
+      const float* mine = a.ws + (2 * static_cast<size_t>(c) + (some && range_begin(units, c, a.ranges) < u0 ? 1 : 0)) *
                                      part_floats(D);
-      const unsigned live = __ballot_sync(0xffffffffu, some && range_start(units, c, a.ranges) <
-                                                                   range_start(units, c + 1, a.ranges));
+      const unsigned live = __ballot_sync(0xffffffffu, some && range_begin(units, c, a.ranges) <
+                                                                   range_begin(units, c + 1, a.ranges));
       if (base == c0) {
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel is complete
         if (c0 == c1) return;  // written by its only range
