@@ -149,71 +149,70 @@ __device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[N]) {
   }
 }
 
-// A warp's pages in shared memory: SELECT: first token (-1: none) and pool page of each slot; else the pool pages w0 + i.
+// A warp's pages in shared memory: SELECT: first token (-1: none) and (pool page, head) of each slot; else the (pool page,
+// head) of pages w0 + i (-1: none).
 struct PageList {
   int tok[32], id[32];
 };
 
-// The chunks of one warp: its share of a range, page by page, and their way into its ring.  (Kept small: what does not
-// fit into a thread's registers beside the accumulators is read again out of the L2, as the rings leave little L1.)
+// The chunks of one warp: its share of a range, page by page, and their way into its ring.  (Kept small: with sixteen warps
+// a SM, 64 of a thread's 128 registers are accumulators, and as the rings leave little L1, what is spilled goes to the L2.)
 template <int D, int C, bool SELECT>
 struct Feed {
   using L = Dec4<D, C>;
   const Decode4Args& a;
   PageList& list;
-  int h, len, x, end;  // next chunk, chunks of the range
-  int first;           // SELECT: first slot; else first token
-  int w0, id_next;     // else: the list's first page; a page of the list after it
-  const int32_t* row;
-  uint32_t ring;
+  int at, end;      // SELECT: next chunk, chunks of the range; else next token, the range's last
+  int first, len;   // SELECT: first slot; tokens of the sequence
+  int w0, id_next;  // else: the list's first page; a page of the list after it
 
   __device__ __forceinline__ int page_log() const { return 31 - __clz(a.page); }
-  __device__ __forceinline__ int page_id(int p) const {
+  // (pool page, head) of page p, one number of 31 bits, or -1.
+  __device__ __forceinline__ int page_id(int p, int b, int h) const {
     if (p >= pieces_of(len, page_log())) return -1;
-    const int i = row[p];
-    return i < a.num_pages ? i : -1;
+    const int i = a.table[static_cast<size_t>(b) * a.max_pages + p];
+    return i >= 0 && i < a.num_pages ? i * a.Hkv + h : -1;
   }
   // Next chunk into place `place` (a group of copies, empty behind the last): its first token, or -1.
-  __device__ __forceinline__ int put(int place) {
-    const int tok0 = next(place);
+  __device__ __forceinline__ int put(uint32_t ring, int place, const volatile int* bh) {
+    const int tok0 = next(ring + place * L::SLOT, bh);
     copy_commit();
     return tok0;
   }
-  __device__ __forceinline__ int next(int place) {
+  __device__ __forceinline__ int next(uint32_t dst, const volatile int* bh) {
     const int lane = threadIdx.x & 31;
-    while (x < end) {
-      int tok0, page;
+    while (at < end) {
+      int tok0, id;
       if constexpr (SELECT) {
-        const int cpp_log = page_log() - (C == 32 ? 5 : 4), u = first + (x >> cpp_log);
-        const int sub = x & ((1 << cpp_log) - 1);
+        const int cpp_log = page_log() - (C == 32 ? 5 : 4), u = first + (at >> cpp_log);
+        const int sub = at & ((1 << cpp_log) - 1);
         tok0 = list.tok[u];
-        page = list.id[u];
-        x += WARPS;
+        id = list.id[u];
+        at += WARPS;
         if (tok0 < 0) continue;
         tok0 += sub * C;
         if (tok0 >= len) continue;
       } else {
-        tok0 = first + x * C;
-        x += WARPS;
+        tok0 = at;
+        at = end - at > WARPS * C ? at + WARPS * C : end;  // (at most 2^31 - 16)
         const int p = tok0 >> page_log();
         if (p >= w0 + 32) {
-          int id;
+          int now;
           do {
             w0 += 32;
-            id = id_next;
-            id_next = page_id(w0 + 32 + lane);
+            now = id_next;
+            id_next = page_id(w0 + 32 + lane, bh[0], bh[1]);
           } while (p >= w0 + 32);
           __syncwarp();
-          list.id[lane] = id;
+          list.id[lane] = now;
           __syncwarp();
         }
-        page = list.id[p - w0];
-        if (page < 0) continue;
+        id = list.id[p - w0];
+        if (id < 0) continue;
       }
-      debug_check(page >= 0 && page < a.num_pages && tok0 + C <= pieces_of(len, page_log()) << page_log());
-      const size_t at = ((static_cast<size_t>(page) * a.Hkv + h) << page_log()) + (tok0 & (a.page - 1));
-      const uint32_t dst = ring + place * L::SLOT;
-      const uint8_t *k = a.k + at * L::RB + lane * 16, *v = a.v + at * L::RB + lane * 16;
+      debug_check(id >= 0 && id < a.num_pages * a.Hkv && tok0 + C <= pieces_of(len, page_log()) << page_log());
+      const size_t row = (static_cast<size_t>(id) << page_log()) + (tok0 & (a.page - 1));
+      const uint8_t *k = a.k + row * L::RB + lane * 16, *v = a.v + row * L::RB + lane * 16;
 #pragma unroll
       for (int i = 0; i < (C * L::RB + 511) / 512; ++i)
         if (C * L::RB >= 512 || lane * 16 < C * L::RB) {
@@ -222,7 +221,7 @@ struct Feed {
           copy16(dst + L::V_OFF + off, v + i * 512);
         }
       // scales of keys by the first half of the warp, of values by the second
-      const uint8_t* sc = (lane < 16 ? a.k_scale : a.v_scale) + at * L::SB;
+      const uint8_t* sc = (lane < 16 ? a.k_scale : a.v_scale) + row * L::SB;
       if ((lane & 15) * 16 < C * L::SB)
         copy16(dst + (lane < 16 ? L::KS_OFF : L::VS_OFF) + (lane & 15) * 16, sc + (lane & 15) * 16);
       return tok0;
@@ -237,7 +236,7 @@ struct Feed {
 template <int D, int C, bool SELECT>
 __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h, int p0, int p1, uint8_t* smem,
                                              PageList* lists, float (*ml)[ROWS][2], float (&y)[D / 8], float& M,
-                                             float& sum) {
+                                             float& sum, const volatile int* bh) {
   using L = Dec4<D, C>;
   constexpr int NT = D / 8, KS = D / 16, RING = L::RING;
   float(*merge)[ROWS][L::CST] = reinterpret_cast<float(*)[ROWS][L::CST]>(smem);
@@ -256,28 +255,27 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
   const float factor = a.scale_log2 * (a.k_factor != nullptr ? a.k_factor[h] : 1.0f);
 
   Feed<D, C, SELECT> feed{a, lists[warp]};
-  feed.h = h;
   feed.len = len;
-  feed.x = warp;
-  feed.first = p0;
-  feed.ring = smem_u32(smem) + warp * RING * L::SLOT;
-  feed.row = a.table + static_cast<size_t>(b) * a.max_pages;
   if constexpr (SELECT) {
+    const int32_t* pages = a.table + static_cast<size_t>(b) * a.max_pages;
     const SlotRow sel = nsa_live_slots(a.block_idx + (static_cast<size_t>(b) * a.Hkv + h) * a.S, a.S, len - 1,
                                        pieces_of(len, feed.page_log()), a.page);
     int tok = -1, id = 0;
     if (lane >= p0 && lane < p1 && ((sel.live >> lane) & 1u)) {
-      id = feed.row[sel.blk_lane];
+      id = pages[sel.blk_lane];
       if (id >= 0 && id < a.num_pages) tok = sel.blk_lane * a.page;
     }
     lists[warp].tok[lane] = tok;
-    lists[warp].id[lane] = id;
+    lists[warp].id[lane] = tok >= 0 ? id * a.Hkv + h : -1;
+    feed.first = p0;
+    feed.at = warp;
     feed.end = (p1 - p0) << (feed.page_log() - (C == 32 ? 5 : 4));
   } else {
     feed.w0 = p0 >> feed.page_log();
-    lists[warp].id[lane] = feed.page_id(feed.w0 + lane);
-    feed.id_next = feed.page_id(feed.w0 + 32 + lane);
-    feed.end = (p1 - p0 + C - 1) / C;
+    lists[warp].id[lane] = feed.page_id(feed.w0 + lane, b, h);
+    feed.id_next = feed.page_id(feed.w0 + 32 + lane, b, h);
+    feed.end = p1;
+    feed.at = p1 - p0 > warp * C ? p0 + warp * C : p1;
   }
   __syncwarp();
   // Query fragments, in the order of the keys' codes, each row under its own power of two.  (Loaded behind the first
@@ -307,9 +305,10 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
     }
   }
   const uint8_t* ring = smem + warp * RING * L::SLOT;
+  const uint32_t ring32 = smem_u32(ring);
   int ahead[RING - 1];  // first tokens of those on their way, the next first
 #pragma unroll
-  for (int i = 0; i < RING - 1; ++i) ahead[i] = feed.put(i);
+  for (int i = 0; i < RING - 1; ++i) ahead[i] = feed.put(ring32, i, bh);
 
   __syncthreads();
   const float f0 = reinterpret_cast<const float*>(q_frag + KS * 512)[g];  // score factors of rows g and g + 8
@@ -327,7 +326,7 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
 #pragma unroll
     for (int i = 0; i < RING - 2; ++i) ahead[i] = ahead[i + 1];
     __syncwarp();  // every lane is done with the chunk used last, whose place is filled now
-    ahead[RING - 2] = feed.put(place == 0 ? RING - 1 : place - 1);
+    ahead[RING - 2] = feed.put(ring32, place == 0 ? RING - 1 : place - 1, bh);
     copy_wait<RING - 1>();
     __syncwarp();  // and every lane's copies of this one are there
     const uint8_t* src = ring + place * L::SLOT;
@@ -521,7 +520,7 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::SELECT_CTAS)) nsa_decode
   const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
   const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
   float y[D / 8], M, sum;
-  decode_range<D, C, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, lists, ml, y, M, sum);
+  decode_range<D, C, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, lists, ml, y, M, sum, nullptr);
   if (cs == 1) {
     if (row < a.G) store_result<D>(a, qrow + row, d0, y, M, sum);
     return;
@@ -574,7 +573,6 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::STREAM_CTAS)) nsa_decode
   __shared__ float ml[WARPS][ROWS][2];
   // the joining kernel's blocks may take the places that this one's leave (they wait for all of it)
   asm volatile("griddepcontrol.launch_dependents;");
-  const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
   const long long units = units_of_warp(a);
   const long long u0 = range_begin(units, blockIdx.x, a.ranges), u1 = range_begin(units, blockIdx.x + 1, a.ranges);
   if (u0 >= u1) return;
@@ -591,31 +589,52 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::STREAM_CTAS)) nsa_decode
     h = static_cast<int>(in / n_st);
     s0 = static_cast<int>(in % n_st);
   }
-  for (long long u = u0; u < u1;) {
-    const int s1 = static_cast<int>(min(static_cast<long long>(n_st), s0 + (u1 - u)));
+  // What the loop needs behind a range waits in shared memory, not in registers beside the accumulators.
+  __shared__ struct {
+    long long u, u1;
+    int bh[2], n_st, whole, part;
+  } at;
+  for (long long u = u0, last = u1; u < last;) {
+    const int s1 = static_cast<int>(min(static_cast<long long>(n_st), s0 + (last - u)));
     const int end = static_cast<int>(min(static_cast<uint32_t>(s1) << STAGE_LOG, static_cast<uint32_t>(tokens_of(a, b))));
+    if (threadIdx.x == 0) {
+      at.u = u + (s1 - s0);
+      at.u1 = last;
+      at.bh[0] = b;
+      at.bh[1] = h;
+      at.n_st = n_st;
+      at.whole = s0 == 0 && s1 == n_st;
+      at.part = 2 * static_cast<int>(blockIdx.x) + (u != u0 ? 1 : 0);
+    }
+    __syncthreads();
     float y[D / 8], M, sum;
-    decode_range<D, C, false>(a, b, h, s0 << STAGE_LOG, end, smem, lists, ml, y, M, sum);
+    decode_range<D, C, false>(a, b, h, s0 << STAGE_LOG, end, smem, lists, ml, y, M, sum, at.bh);
+    const volatile auto& back = at;
+    b = back.bh[0];
+    h = back.bh[1];
+    const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
     if (row < a.G) {
-      if (s0 == 0 && s1 == n_st) {
+      if (back.whole) {
         store_result<D>(a, static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G + row, d0, y, M, sum);
       } else {  // partial: [m, l] of every row, then the accumulator rows
-        float* part = a.ws + (2 * static_cast<size_t>(blockIdx.x) + (u != u0 ? 1 : 0)) * part_floats(D);
+        float* part = a.ws + static_cast<size_t>(back.part) * part_floats(D);
         if ((threadIdx.x & 7) == 0) *reinterpret_cast<float2*>(part + 2 * row) = make_float2(M, sum);
 #pragma unroll
         for (int e = 0; e < D / 8; e += 2)
           *reinterpret_cast<float2*>(part + 2 * ROWS + row * D + d0 + e) = make_float2(y[e], y[e + 1]);
       }
     }
-    u += s1 - s0;
+    u = back.u;
+    last = back.u1;
+    n_st = back.n_st;
     s0 = 0;
-    if (u < u1) {
+    if (u < last) {
       if (++h == a.Hkv) {
         h = 0;
         do n_st = stages_of(a, ++b);
         while (n_st == 0);
       }
-      __syncthreads();  // the merge area is read before the next copies over it
+      __syncthreads();  // the merge area and what was kept are read before the next copies and range over them
     }
   }
 }
