@@ -21,7 +21,7 @@
 // pages come by cp.async into a ring of its own in shared memory, whose places
 // it alone fills and empties, so that warps wait for nothing but their copies.
 // (By four bulk copies a chunk, codes and scales of keys and values, four
-// sequences of up to 131072 tokens took 34 us in place of 30.)
+// sequences of up to 131072 tokens took a sixth longer.)
 //
 // Selected pages: a block of four warps a (sequence, kv head), or with few of
 // them a cluster that shares out the slots.  Every page: the list of
@@ -31,8 +31,8 @@
 // Long lists run at 69% of what the measured copy rate takes for their bytes (32 sequences of 131072 tokens of 32 query
 // and 2 kv heads of 128: 1209 MB in 268 us, 4.5 TB/s): a chunk of 32 tokens is some 700 instructions of a warp (128
 // conversions, 128 products with scales, 64 matrix products of 8 cycles), and issue slots are 55% busy with eleven warps
-// or with fifteen.  About 7.5 us of every call are the chain at its start (lengths, pages, codes) and the blocks' joins:
-// four sequences of 20011 to 131072 tokens, 87 MB, take 29.5 us and the second launch; one sequence on 16 pages 6.4.
+// or with fifteen.  The rest of a call is the chain at its start (lengths, pages, codes) and the joins: four sequences of
+// 20011 to 131072 tokens, 87 MB, take 27.8 us and 30.6 with the second launch; 128 on 16 pages each 26.0, one 5.5.
 #include <cooperative_groups.h>
 
 #include "codes4.cuh"
@@ -62,14 +62,10 @@ struct Decode4Args {
 
 template <int D, int C>
 struct Dec4 {
-  // Blocks of a SM at most.  D = 128: 64 of a thread's registers are accumulators.  Of 128 each, sixteen warps fit (128
-  // sequences of 4 kv heads on 16 pages of 64: 27.5 us, twelve warps of 160 registers 28.4); the kernel over every page,
-  // with a range's state beside them, is faster with twelve (four sequences of up to 131072 tokens 29.5 us and 34.2).
-  
-#ifndef V_CTAS
-#define V_CTAS 3
-#endif
-  static constexpr int SELECT_CTAS = 4, STREAM_CTAS = D == 128 ? V_CTAS : 4;
+  // Blocks of a SM at most.  D = 128: 64 of a thread's registers are accumulators.  Of 128 each, sixteen warps fit, which
+  // selected pages want for their start (128 sequences of 4 kv heads on 16 pages of 64: 27.5 us, twelve warps of 160
+  // registers 28.4); ranges over every page are faster with twelve (four sequences of up to 131072 tokens: 27.8 and 29.6).
+  static constexpr int SELECT_CTAS = 4, STREAM_CTAS = D == 128 ? 3 : 4;
   static constexpr int RING = (D == 128 ? 64 : 128) / C;  // chunks of a warp in flight or in use
   static constexpr int RB = D / 2, SB = D / 16;  // bytes of a token's codes, of its scales
   static constexpr int V_OFF = C * RB, KS_OFF = 2 * C * RB, VS_OFF = KS_OFF + C * SB;
@@ -563,6 +559,14 @@ __device__ __forceinline__ long long range_begin(long long units, int c, int ran
                              : range_start(units, c, ranges);
 }
 
+// range_of likewise.
+__device__ __forceinline__ int range_at(long long units, long long u, int ranges) {
+  static_assert(DECODE4_MAX_RANGES < 1024, "(u + 1) ranges + units in 32 bits");
+  if (units >= (1LL << 21)) return range_of(units, u, ranges);
+  const uint32_t n = static_cast<uint32_t>(units);
+  return static_cast<int>(((static_cast<uint32_t>(u) + 1) * static_cast<uint32_t>(ranges) + n - 1) / n - 1);
+}
+
 // Every page: a block on one contiguous range of the (sequence, kv head, stage) list; stage k holds tokens 128 k .. of
 // the sequence.
 template <int D, int C>
@@ -639,22 +643,26 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::STREAM_CTAS)) nsa_decode
   }
 }
 
-// Joins the parts of a pair that several ranges cover, and answers for a sequence without tokens.  A block of two warps a
-// row, small enough to lie beside the first kernel's blocks: it works out which parts it joins while they run, and waits
-// for them before it reads one.  Each warp takes every other part, eight on their way at once.
-constexpr int JOIN_WARPS = 2, JOIN_AHEAD = 8;
-template <int D>
-__global__ void __launch_bounds__(JOIN_WARPS * 32, 16) nsa_decode4_join_kernel(const Decode4Args a) {
+// Joins the parts of a pair that several ranges cover, and answers for a sequence without tokens.  A block for R rows of
+// a pair, WARPS_A_ROW warps each: its first warp works out which parts it joins, beside the first kernel's last blocks, and
+// all wait for that kernel before they read one.  Warp w of a row takes the parts c0 + w, c0 + w + WARPS_A_ROW, ...,
+// eight on their way at once.
+constexpr int JOIN_WARPS = 8, JOIN_AHEAD = 8;
+template <int D, int R>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 4) nsa_decode4_join_kernel(const Decode4Args a) {
   constexpr int V = D / 32 > 0 ? D / 32 : 1, LANES = D / V;  // dims of a lane, lanes of a row
-  __shared__ float2 state;
-  __shared__ float half[D];
-  const int b = static_cast<int>(blockIdx.x / a.Hq), hq = static_cast<int>(blockIdx.x % a.Hq);
-  const int h = hq / a.G, row = hq % a.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int np = stages_of(a, b);
-  float M = -INFINITY, sum = 0.0f, o[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) o[e] = 0.0f;
-  if (np > 0) {
+  constexpr int WARPS_A_ROW = JOIN_WARPS / R;
+  __shared__ float2 state[JOIN_WARPS];
+  __shared__ float part_o[JOIN_WARPS][D];
+  __shared__ struct {
+    long long units;
+    int c0, c1, first;  // the pair's ranges; 1 if the first begins before it, and so leaves it second
+  } in;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = (a.G + R - 1) / R, pair = static_cast<int>(blockIdx.x / groups);
+  const int b = pair / a.Hkv, h = pair % a.Hkv, row0 = static_cast<int>(blockIdx.x % groups) * R;
+  const int row = row0 + warp / WARPS_A_ROW, w0 = warp % WARPS_A_ROW;
+  if (warp == 0) {
     // units before the sequence and in all
     long long before = 0, units = 0;
     for (int i = lane; i < a.B; i += 32) {
@@ -668,23 +676,54 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 16) nsa_decode4_join_kernel(c
       before += __shfl_xor_sync(0xffffffffu, before, d);
     }
     units *= a.Hkv;
+    const int np = stages_of(a, b);
     const long long u0 = before * a.Hkv + static_cast<long long>(h) * np, u1 = u0 + np;
-    const int c0 = range_of(units, u0, a.ranges), c1 = range_of(units, u1 - 1, a.ranges);
-    for (int base = c0; base <= c1; base += 32 * JOIN_WARPS) {
-      // this lane's part: the first that its range left if that begins within the pair, else the second (none if the
-      // range is empty: a list shorter than the ranges)
-      const int c = base + lane * JOIN_WARPS + warp;
-      const bool some = c <= c1;
-      const float* mine = a.ws + (2 * static_cast<size_t>(c) + (some && range_begin(units, c, a.ranges) < u0 ? 1 : 0)) *
-                                     part_floats(D);
-      const unsigned live = __ballot_sync(0xffffffffu, some && range_begin(units, c, a.ranges) <
-                                                                   range_begin(units, c + 1, a.ranges));
-      if (base == c0) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel is complete
-        if (c0 == c1) return;  // written by its only range
-      }
+    if (lane == 0) {
+      in.units = units;
+      in.c0 = np > 0 ? range_at(units, u0, a.ranges) : 0;
+      in.c1 = np > 0 ? range_at(units, u1 - 1, a.ranges) : -1;
+      in.first = np > 0 && range_begin(units, in.c0, a.ranges) < u0 ? 1 : 0;
+    }
+  }
+  __syncthreads();
+  const int c0 = in.c0, c1 = in.c1, first = in.first;
+  const long long units = in.units;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel is complete
+  if (c0 == c1) return;                                // written by its only range
+  float M = -INFINITY, sum = 0.0f, o[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) o[e] = 0.0f;
+  if (row < a.G)
+    for (int base = c0; base <= c1; base += 32 * WARPS_A_ROW) {
+      const int c = base + lane * WARPS_A_ROW + w0;
+      const float* mine = a.ws + (2 * static_cast<size_t>(c) + (c == c0 ? first : 0)) * part_floats(D);
+      // (in a list shorter than the ranges some are empty, and leave nothing)
+      const unsigned live = __ballot_sync(
+          0xffffffffu, c <= c1 && (units >= a.ranges || range_begin(units, c, a.ranges) <
+                                                             range_begin(units, c + 1, a.ranges)));
+      float x[JOIN_AHEAD][V];
+      const auto load = [&](int k0) {
+#pragma unroll
+        for (int k = 0; k < JOIN_AHEAD; ++k) {
+          const float* acc = reinterpret_cast<const float*>(__shfl_sync(
+                                 0xffffffffu, reinterpret_cast<unsigned long long>(mine), k0 + k)) +
+                             2 * ROWS + row * D + lane * V;
+          const bool some = (live >> (k0 + k) & 1u) && lane < LANES;
+          if constexpr (V == 4) {
+            const float4 v = some ? *reinterpret_cast<const float4*>(acc) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[k][0] = v.x;
+            x[k][1] = v.y;
+            x[k][2] = v.z;
+            x[k][3] = v.w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[k][e] = some ? acc[e] : 0.0f;
+          }
+        }
+      };
       const float2 ml = (live >> lane & 1u) ? *reinterpret_cast<const float2*>(mine + 2 * row)
                                             : make_float2(-INFINITY, 0.0f);
+      load(0);
       float n = fmaxf(M, ml.x);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
@@ -696,52 +735,55 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 16) nsa_decode4_join_kernel(c
       sum = sum * s + part_sum;
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] *= s;
-      for (int k0 = 0; k0 < 32 && (live >> k0) != 0u; k0 += JOIN_AHEAD) {
-        float x[JOIN_AHEAD][V], wk[JOIN_AHEAD];
+      for (int k0 = 0;;) {
 #pragma unroll
         for (int k = 0; k < JOIN_AHEAD; ++k) {
-          wk[k] = __shfl_sync(0xffffffffu, w, k0 + k);
-          const float* acc = reinterpret_cast<const float*>(__shfl_sync(
-                                 0xffffffffu, reinterpret_cast<unsigned long long>(mine), k0 + k)) +
-                             2 * ROWS + row * D + lane * V;
-          const bool in = (live >> (k0 + k) & 1u) && lane < LANES;
-          if constexpr (V == 4) {
-            const float4 v = in ? *reinterpret_cast<const float4*>(acc) : make_float4(0.f, 0.f, 0.f, 0.f);
-            x[k][0] = v.x;
-            x[k][1] = v.y;
-            x[k][2] = v.z;
-            x[k][3] = v.w;
-          } else {
+          const float wk = __shfl_sync(0xffffffffu, w, k0 + k);  // (0 where there is no part)
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[k][e] = in ? acc[e] : 0.0f;
-          }
-          if (!in) wk[k] = 0.0f;
+          for (int e = 0; e < V; ++e) o[e] = fmaf(wk, x[k][e], o[e]);
         }
-#pragma unroll
-        for (int k = 0; k < JOIN_AHEAD; ++k)
-#pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = fmaf(wk[k], x[k][e], o[e]);
+        k0 += JOIN_AHEAD;
+        if (k0 >= 32 || live >> k0 == 0u) break;
+        load(k0);
       }
     }
-  } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-  }
-  if (warp == 1) {
-    if (lane == 0) state = make_float2(M, sum);
-    if (lane < LANES)
-#pragma unroll
-      for (int e = 0; e < V; ++e) half[lane * V + e] = o[e];
-  }
-  __syncthreads();
-  if (warp == 1) return;
-  const float top = fmaxf(M, state.x), tb = top == -INFINITY ? 0.0f : top, w0 = ex2f(M - tb), w1 = ex2f(state.x - tb);
-  const float total = w0 * sum + w1 * state.y, inv = inverse_sum(total);
+  if (lane == 0) state[warp] = make_float2(M, sum);
   if (lane < LANES)
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      a.out[static_cast<size_t>(blockIdx.x) * D + lane * V + e] =
-          __float2bfloat16_rn((w0 * o[e] + w1 * half[lane * V + e]) * inv);
-  if (a.lse != nullptr && lane == 0) a.lse[blockIdx.x] = lse_of(top, total);
+    for (int e = 0; e < V; ++e) part_o[warp][lane * V + e] = o[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < R * D; i += JOIN_WARPS * 32) {
+    const int r = i / D, d = i % D;
+    if (row0 + r >= a.G) break;
+    const float2* st = state + r * WARPS_A_ROW;
+    float top = -INFINITY, total = 0.0f, y = 0.0f;
+#pragma unroll
+    for (int k = 0; k < WARPS_A_ROW; ++k) top = fmaxf(top, st[k].x);
+    const float tb = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int k = 0; k < WARPS_A_ROW; ++k) {
+      const float wt = ex2f(st[k].x - tb);
+      total += wt * st[k].y;
+      y += wt * part_o[r * WARPS_A_ROW + k][d];
+    }
+    const size_t q = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G + row0 + r;
+    a.out[q * D + d] = __float2bfloat16_rn(y * inverse_sum(total));
+    if (a.lse != nullptr && d == 0) a.lse[q] = lse_of(top, total);
+  }
+}
+
+template <int D, int R>
+int launch_join(const Decode4Args& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.B) * a.Hkv * ((a.G + R - 1) / R)));
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, nsa_decode4_join_kernel<D, R>, a) == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
 template <int D, int C>
@@ -784,16 +826,9 @@ int launch_stream(Decode4Args a, cudaStream_t stream) {
     return ERR_LAUNCH;
   kern<<<static_cast<unsigned>(a.ranges), THREADS, L::BYTES, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.B) * a.Hq));
-  cfg.blockDim = dim3(JOIN_WARPS * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, nsa_decode4_join_kernel<D>, a) == cudaSuccess ? OK : ERR_LAUNCH;
+  // A block a row while all of them fit at once, else four rows a block (four sequences of up to 131072 tokens, 128 rows:
+  // 30.6 us, four rows a block 33.4; 32 of 32768, 1024 rows: 84.1 and 81.3; 512 of 1024, 16384 rows: 103 and 70).
+  return static_cast<long long>(a.B) * a.Hq <= 4LL * sms ? launch_join<D, 1>(a, stream) : launch_join<D, 4>(a, stream);
 }
 
 template <int D>
