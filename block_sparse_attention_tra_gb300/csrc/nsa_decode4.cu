@@ -26,13 +26,14 @@
 // Selected pages: a block of four warps a (sequence, kv head), or with few of
 // them a cluster that shares out the slots.  Every page: the list of
 // (sequence, kv head, 128 tokens) is cut into equal contiguous ranges, one a
-// block; pairs that several ranges cover are joined by a second launch.
+// block, or with few pairs each of these by itself; pairs that several ranges
+// cover are joined by a second launch.
 //
 // Long lists run at 69% of what the measured copy rate takes for their bytes (32 sequences of 131072 tokens of 32 query
 // and 2 kv heads of 128: 1209 MB in 268 us, 4.5 TB/s): a chunk of 32 tokens is some 700 instructions of a warp (128
 // conversions, 128 products with scales, 64 matrix products of 8 cycles), and issue slots are 55% busy with eleven warps
 // or with fifteen.  The rest of a call is the chain at its start (lengths, pages, codes) and the joins: four sequences of
-// 20011 to 131072 tokens, 87 MB, take 27.8 us and 30.6 with the second launch; 128 on 16 pages each 26.0, one 5.5.
+// 20011 to 131072 tokens, 87 MB, take 29.5 us with the second launch, some 3 of them in it; 128 on 16 pages each 26.0, one 5.5.
 #include <cooperative_groups.h>
 
 #include "codes4.cuh"
@@ -56,7 +57,8 @@ struct Decode4Args {
   float* lse;
   float* ws;
   int B, Hq, Hkv, G, page, max_pages, num_pages, S;
-  int ranges;  // blocks of the first kernel over every page
+  int ranges;     // blocks of the first kernel over every page
+  bool pairwise;  // ranges within a (sequence, kv head)
   float scale_log2;
 };
 
@@ -567,8 +569,38 @@ __device__ __forceinline__ int range_at(long long units, long long u, int ranges
   return static_cast<int>(((static_cast<uint32_t>(u) + 1) * static_cast<uint32_t>(ranges) + n - 1) / n - 1);
 }
 
-// Every page: a block on one contiguous range of the (sequence, kv head, stage) list; stage k holds tokens 128 k .. of
-// the sequence.
+// What a block of whole pairs' ranges takes: ranges of its pair, and the first of these ranges.  A pair of n of all stages
+// has 1 + n (ranges - pairs) / stages of them, at most n.  One warp, lane i's sequence being i (B <= 32).
+struct PairRanges {
+  int tokens, n_st, count, before;  // of sequence `lane`: its ranges are Hkv times `count`, after `before` others
+};
+__device__ __forceinline__ PairRanges pair_ranges(const Decode4Args& a) {
+  const int lane = threadIdx.x & 31;
+  PairRanges r;
+  r.tokens = lane < a.B ? tokens_of(a, lane) : 0;
+  r.n_st = pieces_of(r.tokens, STAGE_LOG);
+  long long units = r.n_st;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) units += __shfl_xor_sync(0xffffffffu, units, d);
+  units *= a.Hkv;
+  const int spare = a.ranges - a.B * a.Hkv;
+  r.count = 0;
+  if (r.n_st > 0)
+    r.count = min(r.n_st, 1 + (units < (1LL << 21) ? static_cast<int>(static_cast<uint32_t>(r.n_st) * spare /
+                                                                      static_cast<uint32_t>(units))
+                                                   : static_cast<int>(static_cast<long long>(r.n_st) * spare / units)));
+  int n = r.count * a.Hkv;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, n, d);
+    if (lane >= d) n += x;
+  }
+  r.before = n - r.count * a.Hkv;
+  return r;
+}
+
+// Every page: a block on one contiguous range of the (sequence, kv head, stage) list, or of a pair's stages; stage k holds
+// tokens 128 k .. of the sequence.
 template <int D, int C>
 __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::STREAM_CTAS)) nsa_decode4_stream_kernel(const Decode4Args a) {
   using L = Dec4<D, C>;
@@ -577,21 +609,36 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::STREAM_CTAS)) nsa_decode
   __shared__ float ml[WARPS][ROWS][2];
   // the joining kernel's blocks may take the places that this one's leave (they wait for all of it)
   asm volatile("griddepcontrol.launch_dependents;");
-  const long long units = units_of_warp(a);
-  const long long u0 = range_begin(units, blockIdx.x, a.ranges), u1 = range_begin(units, blockIdx.x + 1, a.ranges);
-  if (u0 >= u1) return;
-  long long before;
-  int b = sequence_of(a, u0, &before);
-  int n_st = stages_of(a, b);
-  // (a sequence's units are fewer than 2^31 heads of 2^24 stages; nearly always a 32-bit number)
-  const long long in = u0 - before;
-  int h, s0;
-  if (in >> 32 == 0) {
-    h = static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(n_st));
-    s0 = static_cast<int>(static_cast<uint32_t>(in) % static_cast<uint32_t>(n_st));
+  long long u0, u1;
+  int b, h, s0, n_st;
+  if (a.pairwise) {
+    const PairRanges r = pair_ranges(a);
+    const int block = static_cast<int>(blockIdx.x);
+    const unsigned hit = __ballot_sync(0xffffffffu, block < r.before + r.count * a.Hkv);
+    if (hit == 0u) return;
+    b = __ffs(hit) - 1;
+    n_st = __shfl_sync(0xffffffffu, r.n_st, b);
+    const int count = __shfl_sync(0xffffffffu, r.count, b), k = block - __shfl_sync(0xffffffffu, r.before, b);
+    h = k / count;
+    s0 = static_cast<int>(range_begin(n_st, k % count, count));
+    u0 = 0;
+    u1 = range_begin(n_st, k % count + 1, count) - s0;
   } else {
-    h = static_cast<int>(in / n_st);
-    s0 = static_cast<int>(in % n_st);
+    const long long units = units_of_warp(a);
+    u0 = range_begin(units, blockIdx.x, a.ranges), u1 = range_begin(units, blockIdx.x + 1, a.ranges);
+    if (u0 >= u1) return;
+    long long before;
+    b = sequence_of(a, u0, &before);
+    n_st = stages_of(a, b);
+    // (a sequence's units are fewer than 2^31 heads of 2^24 stages; nearly always a 32-bit number)
+    const long long in = u0 - before;
+    if (in >> 32 == 0) {
+      h = static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(n_st));
+      s0 = static_cast<int>(static_cast<uint32_t>(in) % static_cast<uint32_t>(n_st));
+    } else {
+      h = static_cast<int>(in / n_st);
+      s0 = static_cast<int>(in % n_st);
+    }
   }
   // What the loop needs behind a range waits in shared memory, not in registers beside the accumulators.
   __shared__ struct {
@@ -662,7 +709,16 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) nsa_decode4_join_kernel(co
   const int groups = (a.G + R - 1) / R, pair = static_cast<int>(blockIdx.x / groups);
   const int b = pair / a.Hkv, h = pair % a.Hkv, row0 = static_cast<int>(blockIdx.x % groups) * R;
   const int row = row0 + warp / WARPS_A_ROW, w0 = warp % WARPS_A_ROW;
-  if (warp == 0) {
+  if (warp == 0 && a.pairwise) {
+    const PairRanges r = pair_ranges(a);
+    const int count = __shfl_sync(0xffffffffu, r.count, b), before = __shfl_sync(0xffffffffu, r.before, b);
+    if (lane == 0) {
+      in.units = a.ranges;  // (no range is empty)
+      in.c0 = before + h * count;
+      in.c1 = before + (h + 1) * count - 1;
+      in.first = 0;
+    }
+  } else if (warp == 0) {
     // units before the sequence and in all
     long long before = 0, units = 0;
     for (int i = lane; i < a.B; i += 32) {
@@ -821,13 +877,17 @@ int launch_stream(Decode4Args a, cudaStream_t stream) {
   const long long places = static_cast<long long>(sms) * L::STREAM_CTAS;
   const long long most = places < DECODE4_MAX_RANGES ? places : DECODE4_MAX_RANGES;
   a.ranges = static_cast<int>(units < most ? units : most);
+  // Ranges of one pair each where every pair has ten on average: no block then starts twice, and they differ in length by
+  // less than it costs to (four sequences of up to 131072 tokens 29.5 us, of equal ranges 30.4; 17 of up to 5003 with 3 kv
+  // heads of 64 9.6 and 11.0; 16 of up to 5000 11.6 and 13.1).  With eight a pair, 28 sequences of up to 90000: 113 and 105.
+  a.pairwise = a.B <= 32 && 10LL * a.B * a.Hkv <= a.ranges;
   auto kern = nsa_decode4_stream_kernel<D, C>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
     return ERR_LAUNCH;
   kern<<<static_cast<unsigned>(a.ranges), THREADS, L::BYTES, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ERR_LAUNCH;
   // A block a row while all of them fit at once, else four rows a block (four sequences of up to 131072 tokens, 128 rows:
-  // 30.6 us, four rows a block 33.4; 32 of 32768, 1024 rows: 84.1 and 81.3; 512 of 1024, 16384 rows: 103 and 70).
+  // 30.6 us, of four rows a block 33.4; 32 of 32768, 1024 rows: 84.1 and 81.3; 512 of 1024, 16384 rows: 103 and 70).
   return static_cast<long long>(a.B) * a.Hq <= 4LL * sms ? launch_join<D, 1>(a, stream) : launch_join<D, 4>(a, stream);
 }
 

@@ -459,6 +459,21 @@ def test_decode_ranges_that_end_anywhere(B, H, D, page, longest):
     run_decode(B, 2 * H, H, D, page, [(61 * b * b) % longest for b in range(B)], seed=B)
 
 
+@pytest.mark.parametrize("B,Hkv,longest", [(31, 1, 4000), (32, 1, 4000), (33, 1, 4000), (20, 2, 3000), (22, 2, 3000)])
+@pytest.mark.parametrize("D,page", [(128, 32), (64, 16)])
+def test_decode_few_and_just_too_many_pairs_for_ranges_of_their_own(B, Hkv, longest, D, page):
+    run_decode(B, 3 * Hkv, Hkv, D, page, many(B, page, longest, B), seed=B)
+    run_decode(B, 3 * Hkv, Hkv, D, page, [longest] + [1] * (B - 2) + [0], seed=B)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv", [(4, 16, 1), (150, 5, 1), (90, 14, 2), (70, 15, 1), (170, 4, 1)])
+def test_decode_long_sequences_among_many_short_ones(B, Hq, Hkv):
+    """Many rows to join, of which some have parts from most blocks and most have none."""
+    lens = many(B, 64, 200, B)
+    lens[1], lens[B // 2] = 20011, 9000
+    run_decode(B, Hq, Hkv, 64, 64, lens, seed=B)
+
+
 def test_decode_one_long_sequence_over_every_block():
     run_decode(1, 4, 1, 128, 64, [40001], seed=4)
     run_decode(2, 2, 2, 16, 16, [9000, 3], seed=5)
