@@ -128,6 +128,10 @@ int take_strides(const int64_t* from, int count, const int* heads, int T, int D,
   }
   return BSA_OK;
 }
+// A written tensor's rows are all its own.
+bool repeats_rows(const int64_t (&to)[3], int B, int H, int T) {
+  return (to[0] == 0 && B > 1) || (to[1] == 0 && H > 1) || (to[2] == 0 && T > 1);
+}
 int check_dtypes(int dtype, int weight_dtype) {
   if (dtype != BSA_F32 && dtype != BSA_BF16) return BSA_ERR_DTYPE;
   if (weight_dtype != BSA_F32 && weight_dtype != BSA_BF16) return BSA_ERR_DTYPE;
@@ -567,6 +571,7 @@ int qk_norm_rope_forward(const void* q, const void* k, void* q_out, void* k_out,
   int64_t to[4][3];
   st = take_strides(strides, 4, heads, T, D, dtype == BSA_F32 ? 4 : 2, to);
   if (st != BSA_OK) return st;
+  if (repeats_rows(to[2], B, Hq, T) || repeats_rows(to[3], B, Hkv, T)) return BSA_ERR_SHAPE;
   const void* ptrs[7] = {q, k, q_out, k_out, q_weight, k_weight, inv_freq};
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return BSA_ERR_ALIGN;
@@ -609,6 +614,7 @@ int qk_norm_rope_backward(const void* q, const void* k, const void* dq_out, cons
   int64_t to[6][3];
   st = take_strides(strides, 6, heads, T, D, dtype == BSA_F32 ? 4 : 2, to);
   if (st != BSA_OK) return st;
+  if (repeats_rows(to[4], B, Hq, T) || repeats_rows(to[5], B, Hkv, T)) return BSA_ERR_SHAPE;
   const void* ptrs[9] = {q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, inv_freq};
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return BSA_ERR_ALIGN;
@@ -652,7 +658,8 @@ int nsa_cache4_append(const void* k, const void* v, const void* q, void* q_out, 
   int st = check_dtypes(dtype, weight_dtype);
   if (st == BSA_OK) st = check_cache4(r.cache, Hq);
   if (st != BSA_OK) return st;
-  if (n < 1 || n > (1 << 30) || static_cast<long long>(B) * n > 0x7fffffffLL || static_cast<long long>(B) * Hq * n >= (1LL << 40) / D)
+  if (n < 1 || n > (1 << 30) || static_cast<long long>(B) * n > 0x7fffffffLL ||
+      static_cast<long long>(B) * Hq * n >= (1LL << 40) / D)
     return BSA_ERR_SHAPE;
   st = check_rows(D, rotary_dim, rotary_scale, eps);
   if (st != BSA_OK) return st;

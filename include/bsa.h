@@ -667,8 +667,9 @@ BSA_API int nsa_select_decode(const void* q, const void* k_cache,
  *   strides    : host memory, in elements: batch, head and token stride of q,
  *                k, q_out and k_out (12 numbers), or NULL: all are contiguous.
  *                The elements of a row follow each other.  Strides are multiples
- *                of 16 bytes and not negative (0 repeats rows of an input), so a
- *                fused projection's output is read in place.
+ *                of 16 bytes and not negative (0 repeats rows of an input; rows of
+ *                a result are its own), so a fused projection's output is read in
+ *                place.
  *   B, T, Hq, Hkv >= 1; B * T <= 2^31 - 1; Hq, Hkv <= 65535.
  *   D          : a multiple of 16 from 16 to 128.
  *   rotary_dim : a multiple of 16 from 0 to D.
@@ -693,7 +694,7 @@ BSA_API int nsa_select_decode(const void* q, const void* k_cache,
  *                aligned; overwritten, in use until the work on `stream`
  *                completes (one workspace per concurrent call).
  *
- * Errors: BSA_ERR_NULLPTR, BSA_ERR_SHAPE (sizes, negative strides),
+ * Errors: BSA_ERR_NULLPTR, BSA_ERR_SHAPE (sizes, strides),
  * BSA_ERR_DTYPE, BSA_ERR_UNSUPPORTED (D, rotary_dim, eps, rotary_scale),
  * BSA_ERR_ALIGN, BSA_ERR_SCRATCH_LIMIT, BSA_ERR_DEVICE, BSA_ERR_LAUNCH.
  */

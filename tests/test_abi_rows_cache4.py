@@ -58,6 +58,18 @@ def test_rows_refusals(call, count, names):
         assert call(rotary=0, freq=None) == 6 and call(dtype=0, strides=[4] * count) == 6
 
 
+@pytest.mark.parametrize("call,count,written", [(fwd, 12, 6), (bwd, 18, 12)])
+def test_results_do_not_repeat_rows(call, count, written):
+    """A stride of 0 repeats rows of an input; of a result it would leave several rows in one place."""
+    for i in range(written, count):
+        s = [0] * written + [64] * (count - written)
+        s[i] = 0
+        assert call(strides=s) == 2
+        if no_gpu:
+            axis = i % 3
+            assert call(strides=s, **({"B": 1}, {"Hq": 1, "Hkv": 1}, {"T": 1})[axis]) == 6
+
+
 def test_rows_backward_workspace():
     assert bwd(ws=None) == 1 and bwd(ws=P + 16) == 7 and bwd(dqw=None) == 1 and bwd(dkw=None) == 1
     need = bsa.qk_norm_rope_backward_workspace_size(2, 4, 2, 5, 64)
