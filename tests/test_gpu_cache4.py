@@ -507,6 +507,14 @@ def test_decode_many_selections_with_repeats_and_dead_slots(D, page, S):
     run_decode(B, 4, Hkv, D, page, many(B, page, 8 * page + 5, S), S=S, seed=S, change=odd)
 
 
+@pytest.mark.parametrize("D,page,S", [(128, 64, 32), (64, 16, 9), (16, 128, 17)])
+def test_decode_one_page_in_slots_of_several_blocks(D, page, S):
+    """Few pairs, whose slots are shared out: a page that is listed again, in any block's slots, counts once."""
+    r = np.random.default_rng(S)
+    run_decode(2, 6, 2, D, page, [11 * page + 5, 3 * page], S=S, seed=S,
+               change=lambda idx: torch.from_numpy(r.integers(-1, 6, tuple(idx.shape)).astype(np.int32)).cuda())
+
+
 @pytest.mark.parametrize("B,D,page,S", [(2, 64, 64, 0), (2, 128, 32, 3), (330, 64, 32, 4), (330, 16, 16, 0)])
 def test_decode_garbage_behind_the_end_and_bad_pages(B, D, page, S):
     """NaN scales behind the last token, on unused pages, and pages outside the pool."""
