@@ -6,7 +6,9 @@
 // A code has two significant bits and a scale four, so their product is exact
 // in f16, and no key or value is rounded on the way: a lane turns pairs of
 // codes into f16x2 by one conversion and multiplies them by their scales
-// before the products, mma.sync.m16n8k16 over 16 query rows as there.
+// before the products, mma.sync.m16n8k16 over 16 query rows as there, or over
+// 16 tokens (scores) and 16 dims (output) by eight query rows where a kv head
+// has no more: half the products, scores and accumulators.
 //  - scores: D is summed over, so its order is free: lane (g, t) takes the D/4
 //    dims of its own quarter of a token's row.
 //  - output: lane (g, t) takes, of four tokens, the D/8 dims that are its
@@ -14,6 +16,9 @@
 //    by side (a shift and a select for four pairs), and a pair's scales are
 //    one f16x2.  The tokens of a slice of 16 are numbered so that the four
 //    that a lane has probabilities of follow each other.
+// The fragments are the same numbers either way; with eight rows a slice's
+// probabilities are transposed (movmatrix) from a lane's row of tokens to its
+// column of them.
 // Query rows, probabilities (f16 over 2^-11 to 2^-15 of the largest so far),
 // sums and joins are those of nsa_decode.cu.
 //
@@ -29,11 +34,14 @@
 // block, or with few pairs each of these by itself; pairs that several ranges
 // cover are joined by a second launch.
 //
-// Long lists run at 69% of what the measured copy rate takes for their bytes (32 sequences of 131072 tokens of 32 query
-// and 2 kv heads of 128: 1209 MB in 268 us, 4.5 TB/s): a chunk of 32 tokens is some 700 instructions of a warp (128
-// conversions, 128 products with scales, 64 matrix products of 8 cycles), and issue slots are 55% busy with eleven warps
-// or with fifteen.  The rest of a call is the chain at its start (lengths, pages, codes) and the joins: four sequences of
-// 20011 to 131072 tokens, 87 MB, take 29.5 us with the second launch, some 3 of them in it; 128 on 16 pages each 26.0, one 5.5.
+// Long lists of 16 query rows run at 67% of what the measured copy rate takes for their bytes (32 sequences of 131072
+// tokens of 32 query and 2 kv heads of 128: 1209 MB in 265 us, 4.6 TB/s), of eight at 77% (16 of 20000 to 60000, 4 kv
+// heads: 70 us).  The copies by themselves, nothing worked out, take the copy rate's time to within 1%, the work by itself
+// 93% of the whole: a chunk of 32 tokens is some 700 instructions of a warp, 128 conversions and 128 products with scales
+// of two cycles and 64 matrix products (eight rows: 32) of eight among them, and three or four warps a scheduler do not
+// fill the gaps of their chains.  (Packed pairs of fp32 for the softmax, 24 instructions fewer, changed nothing.)  The
+// rest of a call is the chain at its start (lengths, pages, codes) and the joins: four sequences of 20011 to 131072
+// tokens, 87 MB, take 29.5 us with the second launch, some 3 of them in it; 128 on 16 pages each 26.0, one 5.5.
 #include <cooperative_groups.h>
 
 #include "codes4.cuh"
@@ -62,11 +70,13 @@ struct Decode4Args {
   float scale_log2;
 };
 
-template <int D, int C>
-struct Dec4 {
+template <int D, int C, bool FEW>
+struct Dec4 {  // FEW: at most eight query rows a kv head
   // Blocks of a SM at most.  D = 128: 64 of a thread's registers are accumulators.  Of 128 each, sixteen warps fit, which
   // selected pages want for their start (128 sequences of 4 kv heads on 16 pages of 64: 27.5 us, twelve warps of 160
   // registers 28.4); ranges over every page are faster with twelve (four sequences of up to 131072 tokens: 27.8 and 29.6).
+  // FEW, 32 accumulators, is no different: twelve 70.3 us, sixteen 72.6 over every page (16 sequences of 4 kv heads), 65.2
+  // and 60.5 on selected ones (512 sequences), twenty 62.5.
   static constexpr int SELECT_CTAS = 4, STREAM_CTAS = D == 128 ? 3 : 4;
   static constexpr int RING = (D == 128 ? 64 : 128) / C;  // chunks of a warp in flight or in use
   static constexpr int RB = D / 2, SB = D / 16;  // bytes of a token's codes, of its scales
@@ -76,7 +86,8 @@ struct Dec4 {
   // the ring, and over it (a range's chunks are done with then) the merge area
   static constexpr int MERGE = WARPS * ROWS * CST * 4;
   static constexpr int Q_OFF = WARPS * RING * SLOT > MERGE ? WARPS * RING * SLOT : MERGE;
-  static constexpr int BYTES = Q_OFF + D / 16 * 512 + ROWS * 4;  // query fragments (a uint4 a lane for each 16 dims), factors
+  static constexpr int Q_STEP = FEW ? 256 : 512;                 // query fragments of 16 dims: two or four words a lane
+  static constexpr int BYTES = Q_OFF + D / 16 * Q_STEP + ROWS * 4;  // and the rows' factors
   static_assert(SLOT % 16 == 0 && (C * SB) % 16 == 0 && C * SB <= 256, "16-byte copies");
 };
 
@@ -106,6 +117,12 @@ __device__ __forceinline__ uint32_t f16_of_scales(uint32_t w) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// A matrix of 8 x 8 f16, two neighbours of row lane / 4 a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 // N bytes of shared memory in 32-bit words (fewer than four: the low ones of one).  (Plain loads: the compiler moves them
@@ -155,9 +172,9 @@ struct PageList {
 
 // The chunks of one warp: its share of a range, page by page, and their way into its ring.  (Kept small: with sixteen warps
 // a SM, 64 of a thread's 128 registers are accumulators, and as the rings leave little L1, what is spilled goes to the L2.)
-template <int D, int C, bool SELECT>
+template <int D, int C, bool FEW, bool SELECT>
 struct Feed {
-  using L = Dec4<D, C>;
+  using L = Dec4<D, C, FEW>;
   const Decode4Args& a;
   PageList& list;
   int at, end;      // SELECT: next chunk, chunks of the range; else next token, the range's last
@@ -231,11 +248,11 @@ struct Feed {
 // Slots [p0, p1) of (b, h)'s selection, or tokens [p0, p1) of the sequence: the block's 128 threads leave the range's
 // unnormalised accumulator, weighted into one, in y (row threadIdx.x / 8, dims (threadIdx.x % 8) D/8 ..), its maximum
 // (log2 domain) in M and its sum of exponentials in sum.
-template <int D, int C, bool SELECT>
+template <int D, int C, bool FEW, bool SELECT>
 __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h, int p0, int p1, uint8_t* smem,
                                              PageList* lists, float (*ml)[ROWS][2], float (&y)[D / 8], float& M,
                                              float& sum, const volatile int* bh) {
-  using L = Dec4<D, C>;
+  using L = Dec4<D, C, FEW>;
   constexpr int NT = D / 8, KS = D / 16, RING = L::RING;
   float(*merge)[ROWS][L::CST] = reinterpret_cast<float(*)[ROWS][L::CST]>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -252,7 +269,7 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
     load_words<PAIRS>(a.q + (qrow + (threadIdx.x >> 3)) * D + (threadIdx.x & 7) * (D / 8), qw);
   const float factor = a.scale_log2 * (a.k_factor != nullptr ? a.k_factor[h] : 1.0f);
 
-  Feed<D, C, SELECT> feed{a, lists[warp]};
+  Feed<D, C, FEW, SELECT> feed{a, lists[warp]};
   feed.len = len;
   if constexpr (SELECT) {
     const int32_t* pages = a.table + static_cast<size_t>(b) * a.max_pages;
@@ -291,15 +308,19 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
     const int e = ex >= -100 && ex < 128 ? 14 - ex : 0;
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     if ((threadIdx.x & 7) == 0)
-      reinterpret_cast<float*>(q_frag + KS * 512)[threadIdx.x >> 3] =
+      reinterpret_cast<float*>(q_frag + KS * L::Q_STEP)[threadIdx.x >> 3] =
           factor * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
       // lane (row % 8, part / 2) of k-step (4 dims of a lane's D/4 each), rows g and g + 8, dims 0, 1 and 2, 3 of the four
       const int qr = threadIdx.x >> 3, part = threadIdx.x & 7, at = (part & 1) * (D / 8) + 2 * i;
-      *reinterpret_cast<uint32_t*>(q_frag + at / 4 * 512 + (4 * (qr & 7) + (part >> 1)) * 16 + (at >> 1 & 1) * 8 +
-                                   (qr >> 3) * 4) =
-          pack_f16x2(__uint_as_float(qw[i] << 16) * up, __uint_as_float(qw[i] & 0xffff0000u) * up);
+      const uint32_t two = pack_f16x2(__uint_as_float(qw[i] << 16) * up, __uint_as_float(qw[i] & 0xffff0000u) * up);
+      uint8_t* of_lane = q_frag + at / 4 * L::Q_STEP + (4 * (qr & 7) + (part >> 1)) * (L::Q_STEP / 32);
+      if constexpr (FEW) {
+        if (qr < 8) *reinterpret_cast<uint32_t*>(of_lane + (at >> 1 & 1) * 4) = two;
+      } else {
+        *reinterpret_cast<uint32_t*>(of_lane + (at >> 1 & 1) * 8 + (qr >> 3) * 4) = two;
+      }
     }
   }
   const uint8_t* ring = smem + warp * RING * L::SLOT;
@@ -309,14 +330,17 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
   for (int i = 0; i < RING - 1; ++i) ahead[i] = feed.put(ring32, i, bh);
 
   __syncthreads();
-  const float f0 = reinterpret_cast<const float*>(q_frag + KS * 512)[g];  // score factors of rows g and g + 8
-  const float f1 = reinterpret_cast<const float*>(q_frag + KS * 512)[g + 8];
-  q_frag += lane * 16;
+  // A lane's two rows: of eight, 2 t and 2 t + 1 (the columns of its scores), else g and g + 8; their score factors
+  const int row0 = FEW ? 2 * t : g, row1 = FEW ? 2 * t + 1 : g + 8;
+  const float f0 = reinterpret_cast<const float*>(q_frag + KS * L::Q_STEP)[row0];
+  const float f1 = reinterpret_cast<const float*>(q_frag + KS * L::Q_STEP)[row1];
+  q_frag += lane * (L::Q_STEP / 32);
 
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-  float acc[NT][4];
+  constexpr int NA = FEW ? NT / 2 : NT;
+  float acc[NA][4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+  for (int j = 0; j < NA; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
 
   int place = 0;
   while (ahead[0] >= 0) {
@@ -330,68 +354,80 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
     const uint8_t* src = ring + place * L::SLOT;
     place = place == RING - 1 ? 0 : place + 1;
     // ---- scores: slices of 16 tokens, two tiles of 8 each; tile j's column n is token 4 (n / 2) + 2 j + n % 2
-    float sc[C / 8][4];
+    constexpr int SC = FEW ? C / 16 : C / 8;
+    float sc[SC][4];
 #pragma unroll
-    for (int jj = 0; jj < C / 8; jj += 2) {
-      uint32_t kw[2][(D / 8 + 3) / 4], ks2[2][D == 128 ? 2 : 1];
+    for (int j = 0; j < SC; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
+    uint32_t kw[C / 8][(D / 8 + 3) / 4], ks2[C / 8][D == 128 ? 2 : 1];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int tk = 8 * jj + 4 * (g >> 1) + 2 * j + (g & 1);
-        load_bytes<D / 8>(src + place_of<D>(tk * L::RB + t * (D / 8)), kw[j]);
-        const uint8_t* sp = src + L::KS_OFF + tk * L::SB + t * (D / 4) / 16;
-        if constexpr (D == 128) {
-          const uint32_t s = *reinterpret_cast<const uint16_t*>(sp);
-          ks2[j][0] = f16_of_scales(__byte_perm(s, 0u, 0x4400));
-          ks2[j][1] = f16_of_scales(__byte_perm(s, 0u, 0x4411));
-        } else {
-          ks2[j][0] = f16_of_scales(*sp * 0x101u);
-        }
-        sc[jj + j][0] = sc[jj + j][1] = sc[jj + j][2] = sc[jj + j][3] = 0.0f;
+    for (int j = 0; j < C / 8; ++j) {
+      const int tk = 16 * (j >> 1) + 4 * (g >> 1) + 2 * (j & 1) + (g & 1);
+      load_bytes<D / 8>(src + place_of<D>(tk * L::RB + t * (D / 8)), kw[j]);
+      const uint8_t* sp = src + L::KS_OFF + tk * L::SB + t * (D / 4) / 16;
+      if constexpr (D == 128) {
+        const uint32_t s = *reinterpret_cast<const uint16_t*>(sp);
+        ks2[j][0] = f16_of_scales(__byte_perm(s, 0u, 0x4400));
+        ks2[j][1] = f16_of_scales(__byte_perm(s, 0u, 0x4411));
+      } else {
+        ks2[j][0] = f16_of_scales(*sp * 0x101u);
       }
+    }
 #pragma unroll
-      for (int k = 0; k < (KS + 1) / 2; ++k) {  // a word of the row: two k-steps (D = 16: half a word, one)
+    for (int k = 0; k < (KS + 1) / 2; ++k) {  // a word of the row: two k-steps (D = 16: half a word, one)
+      uint32_t q[2][L::Q_STEP / 128];
+#pragma unroll
+      for (int i = 0; i < 2 && 2 * k + i < KS; ++i) load_bytes<L::Q_STEP / 32>(q_frag + (2 * k + i) * L::Q_STEP, q[i]);
+#pragma unroll
+      for (int j = 0; j < C / 8; j += 2) {
         uint32_t x[2][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          f16_of_codes(kw[j][k], x[j]);
+        for (int e = 0; e < 2; ++e) {
+          f16_of_codes(kw[j + e][k], x[e]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[j][i] = mul_f16x2(x[j][i], ks2[j][D == 128 ? k / 2 : 0]);
+          for (int i = 0; i < 4; ++i) x[e][i] = mul_f16x2(x[e][i], ks2[j + e][D == 128 ? k / 2 : 0]);
         }
 #pragma unroll
         for (int i = 0; i < 2 && 2 * k + i < KS; ++i) {
-          uint32_t q[4];
-          load_bytes<16>(q_frag + (2 * k + i) * 512, q);
+          if constexpr (FEW) {  // tokens as rows, query rows as columns
+            const uint32_t keys[4] = {x[0][2 * i], x[1][2 * i], x[0][2 * i + 1], x[1][2 * i + 1]};
+            mma_f16(sc[j / 2], keys, q[i][0], q[i][1]);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) mma_f16(sc[jj + j], q, x[j][2 * i], x[j][2 * i + 1]);
+            for (int e = 0; e < 2; ++e) mma_f16(sc[j + e], q[i], x[e][2 * i], x[e][2 * i + 1]);
+          }
         }
       }
     }
     const bool tail = tok0 + C > len;
+    // score e of sc[j]: of the lane's row `second(e)`, at token `token(j, e)` of the chunk
+    const auto second = [](int e) { return FEW ? e & 1 : e >> 1; };
+    const auto token = [&](int j, int e) {
+      return FEW ? 16 * j + 4 * (g >> 1) + (g & 1) + (e & 2) : 16 * (j >> 1) + 4 * t + 2 * (j & 1) + (e & 1);
+    };
     float mx0 = -INFINITY, mx1 = -INFINITY;
     // (rounded before the maximum is taken off: a fused form leaves the rounding of scores past 2^24 in the exponent)
 #pragma unroll
-    for (int j = 0; j < C / 8; ++j)
+    for (int j = 0; j < SC; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sc[j][e] *= f0;
-        sc[j][2 + e] *= f1;
-      }
+      for (int e = 0; e < 4; ++e) sc[j][e] *= second(e) ? f1 : f0;
     if (tail) {
 #pragma unroll
-      for (int j = 0; j < C / 8; ++j)
+      for (int j = 0; j < SC; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (tok0 + 16 * (j >> 1) + 4 * t + 2 * (j & 1) + e >= len) sc[j][e] = sc[j][2 + e] = -INFINITY;
+        for (int e = 0; e < 4; ++e)
+          if (tok0 + token(j, e) >= len) sc[j][e] = -INFINITY;
     }
 #pragma unroll
-    for (int j = 0; j < C / 8; ++j) {
-      mx0 = fmaxf(mx0, fmaxf(sc[j][0], sc[j][1]));
-      mx1 = fmaxf(mx1, fmaxf(sc[j][2], sc[j][3]));
+    for (int j = 0; j < SC; ++j) {
+      mx0 = fmaxf(mx0, fmaxf(sc[j][0], sc[j][FEW ? 2 : 1]));
+      mx1 = fmaxf(mx1, fmaxf(sc[j][FEW ? 1 : 2], sc[j][3]));
     }
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+    // over the lanes that hold scores of the same rows
+#pragma unroll
+    for (int d = FEW ? 4 : 1; d < (FEW ? 32 : 4); d *= 2) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+    }
     // lazy rescale: the reference moves only when a probability would exceed 2^15
     if (__any_sync(0xffffffffu, mx0 - m0 > P_MAX || mx1 - m1 > P_MAX)) {
       const float n0 = fmaxf(m0, reference_of(mx0)), n1 = fmaxf(m1, reference_of(mx1));
@@ -402,25 +438,32 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
       l0 *= s0;
       l1 *= s1;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        acc[j][0] *= s0;
-        acc[j][1] *= s0;
-        acc[j][2] *= s1;
-        acc[j][3] *= s1;
-      }
+      for (int j = 0; j < NA; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] *= second(e) ? s1 : s0;
     }
     const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
 #pragma unroll
     for (int s = 0; s < C / 16; ++s) {
       uint32_t pa[4];
+      if constexpr (FEW) {
+        const float y0 = ex2f(sc[s][0] - b0), y1 = ex2f(sc[s][1] - b1);
+        const float y2 = ex2f(sc[s][2] - b0), y3 = ex2f(sc[s][3] - b1);
+        l0 += y0 + y2;
+        l1 += y1 + y3;
+        // from a lane's row of tokens to its column of them
+        pa[0] = transpose8(pack_f16x2(y0, y1));
+        pa[1] = transpose8(pack_f16x2(y2, y3));
+      } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float y0 = ex2f(sc[2 * s + j][0] - b0), y1 = ex2f(sc[2 * s + j][1] - b0);
-        const float y2 = ex2f(sc[2 * s + j][2] - b1), y3 = ex2f(sc[2 * s + j][3] - b1);
-        l0 += y0 + y1;
-        l1 += y2 + y3;
-        pa[2 * j] = pack_f16x2(y0, y1);
-        pa[2 * j + 1] = pack_f16x2(y2, y3);
+        for (int j = 0; j < 2; ++j) {
+          const float y0 = ex2f(sc[2 * s + j][0] - b0), y1 = ex2f(sc[2 * s + j][1] - b0);
+          const float y2 = ex2f(sc[2 * s + j][2] - b1), y3 = ex2f(sc[2 * s + j][3] - b1);
+          l0 += y0 + y1;
+          l1 += y2 + y3;
+          pa[2 * j] = pack_f16x2(y0, y1);
+          pa[2 * j + 1] = pack_f16x2(y2, y3);
+        }
       }
       // ---- acc += P V of tokens 4t .. 4t + 3 of the slice
       uint32_t vw[4][(D / 16 + 3) / 4], vs[4];
@@ -437,38 +480,60 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
       }
       const uint32_t s01 = f16_of_scales(vs[0] | vs[1] << 8), s23 = f16_of_scales(vs[2] | vs[3] << 8);
 #pragma unroll
-      for (int w = 0; w < (D / 16 + 3) / 4; ++w)
+      for (int w = 0; w < (D / 16 + 3) / 4; ++w) {
+        uint32_t x01[2][4], x23[2][4];
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {  // even and odd nibbles of tokens 0 and 1, 2 and 3 side by side
           constexpr uint32_t LOW = 0x0f0f0f0fu;
-          uint32_t x01[4], x23[4];
-          f16_of_codes(odd ? (vw[0][w] >> 4 & LOW) | (vw[1][w] & ~LOW) : (vw[0][w] & LOW) | (vw[1][w] << 4 & ~LOW), x01);
-          f16_of_codes(odd ? (vw[2][w] >> 4 & LOW) | (vw[3][w] & ~LOW) : (vw[2][w] & LOW) | (vw[3][w] << 4 & ~LOW), x23);
+          f16_of_codes(odd ? (vw[0][w] >> 4 & LOW) | (vw[1][w] & ~LOW) : (vw[0][w] & LOW) | (vw[1][w] << 4 & ~LOW),
+                       x01[odd]);
+          f16_of_codes(odd ? (vw[2][w] >> 4 & LOW) | (vw[3][w] & ~LOW) : (vw[2][w] & LOW) | (vw[3][w] << 4 & ~LOW),
+                       x23[odd]);
+          if constexpr (!FEW) {
 #pragma unroll
-          for (int i = 0; i < 4 && 2 * i + odd < NT; ++i)
-            mma_f16(acc[8 * w + 2 * i + odd], pa, mul_f16x2(x01[i], s01), mul_f16x2(x23[i], s23));
+            for (int i = 0; i < 4 && 2 * i + odd < NT; ++i)
+              mma_f16(acc[8 * w + 2 * i + odd], pa, mul_f16x2(x01[odd][i], s01), mul_f16x2(x23[odd][i], s23));
+          }
         }
+        if constexpr (FEW) {  // dims as rows, query rows as columns
+#pragma unroll
+          for (int i = 0; i < 4 && 2 * i < NT; ++i) {
+            const uint32_t values[4] = {mul_f16x2(x01[0][i], s01), mul_f16x2(x01[1][i], s01),
+                                        mul_f16x2(x23[0][i], s23), mul_f16x2(x23[1][i], s23)};
+            mma_f16(acc[4 * w + i], values, pa[0], pa[1]);
+          }
+        }
+      }
     }
   }
   copy_wait<0>();
 
   // ---- the warps' states into one (over the ring: every warp is done with its chunks)
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-  __syncthreads();
-  // column n = 2t, 2t + 1 of tile j, which is dim n D/8 + j, at place 8 j + n: no bank conflicts here or below
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    *reinterpret_cast<float2*>(&merge[warp][g][8 * j + 2 * t]) = make_float2(acc[j][0], acc[j][1]);
-    *reinterpret_cast<float2*>(&merge[warp][g + 8][8 * j + 2 * t]) = make_float2(acc[j][2], acc[j][3]);
+  for (int d = FEW ? 4 : 1; d < (FEW ? 32 : 4); d *= 2) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, d);
   }
-  if (t == 0) {
-    ml[warp][g][0] = m0;
-    ml[warp][g][1] = l0 * P_UNIT;
-    ml[warp][g + 8][0] = m1;
-    ml[warp][g + 8][1] = l1 * P_UNIT;
+  __syncthreads();
+  // dim n D/8 + j at place 8 j + n: no bank conflicts (few rows: two lanes a bank) here or below
+  if constexpr (FEW) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      merge[warp][row0][8 * j + g] = acc[j / 2][2 * (j & 1)];
+      merge[warp][row1][8 * j + g] = acc[j / 2][2 * (j & 1) + 1];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      *reinterpret_cast<float2*>(&merge[warp][row0][8 * j + 2 * t]) = make_float2(acc[j][0], acc[j][1]);
+      *reinterpret_cast<float2*>(&merge[warp][row1][8 * j + 2 * t]) = make_float2(acc[j][2], acc[j][3]);
+    }
+  }
+  if ((FEW ? g : t) == 0) {
+    ml[warp][row0][0] = m0;
+    ml[warp][row0][1] = l0 * P_UNIT;
+    ml[warp][row1][0] = m1;
+    ml[warp][row1][1] = l1 * P_UNIT;
   }
   __syncthreads();
   const int row = threadIdx.x >> 3;
@@ -505,9 +570,10 @@ __device__ __forceinline__ void store_result(const Decode4Args& a, size_t row, i
 }
 
 // Selected pages: a cluster for each (sequence, kv head), its slots shared out over the cluster's blocks.
-template <int D, int C>
-__global__ void __launch_bounds__(THREADS, (Dec4<D, C>::SELECT_CTAS)) nsa_decode4_select_kernel(const Decode4Args a) {
-  using L = Dec4<D, C>;
+template <int D, int C, bool FEW>
+__global__ void __launch_bounds__(THREADS, (Dec4<D, C, FEW>::SELECT_CTAS))
+    nsa_decode4_select_kernel(const Decode4Args a) {
+  using L = Dec4<D, C, FEW>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PageList lists[WARPS];
   __shared__ float ml[WARPS][ROWS][2];
@@ -518,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::SELECT_CTAS)) nsa_decode
   const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
   const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
   float y[D / 8], M, sum;
-  decode_range<D, C, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, lists, ml, y, M, sum, nullptr);
+  decode_range<D, C, FEW, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, lists, ml, y, M, sum, nullptr);
   if (cs == 1) {
     if (row < a.G) store_result<D>(a, qrow + row, d0, y, M, sum);
     return;
@@ -601,9 +667,10 @@ __device__ __forceinline__ PairRanges pair_ranges(const Decode4Args& a) {
 
 // Every page: a block on one contiguous range of the (sequence, kv head, stage) list, or of a pair's stages; stage k holds
 // tokens 128 k .. of the sequence.
-template <int D, int C>
-__global__ void __launch_bounds__(THREADS, (Dec4<D, C>::STREAM_CTAS)) nsa_decode4_stream_kernel(const Decode4Args a) {
-  using L = Dec4<D, C>;
+template <int D, int C, bool FEW>
+__global__ void __launch_bounds__(THREADS, (Dec4<D, C, FEW>::STREAM_CTAS))
+    nsa_decode4_stream_kernel(const Decode4Args a) {
+  using L = Dec4<D, C, FEW>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PageList lists[WARPS];
   __shared__ float ml[WARPS][ROWS][2];
@@ -659,7 +726,7 @@ __global__ void __launch_bounds__(THREADS, (Dec4<D, C>::STREAM_CTAS)) nsa_decode
     }
     __syncthreads();
     float y[D / 8], M, sum;
-    decode_range<D, C, false>(a, b, h, s0 << STAGE_LOG, end, smem, lists, ml, y, M, sum, at.bh);
+    decode_range<D, C, FEW, false>(a, b, h, s0 << STAGE_LOG, end, smem, lists, ml, y, M, sum, at.bh);
     const volatile auto& back = at;
     b = back.bh[0];
     h = back.bh[1];
@@ -842,15 +909,15 @@ int launch_join(const Decode4Args& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, nsa_decode4_join_kernel<D, R>, a) == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
-template <int D, int C>
+template <int D, int C, bool FEW>
 int launch_select(const Decode4Args& a, cudaStream_t stream) {
-  using L = Dec4<D, C>;
+  using L = Dec4<D, C, FEW>;
   const long long items = static_cast<long long>(a.B) * a.Hkv;
   // Blocks of a cluster: as many, of whole slots, as leave each a SM.  More do not pay for their start and their join (512
   // pairs: one block a pair 30 us, two 44, four 54).
   int cs = 1;
   while (cs < 8 && 2 * cs <= a.S && 2 * items * cs <= sm_count()) cs *= 2;
-  auto kern = nsa_decode4_select_kernel<D, C>;
+  auto kern = nsa_decode4_select_kernel<D, C, FEW>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
     return ERR_LAUNCH;
   cudaLaunchConfig_t cfg = {};
@@ -867,9 +934,9 @@ int launch_select(const Decode4Args& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
-template <int D, int C>
+template <int D, int C, bool FEW>
 int launch_stream(Decode4Args a, cudaStream_t stream) {
-  using L = Dec4<D, C>;
+  using L = Dec4<D, C, FEW>;
   const int sms = sm_count();
   if (sms < 1) return ERR_DEVICE;
   const long long units = static_cast<long long>(a.B) * a.Hkv *
@@ -881,7 +948,7 @@ int launch_stream(Decode4Args a, cudaStream_t stream) {
   // less than it costs to (four sequences of up to 131072 tokens 29.5 us, of equal ranges 30.4; 17 of up to 5003 with 3 kv
   // heads of 64 9.6 and 11.0; 16 of up to 5000 11.6 and 13.1).  With eight a pair, 28 sequences of up to 90000: 113 and 105.
   a.pairwise = a.B <= 32 && 10LL * a.B * a.Hkv <= a.ranges;
-  auto kern = nsa_decode4_stream_kernel<D, C>;
+  auto kern = nsa_decode4_stream_kernel<D, C, FEW>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
     return ERR_LAUNCH;
   kern<<<static_cast<unsigned>(a.ranges), THREADS, L::BYTES, stream>>>(a);
@@ -891,11 +958,18 @@ int launch_stream(Decode4Args a, cudaStream_t stream) {
   return static_cast<long long>(a.B) * a.Hq <= 4LL * sms ? launch_join<D, 1>(a, stream) : launch_join<D, 4>(a, stream);
 }
 
+template <int D, bool FEW>
+int launch_rows(const Decode4Args& a, cudaStream_t stream) {
+  // chunks of 32 tokens (half the work for masks and maxima per token) where a page holds them
+  if (a.block_idx == nullptr)
+    return a.page >= 32 ? launch_stream<D, 32, FEW>(a, stream) : launch_stream<D, 16, FEW>(a, stream);
+  return a.page >= 32 ? launch_select<D, 32, FEW>(a, stream) : launch_select<D, 16, FEW>(a, stream);
+}
+// Eight query rows a kv head or fewer have products of their own (32 query and 4 kv heads of 128, 16 sequences of 20000 to
+// 60000 tokens: 70 us, by the form for sixteen 88; 512 on 16 pages each: 60.5 and 76.5; heads of 64: 47.7 and 57.9).
 template <int D>
 int launch_decode4(const Decode4Args& a, cudaStream_t stream) {
-  // chunks of 32 tokens (half the work for masks and maxima per token) where a page holds them
-  if (a.block_idx == nullptr) return a.page >= 32 ? launch_stream<D, 32>(a, stream) : launch_stream<D, 16>(a, stream);
-  return a.page >= 32 ? launch_select<D, 32>(a, stream) : launch_select<D, 16>(a, stream);
+  return a.G <= 8 ? launch_rows<D, true>(a, stream) : launch_rows<D, false>(a, stream);
 }
 
 }  // namespace

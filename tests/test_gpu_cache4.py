@@ -433,6 +433,14 @@ def test_decode_group_sizes(Hq, Hkv):
     run_decode(2, Hq, Hkv, 128, 64, [700, 64], S=4, seed=Hq)
 
 
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("S", [0, 5])
+@pytest.mark.parametrize("G", [8, 9, 16])
+def test_decode_groups_of_eight_and_more(D, page, S, G):
+    run_decode(3, 2 * G, 2, D, page, [2, 3 * page + 9, 7 * page - 1], S=S, seed=D + page + G, factors=page < 128)
+
+
 def test_decode_empty_and_full_sequences():
     out, lse = run_decode(6, 4, 2, 64, 16, [0, 16, 1, 0, 15, 17], seed=1)
     assert not out[0].any() and not out[3].any() and (lse[0] == -1.0e9).all()
