@@ -67,7 +67,7 @@ template <class Args>
 __device__ __forceinline__ int tokens_of(const Args& a, int b) {
   return max(0, min(a.lens[b], a.max_pages * a.page));
 }
-__device__ __forceinline__ int pieces_of(int tokens, int size_log) {
+__host__ __device__ __forceinline__ int pieces_of(int tokens, int size_log) {
   return static_cast<int>((static_cast<uint32_t>(tokens) + (1u << size_log) - 1u) >> size_log);
 }
 template <class Args>

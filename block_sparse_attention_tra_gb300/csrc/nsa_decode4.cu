@@ -29,8 +29,9 @@
 // sequences of up to 131072 tokens took a sixth longer.)
 //
 // Selected pages: a block of four warps a (sequence, kv head), or with few of
-// them a cluster that shares out the slots.  Every page: the list of
-// (sequence, kv head, 128 tokens) is cut into equal contiguous ranges, one a
+// them a cluster that shares out the slots; and so, by their stages of 128
+// tokens, every page of short tables.  Else the list of (sequence, kv head,
+// stage) is cut into equal contiguous ranges, one a
 // block, or with few pairs each of these by itself; pairs that several ranges
 // cover are joined by a second launch.
 //
@@ -41,7 +42,8 @@
 // of two cycles and 64 matrix products (eight rows: 32) of eight among them, and three or four warps a scheduler do not
 // fill the gaps of their chains.  (Packed pairs of fp32 for the softmax, 24 instructions fewer, changed nothing.)  The
 // rest of a call is the chain at its start (lengths, pages, codes) and the joins: four sequences of 20011 to 131072
-// tokens, 87 MB, take 29.5 us with the second launch, some 3 of them in it; 128 on 16 pages each 26.0, one 5.5.
+// tokens, 87 MB, take 29.5 us with the second launch, some 3 of them in it; 128 on 16 pages each 26.0, one 5.5,
+// 17 of up to 5003 in one launch 8.7.
 #include <cooperative_groups.h>
 
 #include "codes4.cuh"
@@ -55,6 +57,7 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
+constexpr int PAIR_STAGES = 16;  // of a block in a cluster over every page, at most
 
 struct Decode4Args {
   const __nv_bfloat16* q;
@@ -78,6 +81,7 @@ struct Dec4 {  // FEW: at most eight query rows a kv head
   // FEW, 32 accumulators, is no different: twelve 70.3 us, sixteen 72.6 over every page (16 sequences of 4 kv heads), 65.2
   // and 60.5 on selected ones (512 sequences), twenty 62.5.
   static constexpr int SELECT_CTAS = 4, STREAM_CTAS = D == 128 ? 3 : 4;
+  static constexpr int PAIR_CTAS(bool select) { return select || FEW ? SELECT_CTAS : STREAM_CTAS; }
   static constexpr int RING = (D == 128 ? 64 : 128) / C;  // chunks of a warp in flight or in use
   static constexpr int RB = D / 2, SB = D / 16;  // bytes of a token's codes, of its scales
   static constexpr int V_OFF = C * RB, KS_OFF = 2 * C * RB, VS_OFF = KS_OFF + C * SB;
@@ -569,22 +573,38 @@ __device__ __forceinline__ void store_result(const Decode4Args& a, size_t row, i
   if (a.lse != nullptr && d0 == 0) a.lse[row] = lse_of(M, sum);
 }
 
-// Selected pages: a cluster for each (sequence, kv head), its slots shared out over the cluster's blocks.
-template <int D, int C, bool FEW>
-__global__ void __launch_bounds__(THREADS, (Dec4<D, C, FEW>::SELECT_CTAS))
-    nsa_decode4_select_kernel(const Decode4Args a) {
+// Selected pages (SELECT), or every page of short sequences: a cluster for each (sequence, kv head), whose blocks share out
+// the slots or the stages.
+template <int D, int C, bool FEW, bool SELECT>
+__global__ void __launch_bounds__(THREADS, (Dec4<D, C, FEW>::PAIR_CTAS(SELECT)))
+    nsa_decode4_pair_kernel(const Decode4Args a) {
   using L = Dec4<D, C, FEW>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PageList lists[WARPS];
   __shared__ float ml[WARPS][ROWS][2];
   __shared__ float part_ml[ROWS][2];
+  __shared__ int bh[2];
   const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
   const int cs = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int item = blockIdx.x / cs, b = item / a.Hkv, h = item % a.Hkv;
   const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (D / 8);
   const size_t qrow = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.G;
   float y[D / 8], M, sum;
-  decode_range<D, C, FEW, true>(a, b, h, a.S * rank / cs, a.S * (rank + 1) / cs, smem, lists, ml, y, M, sum, nullptr);
+  int p0 = 0, p1 = 0;
+  if constexpr (SELECT) {
+    p0 = a.S * rank / cs;
+    p1 = a.S * (rank + 1) / cs;
+  } else {
+    if (threadIdx.x == 0) {
+      bh[0] = b;
+      bh[1] = h;
+    }
+    __syncthreads();
+    const int n = tokens_of(a, b), n_st = pieces_of(n, STAGE_LOG);  // (at most 8 * PAIR_STAGES)
+    p0 = min(n_st * rank / cs << STAGE_LOG, n);
+    p1 = min(n_st * (rank + 1) / cs << STAGE_LOG, n);
+  }
+  decode_range<D, C, FEW, SELECT>(a, b, h, p0, p1, smem, lists, ml, y, M, sum, bh);
   if (cs == 1) {
     if (row < a.G) store_result<D>(a, qrow + row, d0, y, M, sum);
     return;
@@ -909,19 +929,14 @@ int launch_join(const Decode4Args& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, nsa_decode4_join_kernel<D, R>, a) == cudaSuccess ? OK : ERR_LAUNCH;
 }
 
-template <int D, int C, bool FEW>
-int launch_select(const Decode4Args& a, cudaStream_t stream) {
+template <int D, int C, bool FEW, bool SELECT>
+int launch_pairs(const Decode4Args& a, int cs, cudaStream_t stream) {
   using L = Dec4<D, C, FEW>;
-  const long long items = static_cast<long long>(a.B) * a.Hkv;
-  // Blocks of a cluster: as many, of whole slots, as leave each a SM.  More do not pay for their start and their join (512
-  // pairs: one block a pair 30 us, two 44, four 54).
-  int cs = 1;
-  while (cs < 8 && 2 * cs <= a.S && 2 * items * cs <= sm_count()) cs *= 2;
-  auto kern = nsa_decode4_select_kernel<D, C, FEW>;
+  auto kern = nsa_decode4_pair_kernel<D, C, FEW, SELECT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
     return ERR_LAUNCH;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items * cs));
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.B) * a.Hkv * cs));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = L::BYTES;
   cfg.stream = stream;
@@ -935,18 +950,34 @@ int launch_select(const Decode4Args& a, cudaStream_t stream) {
 }
 
 template <int D, int C, bool FEW>
+int launch_select(const Decode4Args& a, cudaStream_t stream) {
+  // Blocks of a cluster: as many, of whole slots, as leave each a SM.  More do not pay for their start and their join (512
+  // pairs: one block a pair 30 us, two 44, four 54).
+  int cs = 1;
+  while (cs < 8 && 2 * cs <= a.S && 2LL * a.B * a.Hkv * cs <= sm_count()) cs *= 2;
+  return launch_pairs<D, C, FEW, true>(a, cs, stream);
+}
+
+template <int D, int C, bool FEW>
 int launch_stream(Decode4Args a, cudaStream_t stream) {
   using L = Dec4<D, C, FEW>;
   const int sms = sm_count();
   if (sms < 1) return ERR_DEVICE;
-  const long long units = static_cast<long long>(a.B) * a.Hkv *
-                          ((static_cast<long long>(a.max_pages) * a.page + STAGE_TOK - 1) / STAGE_TOK);
-  const long long places = static_cast<long long>(sms) * L::STREAM_CTAS;
+  const long long pairs = static_cast<long long>(a.B) * a.Hkv, most_st = pieces_of(a.max_pages * a.page, STAGE_LOG);
+  const long long units = pairs * most_st, places = static_cast<long long>(sms) * L::STREAM_CTAS;
   const long long most = places < DECODE4_MAX_RANGES ? places : DECODE4_MAX_RANGES;
   a.ranges = static_cast<int>(units < most ? units : most);
+  // Short tables: a cluster a pair, up to eight blocks that all fit at once, in one launch, while its blocks' longest share
+  // (at most 2048 tokens: nothing evens out what sequences differ by) is up to four stages longer than half of a range of
+  // full sequences.  (Two kv heads of 128: 4 sequences of up to 1000 tokens 5.5 us, by ranges 7.0, of 4000 both 8.0, of
+  // 8000 11.5 and 9.1; 512 of 1000 36.6 and 55.9; 100 with 4 kv heads of 64 of up to 500 6.7 and 14.2.)
+  int cs = 1;
+  while (cs < 8 && cs < most_st && 2 * pairs * cs <= static_cast<long long>(sms) * L::PAIR_CTAS(false)) cs *= 2;
+  if (most_st <= PAIR_STAGES * cs && 2LL * a.ranges * (most_st - 4 * cs) <= units * cs)
+    return launch_pairs<D, C, FEW, false>(a, cs, stream);
   // Ranges of one pair each where every pair has ten on average: no block then starts twice, and they differ in length by
-  // less than it costs to (four sequences of up to 131072 tokens 29.5 us, of equal ranges 30.4; 17 of up to 5003 with 3 kv
-  // heads of 64 9.6 and 11.0; 16 of up to 5000 11.6 and 13.1).  With eight a pair, 28 sequences of up to 90000: 113 and 105.
+  // less than it costs to (four sequences of up to 131072 tokens 29.5 us, of equal ranges 30.4; 16 of 1000 to 5000
+  // 11.6 and 13.1).  With eight a pair, 28 sequences of up to 90000: 113 and 105.
   a.pairwise = a.B <= 32 && 10LL * a.B * a.Hkv <= a.ranges;
   auto kern = nsa_decode4_stream_kernel<D, C, FEW>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)

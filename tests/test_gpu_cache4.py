@@ -406,9 +406,14 @@ def select(B, Hkv, S, lens, page, seed):
     return torch.from_numpy(idx).cuda()
 
 
-def run_decode(B, Hq, Hkv, D, page, lens, S=0, seed=0, pool=None, change=None, factors=False, size=1.0):
+def run_decode(B, Hq, Hkv, D, page, lens, S=0, seed=0, pool=None, change=None, factors=False, size=1.0,
+               room=0):
+    """``room``: tokens for which the table has places behind the longest sequence's, with no pages there."""
     max_pages = max(1, max(-(-x // page) for x in lens))
     pool = pool or Pool(B, Hkv, D, page, max_pages, seed, factors=factors).clean()
+    if room:
+        none = torch.full((B, -(-room // page)), -1, dtype=torch.int32, device="cuda")
+        pool.table = torch.cat((pool.table, none), 1)
     q = (torch.randn((B, Hq, 1, D), generator=torch.Generator().manual_seed(seed)) * size).to(BF).cuda()
     idx = select(B, Hkv, S, lens, page, seed) if S else None
     if change is not None:
@@ -465,6 +470,28 @@ def test_decode_ragged_batches(B):
 def test_decode_ranges_that_end_anywhere(B, H, D, page, longest):
     """Lists of many short pairs (several to a block, empty ones between) and of few long ones (several blocks to one)."""
     run_decode(B, 2 * H, H, D, page, [(61 * b * b) % longest for b in range(B)], seed=B)
+
+
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("G", [3, 8, 9, 16])
+def test_decode_short_sequences_of_long_tables(D, page, G):
+    """Tables that are too long for the form of short ones, whatever the sequences: empty ranges among them."""
+    run_decode(4, 2 * G, 2, D, page, [2, 0, 4 * page + 9, 9 * page - 1], seed=D + page + G, factors=page < 64, room=20000)
+
+
+@pytest.mark.parametrize("B,Hkv", [(2, 2), (33, 1), (130, 1), (300, 2), (600, 1)])
+@pytest.mark.parametrize("room", [0, 1100, 20000])
+def test_decode_batches_of_short_and_long_tables(B, Hkv, room):
+    run_decode(B, 4 * Hkv, Hkv, 32, 16, [(37 * b) % 330 for b in range(B)], seed=B, room=room)
+    run_decode(B, 9 * Hkv, Hkv, 128, 64, many(B, 64, 700, B), seed=B, room=room)
+
+
+@pytest.mark.parametrize("stages", [1, 2, 3, 4, 7, 8, 9, 16, 31, 32, 33, 63, 64, 65])
+def test_decode_tables_around_the_rule_for_short_ones(stages):
+    n = 128 * stages
+    run_decode(2, 8, 2, 64, 64, [n, n - 63], seed=stages)
+    run_decode(40, 16, 1, 128, 128, [n - 1] + [1, 0, 77, 130] * 9 + [n // 2, n, 128], seed=stages)
 
 
 @pytest.mark.parametrize("B,Hkv,longest", [(31, 1, 4000), (32, 1, 4000), (33, 1, 4000), (20, 2, 3000), (22, 2, 3000)])

@@ -33,3 +33,19 @@ def test_cache4_debug_build(debug_lib, B, Hq, Hkv, D, page, S):  # noqa: F811
         return (qr, *codes, *scales, out, lse, *back, *rows, *bsa.qk_norm_rope_backward(q, k, *rows, w, w, freq))
 
     both(debug_lib, run)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,page", [(3, 8, 2, 64, 32), (2, 16, 1, 128, 128), (600, 2, 1, 128, 16), (40, 9, 1, 32, 64)])
+def test_cache4_debug_build_of_long_tables(debug_lib, B, Hq, Hkv, D, page):  # noqa: F811
+    g = torch.Generator().manual_seed(B)
+    pages = 5
+    codes = [torch.randint(0, 256, (B * pages, Hkv, page, D // 2), generator=g, dtype=torch.uint8).cuda() for _ in range(2)]
+    scales = [torch.randint(0x30, 0x40, (B * pages, Hkv, page, D // 16), generator=g, dtype=torch.uint8).cuda()
+              for _ in range(2)]
+    table = torch.full((B, 20000 // page), -1, dtype=torch.int32)
+    table[:, :pages] = torch.randperm(B * pages, generator=g).view(B, pages)
+    table[0, 1] = B * pages + 7  # a page outside the pool
+    held = (torch.arange(B) * 37 % (pages * page + 1)).int().cuda()
+    held[-1] = 19000  # most of it on pages that the table does not have
+    table, q = table.cuda(), torch.randn((B, Hq, 1, D), generator=g).to(torch.bfloat16).cuda()
+    both(debug_lib, lambda: bsa.nsa_cache4_decode(q, *codes, *scales, table, held, return_lse=True))
