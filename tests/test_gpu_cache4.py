@@ -821,3 +821,46 @@ def test_calls_on_parameters_without_autograd_and_in_place_versions():
         call()
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.backward()
+
+
+def test_two_threads_on_streams_of_their_own():
+    """Calls of two host threads at once, each on its own tensors and stream, against the same calls one by one."""
+    import threading
+
+    def work(i):
+        B, Hq, Hkv, D, page = (3, 8, 2, 64, 32) if i else (2, 16, 1, 128, 64)
+        g = torch.Generator(device="cuda").manual_seed(i)
+        x = torch.randn((B, 40, Hq + 2 * Hkv, D), generator=g, device="cuda").to(BF)
+        q, k, v = x.transpose(1, 2).split([Hq, Hkv, Hkv], 1)
+        w, f = weights(D), freqs(D)
+        pool = Pool(B, Hkv, D, page, 30, seed=i).clean()
+        lens = torch.tensor([700, 3, 40][:B], dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        out = []
+        for _ in range(20):
+            q2, k2 = bsa.qk_norm_rope_forward(q, k, w[0], w[1], f)
+            grads = bsa.qk_norm_rope_backward(q, k, q2, k2, w[0], w[1], f)
+            q1 = bsa.nsa_cache4_append(k, v, *pool.args(), lens, inv_freq=f, q=q, q_weight=w[0], k_weight=w[1])
+            out.append((q2, k2, *grads, q1, *bsa.nsa_cache4_read(*pool.args(), lens + 40, 50),
+                        bsa.nsa_cache4_decode(q1[:, :, -1:], *pool.args(), lens + 40)))
+        return out
+
+    want, got, wrong = [work(i) for i in (0, 1)], [None, None], []
+    torch.cuda.synchronize()
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[i] = work(i)
+        except BaseException as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for r, s in zip(a, b) for x, y in zip(r, s))
