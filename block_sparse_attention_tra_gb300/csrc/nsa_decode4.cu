@@ -42,8 +42,8 @@
 // of two cycles and 64 matrix products (eight rows: 32) of eight among them, and three or four warps a scheduler do not
 // fill the gaps of their chains.  (Packed pairs of fp32 for the softmax, 24 instructions fewer, changed nothing.)  The
 // rest of a call is the chain at its start (lengths, pages, codes) and the joins: four sequences of 20011 to 131072
-// tokens, 87 MB, take 29.5 us with the second launch, some 3 of them in it; 128 on 16 pages each 26.0, one 5.5,
-// 17 of up to 5003 in one launch 8.7.
+// tokens, 87 MB, take 29.3 us with the second launch, some 3 of them in it; 128 on 16 pages each 26.0, one 5.5,
+// 17 of up to 5003 in one launch 8.5.
 #include <cooperative_groups.h>
 
 #include "codes4.cuh"
@@ -402,6 +402,18 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
         }
       }
     }
+    // The values' codes and scales, asked for before the scores are looked at (behind the probabilities: 17 sequences of
+    // up to 5003 tokens of 3 heads of 64 8.7 us in place of 8.45, 16 of up to 60000 of 4 heads 47.7 and 46.7).
+    uint32_t vw[C / 16][4][(D / 16 + 3) / 4], vs[C / 16][4];
+#pragma unroll
+    for (int s = 0; s < C / 16; ++s) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tk = 16 * s + 4 * t + i;
+        load_bytes<D / 16>(src + L::V_OFF + place_of<D>(tk * L::RB + g * (D / 16)), vw[s][i]);
+        vs[s][i] = src[L::VS_OFF + tk * L::SB + g * (D / 8) / 16];
+      }
+    }
     const bool tail = tok0 + C > len;
     // score e of sc[j]: of the lane's row `second(e)`, at token `token(j, e)` of the chunk
     const auto second = [](int e) { return FEW ? e & 1 : e >> 1; };
@@ -420,6 +432,11 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (tok0 + token(j, e) >= len) sc[j][e] = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < C / 16; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tok0 + 16 * s + 4 * t + i >= len) vs[s][i] = 0u;  // scales behind the last token may be anything
     }
 #pragma unroll
     for (int j = 0; j < SC; ++j) {
@@ -470,28 +487,17 @@ __device__ __forceinline__ void decode_range(const Decode4Args& a, int b, int h,
         }
       }
       // ---- acc += P V of tokens 4t .. 4t + 3 of the slice
-      uint32_t vw[4][(D / 16 + 3) / 4], vs[4];
-      const int tk = 16 * s + 4 * t;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        load_bytes<D / 16>(src + L::V_OFF + place_of<D>((tk + i) * L::RB + g * (D / 16)), vw[i]);
-        vs[i] = src[L::VS_OFF + (tk + i) * L::SB + g * (D / 8) / 16];
-      }
-      if (tail) {  // scales behind the last token may be anything
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (tok0 + tk + i >= len) vs[i] = 0u;
-      }
-      const uint32_t s01 = f16_of_scales(vs[0] | vs[1] << 8), s23 = f16_of_scales(vs[2] | vs[3] << 8);
+      const auto& of = vw[s];
+      const uint32_t s01 = f16_of_scales(vs[s][0] | vs[s][1] << 8), s23 = f16_of_scales(vs[s][2] | vs[s][3] << 8);
 #pragma unroll
       for (int w = 0; w < (D / 16 + 3) / 4; ++w) {
         uint32_t x01[2][4], x23[2][4];
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {  // even and odd nibbles of tokens 0 and 1, 2 and 3 side by side
           constexpr uint32_t LOW = 0x0f0f0f0fu;
-          f16_of_codes(odd ? (vw[0][w] >> 4 & LOW) | (vw[1][w] & ~LOW) : (vw[0][w] & LOW) | (vw[1][w] << 4 & ~LOW),
+          f16_of_codes(odd ? (of[0][w] >> 4 & LOW) | (of[1][w] & ~LOW) : (of[0][w] & LOW) | (of[1][w] << 4 & ~LOW),
                        x01[odd]);
-          f16_of_codes(odd ? (vw[2][w] >> 4 & LOW) | (vw[3][w] & ~LOW) : (vw[2][w] & LOW) | (vw[3][w] << 4 & ~LOW),
+          f16_of_codes(odd ? (of[2][w] >> 4 & LOW) | (of[3][w] & ~LOW) : (of[2][w] & LOW) | (of[3][w] << 4 & ~LOW),
                        x23[odd]);
           if constexpr (!FEW) {
 #pragma unroll
