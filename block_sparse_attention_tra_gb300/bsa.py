@@ -895,8 +895,8 @@ def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
 
     q ``[B, Hq, 1, D]`` bf16 (rotated), the cache as for ``nsa_cache_append``,
     ``cache_lens [B]`` with the query's own token counted; ``block_idx [B,
-    Hkv, 1, S]`` lists logical pages (a set, -1 = padding), None reads every
-    page.  Returns ``out [B, Hq, 1, D]`` (and ``lse [B, Hq, 1]`` fp32 when
+    Hkv, 1, S]``, S from 1 to 32, lists logical pages (a set, -1 = padding), None
+    reads every page.  Returns ``out [B, Hq, 1, D]`` (and ``lse [B, Hq, 1]`` fp32 when
     ``return_lse``); an empty sequence or selection gives 0 and -1e9.
     ``workspace`` is a uint8 CUDA tensor of at least
     ``nsa_select_decode_workspace_size(...)`` bytes (allocated when None).
@@ -925,9 +925,9 @@ def nsa_select_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
                                                B, Hkv, D)
     S = 0
     if block_idx is not None:
-        S = block_idx.shape[-1]
-        if block_idx.shape != (B, Hkv, 1, S):
-            raise BsaError("block_idx must be [B,Hkv,1,S]", 2)
+        S = block_idx.shape[-1] if block_idx.dim() == 4 else 0
+        if block_idx.shape != (B, Hkv, 1, S) or not 0 < S <= 32:  # (an empty one has no address: none, to the library)
+            raise BsaError("block_idx must be [B,Hkv,1,S] with S from 1 to 32", 2)
     written = []
     if out is not None:
         _in_place(what, "out", out, q.shape, torch.bfloat16)
@@ -1413,9 +1413,9 @@ def nsa_cache4_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
                                                 page_table, cache_lens, B, Hkv, D)
     S = 0
     if block_idx is not None:
-        S = block_idx.shape[-1]
-        if block_idx.shape != (B, Hkv, 1, S):
-            raise BsaError("block_idx must be [B,Hkv,1,S]", 2)
+        S = block_idx.shape[-1] if block_idx.dim() == 4 else 0
+        if block_idx.shape != (B, Hkv, 1, S) or not 0 < S <= 32:  # (an empty one has no address: none, to the library)
+            raise BsaError("block_idx must be [B,Hkv,1,S] with S from 1 to 32", 2)
     written = []
     if out is not None:
         _in_place(what, "out", out, q.shape, torch.bfloat16)
