@@ -1,6 +1,8 @@
 """CPU: a selection without a slot is no selection of every page.  (Tensors that pass for a device's, and no library
 behind them: a refusal that is missed ends in Python.)"""
 
+import types
+
 import pytest
 import torch
 
@@ -18,6 +20,7 @@ def on_device(monkeypatch):
 
     monkeypatch.setattr(bsa, "_one_device", lambda *a: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0))
     monkeypatch.setattr(bsa, "load_library", reached)
 
 
