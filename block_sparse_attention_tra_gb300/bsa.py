@@ -1125,10 +1125,10 @@ def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, inv_freq=None, posi
         written = [*(written or ()), k_out]
     (q, qs), (k, ks) = _row_strides(q), _row_strides(k)
     row = T * D
-    st = load_library().qk_norm_rope_forward(
+    st = qk_norm_rope_forward_raw(
         q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(qw), _ptr(kw), _ptr(pos), _ptr(freq),
-        _stride_array((*qs, *ks, Hq * row, row, D, Hkv * row, row, D)), B, Hq, Hkv, T, D,
-        0 if freq is None else 2 * freq.numel(), 1 if interleaved else 0, rotary_scale, eps, _dtype_code(q), kind,
+        (*qs, *ks, Hq * row, row, D, Hkv * row, row, D), B, Hq, Hkv, T, D,
+        0 if freq is None else 2 * freq.numel(), interleaved, rotary_scale, eps, _dtype_code(q), kind,
         _raw_stream(torch, dev))
     if st:
         _check(st, what)
@@ -1173,11 +1173,11 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, in
     dq, dk = _rows_like(torch, q), _rows_like(torch, k)
     dqw, dkw = (None if w is None else torch.empty(D, dtype=torch.float32, device=q.device) for w in (qw, kw))
     (q, s0), (k, s1), (dq_out, s2), (dk_out, s3) = (_row_strides(t) for t in (q, k, dq_out, dk_out))
-    st = load_library().qk_norm_rope_backward(
+    st = qk_norm_rope_backward_raw(
         q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dqw),
         _ptr(dkw), _ptr(qw), _ptr(kw), _ptr(pos), _ptr(freq),
-        _stride_array((*s0, *s1, *s2, *s3, *dq.stride()[:3], *dk.stride()[:3])), B, Hq, Hkv, T, D,
-        0 if freq is None else 2 * freq.numel(), 1 if interleaved else 0, rotary_scale, eps, _dtype_code(q), kind,
+        (*s0, *s1, *s2, *s3, *dq.stride()[:3], *dk.stride()[:3]), B, Hq, Hkv, T, D,
+        0 if freq is None else 2 * freq.numel(), interleaved, rotary_scale, eps, _dtype_code(q), kind,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(torch, dev))
     if st:
         _check(st, what)
@@ -1316,11 +1316,11 @@ def nsa_cache4_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cach
             make = torch.empty if news is None else torch.zeros
             q_out = make(q.shape, dtype=q.dtype, device=q.device)
         q, qs = _row_strides(q)
-    st = load_library().nsa_cache4_append(
+    st = nsa_cache4_append_raw(
         k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), _ptr(k_factor), _ptr(v_factor), table.data_ptr(), lens.data_ptr(), _ptr(news), _ptr(qw),
-        _ptr(kw), _ptr(freq), _stride_array((*ks, *vs, *qs)), B, Hq, Hkv, n, D, page_size, max_pages, pages,
-        0 if freq is None else 2 * freq.numel(), 1 if interleaved else 0, rotary_scale, eps, _dtype_code(k), kind,
+        _ptr(kw), _ptr(freq), (*ks, *vs, *qs), B, Hq, Hkv, n, D, page_size, max_pages, pages,
+        0 if freq is None else 2 * freq.numel(), interleaved, rotary_scale, eps, _dtype_code(k), kind,
         _raw_stream(torch, dev))
     if st:
         _check(st, what)
@@ -1371,7 +1371,7 @@ def nsa_cache4_read(k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, 
         k_out, v_out = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
     table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
     begin = None if starts is None else _int32(torch, starts)
-    st = load_library().nsa_cache4_read(
+    st = nsa_cache4_read_raw(
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_factor), _ptr(v_factor),
         table.data_ptr(), _ptr(begin), lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, Hkv, n, D, page_size,
         max_pages, pages, _dtype_code(k_out), _raw_stream(torch, dev))
@@ -1438,7 +1438,7 @@ def nsa_cache4_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_l
         out = torch.empty_like(q)
     if lse is None and return_lse:
         lse = torch.empty((B, Hq, 1), device=q.device, dtype=torch.float32)
-    st = load_library().nsa_cache4_decode(
+    st = nsa_cache4_decode_raw(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_factor),
         _ptr(v_factor), table.data_ptr(), lens.data_ptr(), _ptr(idx), out.data_ptr(), _ptr(lse), B, Hq, Hkv, D,
         page_size, max_pages, pages, S, _ptr(workspace), space, _raw_stream(torch, dev))
