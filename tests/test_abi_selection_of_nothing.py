@@ -21,6 +21,7 @@ def on_device(monkeypatch):
     monkeypatch.setattr(bsa, "_one_device", lambda *a: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(bsa, "_raw_stream", lambda *a: 0)
     monkeypatch.setattr(bsa, "load_library", reached)
 
 
