@@ -377,6 +377,21 @@ def _in_place(what, name, t, shape, *dtypes):
         raise BsaError(f"{what}: {name} must be contiguous", 2)
 
 
+def _apart(what, name, result, own, *others):
+    """Refuses a contiguous result whose memory meets another tensor's (None: absent), from that one's first element to
+    its last; over ``own`` only where the two are the same elements (None: nowhere)."""
+    begin = result.data_ptr()
+    end = begin + result.numel() * result.element_size()
+    if own is not None and not (own.data_ptr() == begin and own.is_contiguous()):
+        others = (own, *others)
+    for t in others:
+        if t is not None:
+            first = t.data_ptr()
+            last = first + t.element_size() * sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+            if first < end and begin < last + t.element_size():
+                raise BsaError(f"{what}: {name} overlaps another tensor of the call")
+
+
 def _no_gradient(what, *tensors):
     """Refuses tensors that a gradient is asked of (called where autograd records): nothing would flow through the
     cache's codes, and what is written in place would change under a graph that holds it."""
@@ -1095,7 +1110,9 @@ def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, inv_freq=None, posi
     rotation; ``rope_frequencies`` makes them) with pairs halves apart or
     neighbours if ``interleaved``, ``positions [B, T]`` or ``[T]`` (None: 0 ..
     T - 1); the rotated elements are multiplied by ``rotary_scale``.  Arithmetic
-    is fp32, rounded once.  Where autograd records, tensors that require a
+    is fp32, rounded once.  ``q_out``/``k_out`` (None: new ones) may be q and k
+    themselves where these are contiguous; memory that meets another tensor's
+    is refused.  Where autograd records, tensors that require a
     gradient are refused: ``qk_norm_rope`` has one.  Runs on ``stream`` (default:
     torch's current stream) without synchronising.
     """
@@ -1124,6 +1141,9 @@ def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, inv_freq=None, posi
         _in_place(what, "k_out", k_out, k.shape, k.dtype)
         written = [*(written or ()), k_out]
     (q, qs), (k, ks) = _row_strides(q), _row_strides(k)
+    if written:
+        _apart(what, "q_out", q_out, q, k, k_out, qw, kw, pos, freq)
+        _apart(what, "k_out", k_out, k, q, qw, kw, pos, freq)
     row = T * D
     st = qk_norm_rope_forward_raw(
         q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(qw), _ptr(kw), _ptr(pos), _ptr(freq),
@@ -1335,8 +1355,9 @@ def nsa_cache4_read(k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, 
     ``dtype`` (bf16 or fp32; default bf16, or that of ``k_out``).
 
     The cache, its factors and ``cache_lens`` as ``nsa_cache4_append`` left
-    them, the new tokens counted.  Rows past a sequence's length are zero.  Runs on ``stream`` (default: torch's
-    current stream) without synchronising.
+    them, the new tokens counted.  Rows past a sequence's length are zero.
+    ``k_out`` and ``v_out``, given together, overlap nothing else.  Runs on
+    ``stream`` (default: torch's current stream) without synchronising.
     """
     import torch
 
@@ -1371,6 +1392,10 @@ def nsa_cache4_read(k_cache, v_cache, k_scale, v_scale, page_table, cache_lens, 
         k_out, v_out = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
     table, lens = _int32(torch, page_table), _int32(torch, cache_lens)
     begin = None if starts is None else _int32(torch, starts)
+    if written:
+        cache = k_cache, v_cache, k_scale, v_scale, k_factor, v_factor, table, lens, begin
+        _apart(what, "k_out", k_out, None, v_out, *cache)
+        _apart(what, "v_out", v_out, None, *cache)
     st = nsa_cache4_read_raw(
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_factor), _ptr(v_factor),
         table.data_ptr(), _ptr(begin), lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, Hkv, n, D, page_size,

@@ -674,8 +674,9 @@ BSA_API int nsa_select_decode(const void* q, const void* k_cache,
  *   D          : a multiple of 16 from 16 to 128.
  *   rotary_dim : a multiple of 16 from 0 to D.
  *   eps        : > 0 and finite.    rotary_scale : finite.
- *   q_out and k_out overlap no input and not each other.  q, k, q_out, k_out,
- *   inv_freq and the weights start on a 16-byte boundary.  Rows with a NaN, an
+ *   q_out may be q, and k_out k, where the two are laid out alike; else they
+ *   overlap no input, and never each other.  q, k, q_out, k_out, inv_freq and
+ *   the weights start on a 16-byte boundary.  Rows with a NaN, an
  *   infinity or elements of 2^60 and more (their squares leave fp32) have
  *   unspecified results; other rows are not touched by them.
  *
