@@ -747,10 +747,11 @@ BSA_API int qk_norm_rope_backward(const void* q, const void* k,
  * beside them) normalised and rotated as in qk_norm_rope_forward.  The scale of
  * a group x is the e4m3 value nearest to max |x / factor| / 6 (ties to even, at
  * most 448), and the codes are the ones nearest to x / factor / scale, ties to
- * even, at most 6 (a scale of 0 has codes of 0).  A group that holds a NaN or an
- * infinity gets a NaN for its scale, and its codes are unspecified.  Nothing is
- * kept of the tokens held before, and no value of theirs changes; slots that get
- * no token are left as they were.
+ * even, at most 6, each with its element's sign: zeros keep theirs (codes 0 and
+ * 8), and so do the zeros that stand for any element under a scale of 0.  A
+ * group that holds a NaN or an infinity gets a NaN for its scale, and its codes
+ * are unspecified.  Nothing is kept of the tokens held before, and no value of
+ * theirs changes; slots that get no token are left as they were.
  *
  *   k, v, q, q_out, page_table, cache_lens, new_lens : as for
  *                nsa_cache_append (q and q_out may be NULL; q_out is contiguous
