@@ -236,6 +236,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) qk_rope_backward_kernel(const 
 }
 
 // Adds up the blocks' rows: one block for 16 columns of one tensor's weights, four columns a thread.
+// (Roundings that a row's product goes through in all: up to 16 rows of a thread, 5 shuffles and 8 warps above, the 256th
+// part of the blocks, 3 shuffles and 32 warps here.)
 constexpr int SUM_THREADS = 1024;
 __global__ void __launch_bounds__(SUM_THREADS) qk_rope_weights_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float4 part[SUM_THREADS / 32][4];
