@@ -983,7 +983,9 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     * ``"linear"``: every frequency over ``factor``;
     * ``"base"``: the base times ``factor ** (r / (r - 2))``, which leaves the fastest pair and divides the slowest;
     * ``"bands"``: pairs that make more than ``fast`` turns over ``original_length`` as they are, those under ``slow``
-      turns over ``factor``, those between in proportion, and ``rotary_scale = 0.1 ln(factor) + 1``.
+      turns over ``factor``, those between in proportion to their turns, and ``rotary_scale = 0.1 ln(factor) + 1``.
+      Checkpoints differ in both: some take the pairs between in proportion to their index j, whose frequencies a
+      caller makes for itself, and some use no factor on attention: leave ``rotary_scale`` at 1 for those.
 
     ``inv_freq`` is float32, ``rotary_scale`` a number (1 but for ``"bands"``).
     """

@@ -36,8 +36,9 @@
 // cover are joined by a second launch.
 //
 // Long lists of 16 query rows run at 67% of what the measured copy rate takes for their bytes (32 sequences of 131072
-// tokens of 32 query and 2 kv heads of 128: 1209 MB in 265 us, 4.6 TB/s), of eight at 77% (16 of 20000 to 60000, 4 kv
-// heads: 70 us).  The copies by themselves, nothing worked out, take the copy rate's time to within 1%, the work by itself
+// tokens of 32 query and 2 kv heads of 128: 1209 MB in 265 us, 4.6 TB/s), of eight at 78% (16 of 20000 to 60000, 4 kv
+// heads: 70 us), at 58% with heads of 64 and at 38% with heads of 32 (46.6 and 35.7 us): a chunk then has a half or a
+// quarter of the bytes under the same softmax and page steps.  The copies by themselves, nothing worked out, take the copy rate's time to within 1%, the work by itself
 // 93% of the whole: a chunk of 32 tokens is some 700 instructions of a warp, 128 conversions and 128 products with scales
 // of two cycles and 64 matrix products (eight rows: 32) of eight among them, and three or four warps a scheduler do not
 // fill the gaps of their chains.  (Packed pairs of fp32 for the softmax, 24 instructions fewer, changed nothing.)  The
